@@ -15,8 +15,14 @@ Entry points (same names as the C ABI):
   conv1d               short causal conv, varlen          -> gdn_conv1d
   conv1d_update        short causal conv, one token/row   -> gdn_conv1d_update
   validate_slots       opt-in device check of slots       -> gdn_validate_slots
-and the two call shapes of the pages:
+the softmax attention of the model's other layers (attention.py):
+  kv_cache, kv_store   paged 8-bit key/value cache         -> gdn_kv_store
+  attn_extend          packed varlen, cached prefix        -> gdn_attn_extend
+  attn_decode          one token per sequence, cache       -> gdn_attn_decode
+  kv_evict             by accumulated weight, in place     -> gdn_kv_evict
+and the call shapes of the pages:
   forward_gdn(layer, forward_batch, mixed_qkv, a, b)  (pymllm HybridAttnBackend.forward_gdn)
+  forward_attn(layer, forward_batch, q, k, v)         (pymllm RadixAttention.forward)
   ssd_combined_fwd(x, dt, A, B, C, ...)               (flashinfer.mamba.ssd_combined_fwd subset)
 """
 from __future__ import annotations
@@ -31,7 +37,9 @@ from ._lib import GDN_BF16, GDN_F32, GDN_MODE_GDN, GDN_MODE_SSD, GDNError
 
 __all__ = ["load", "gate", "ssd_gate", "extend", "extend_noalloc", "extend_kernel",
            "extend_workspace_size", "decode", "conv1d", "conv1d_update", "validate_slots", "forward_gdn",
-           "ssd_combined_fwd", "GDNError", "split_mixed_qkv", "probe_copy", "probe_mfma"]
+           "ssd_combined_fwd", "GDNError", "split_mixed_qkv", "probe_copy", "probe_mfma",
+           "KVCache", "kv_cache", "kv_store", "attn_extend", "attn_decode", "attn_decode_workspace_size",
+           "kv_evict", "kv_evict_workspace_size", "forward_attn"]
 
 
 def load():
@@ -699,3 +707,7 @@ def ssd_combined_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=F
                ckpt_token=checkpoint_token_indices, ckpt_slot=checkpoint_state_slots,
                ckpt_states=checkpoint_states, ckpt_relative=relative)
     return o.view(batch, L, H, P), (pool if return_final_states else None)
+
+
+from .attention import (KVCache, attn_decode, attn_decode_workspace_size, attn_extend, forward_attn,  # noqa: E402
+                        kv_cache, kv_evict, kv_evict_workspace_size, kv_store)

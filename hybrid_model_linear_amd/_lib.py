@@ -10,12 +10,14 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_DTYPE, GDN_E_UNSUPPORTED, GDN_E_INDEX, GDN_E_HIP, GDN_E_SCRATCH = range(8)
 GDN_F32, GDN_BF16 = 0, 1
 GDN_MODE_GDN, GDN_MODE_SSD = 0, 1
-ABI_VERSION = 8
+ABI_VERSION = 9
 
 EXPORTED = ["gdn_gate", "gdn_extend", "gdn_decode", "gdn_extend_gated", "gdn_decode_gated",
             "gdn_conv1d", "gdn_conv1d_update", "gdn_validate_slots", "gdn_status_str",
             "gdn_last_hip_error", "gdn_abi_version", "gdn_extend_workspace_size", "gdn_extend_kernel",
-            "gdn_extend_noalloc", "gdn_probe_copy", "gdn_probe_mfma"]
+            "gdn_extend_noalloc", "gdn_probe_copy", "gdn_probe_mfma",
+            "gdn_kv_store", "gdn_attn_extend", "gdn_attn_decode", "gdn_attn_decode_workspace_size",
+            "gdn_kv_evict", "gdn_kv_evict_workspace_size"]
 
 # gdn_extend_kernel results and reason bits (include/gdn.h)
 GDN_KERNEL_RECURRENT, GDN_KERNEL_CHUNKED, GDN_KERNEL_SSD_CHUNKED = 1, 2, 3
@@ -73,6 +75,48 @@ class ConvArgs(C.Structure):
                 ("parent", C.c_void_p)]
 
 
+class KVCacheArgs(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("pos", C.c_void_p), ("weight", C.c_void_p), ("num_pages", C.c_int64),
+                ("page", C.c_int32), ("H_kv", C.c_int32), ("d", C.c_int32), ("_pad0", C.c_int32)]
+
+
+class KVStoreArgs(C.Structure):
+    _fields_ = [("cache", KVCacheArgs), ("in_dtype", C.c_int32), ("N", C.c_int32), ("T", C.c_int64),
+                ("k", C.c_void_p), ("k_stride", C.c_int64), ("v", C.c_void_p), ("v_stride", C.c_int64),
+                ("cu_seqlens", C.c_void_p), ("cache_len", C.c_void_p), ("start", C.c_void_p),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32),
+                ("_pad0", C.c_int32)]
+
+
+class AttnExtendArgs(C.Structure):
+    _fields_ = [("cache", KVCacheArgs), ("in_dtype", C.c_int32), ("out_dtype", C.c_int32), ("N", C.c_int32),
+                ("H", C.c_int32), ("H_kv", C.c_int32), ("d", C.c_int32), ("T", C.c_int64),
+                ("q", C.c_void_p), ("q_stride", C.c_int64), ("k", C.c_void_p), ("k_stride", C.c_int64),
+                ("v", C.c_void_p), ("v_stride", C.c_int64), ("out", C.c_void_p), ("out_stride", C.c_int64),
+                ("cu_seqlens", C.c_void_p), ("cache_len", C.c_void_p), ("start", C.c_void_p),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32),
+                ("causal", C.c_int32), ("visible", C.c_void_p), ("doc", C.c_void_p), ("slopes", C.c_void_p),
+                ("window", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float), ("_pad0", C.c_int32)]
+
+
+class AttnDecodeArgs(C.Structure):
+    _fields_ = [("cache", KVCacheArgs), ("in_dtype", C.c_int32), ("out_dtype", C.c_int32), ("N", C.c_int32),
+                ("H", C.c_int32), ("q", C.c_void_p), ("q_stride", C.c_int64), ("out", C.c_void_p),
+                ("out_stride", C.c_int64), ("kv_len", C.c_void_p), ("q_pos", C.c_void_p),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32),
+                ("max_kvlen", C.c_int32), ("slopes", C.c_void_p), ("window", C.c_int32), ("scale", C.c_float),
+                ("softcap", C.c_float), ("accumulate", C.c_int32), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_int64)]
+
+
+class KVEvictArgs(C.Structure):
+    _fields_ = [("cache", KVCacheArgs), ("N", C.c_int32), ("budget", C.c_int32), ("recent", C.c_int32),
+                ("table_width", C.c_int32), ("kv_len", C.c_void_p), ("new_len", C.c_void_p),
+                ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_int64)]
+
+
 _lib = None
 
 
@@ -108,6 +152,13 @@ def load(path: str | None = None) -> C.CDLL:
     lib.gdn_probe_copy.restype = C.c_int
     lib.gdn_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p]
     lib.gdn_probe_mfma.restype = C.c_int
+    for fn, args in (("gdn_kv_store", KVStoreArgs), ("gdn_attn_extend", AttnExtendArgs),
+                     ("gdn_attn_decode", AttnDecodeArgs), ("gdn_kv_evict", KVEvictArgs)):
+        getattr(lib, fn).argtypes = [C.POINTER(args), C.c_void_p]
+        getattr(lib, fn).restype = C.c_int
+    for fn, args in (("gdn_attn_decode_workspace_size", AttnDecodeArgs), ("gdn_kv_evict_workspace_size", KVEvictArgs)):
+        getattr(lib, fn).argtypes = [C.POINTER(args)]
+        getattr(lib, fn).restype = C.c_int64
     lib.gdn_status_str.argtypes = [C.c_int]
     lib.gdn_status_str.restype = C.c_char_p
     lib.gdn_last_hip_error.argtypes = []

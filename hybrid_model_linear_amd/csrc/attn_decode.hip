@@ -1,0 +1,421 @@
+// Attention of one token per sequence over the paged 8-bit cache (gdn_attn_decode).
+//
+//   o_h = sum_r p_r v_r / sum_r p_r,  p_r = exp2(s_r - m),  s_r = log2(e) cap(scale q_h.k_r) + ...
+//
+// Bound by HBM: 2 d bytes of codes per row and kv head against 4 d H / H_kv flop.  The
+// H / H_kv query heads of a kv head share the rows, so they are the 16 columns of one
+// 16x16x32 MFMA tile and every code is read once.  A wave takes 64 rows at a time with no
+// LDS in the loop:
+//   - S^T = K Q^T.  Row 4 g + r of tile t (t = 0..3) is row 16 g + 4 t + r of the 64, so that
+//     lane (query j, group g) ends up with the scores of the 16 consecutive rows 16 g ..
+//     16 g + 15: one page (pages hold 16 rows at least), and in the order in which the B
+//     operand of P wants them.  The d axis of K is taken in 16-byte pieces straight from
+//     memory (Q is read in the same order).
+//   - O^T = V^T P^T.  Lane (j, g) loads d / 16 bytes of each of its group's 16 rows and
+//     transposes 4 x 4 bytes at a time with byte permutes: it then holds 16 rows of each of
+//     its d / 16 columns, the A operand's order.
+// Codes become bf16 times their page's power-of-two scale, which is exact; the products
+// are summed in fp32.  The weights p are rounded to bf16 for the second product (2^-9 of
+// each weight at most, as the output's own rounding); their sum and the accumulated
+// weights use the unrounded ones.
+// The rows of a sequence are split over workgroups (and the waves of one); the partial
+// (m, l, o) are joined in fp32 by a second launch, which also adds the weights: they
+// need the final m and l, so the first launch leaves the scores.
+#include "attn_common.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kDecThreads = 256;
+constexpr int kDecWaves = kDecThreads / kWave;
+constexpr int kRows = 64;                       // rows of a wave's tile
+
+// The 64-row tiles [t0, t1) that hold rows a sequence's query can see, and how many each
+// split takes.
+struct DecRange {
+  int lo, hi;                                   // rows [lo, hi)
+  int t0, t1, per;
+};
+__device__ __forceinline__ DecRange dec_range(const AttnDecodeLaunch& p, int n, int& qpos) {
+  DecRange r;
+  const int64_t cap = (int64_t)p.c.table_width << p.c.page_log2;
+  const int len = p.kv_len[n];
+  qpos = p.q_pos ? p.q_pos[n] : len - 1;
+  r.lo = 0;
+  r.hi = (int)min((int64_t)len, cap);           // (a padding row: negative)
+  if (p.window > 0 && !p.c.pos) {               // a row's position is its index
+    r.lo = max(0, (int)max((int64_t)qpos - p.window + 1, (int64_t)-1));
+    r.hi = (int)min((int64_t)r.hi, (int64_t)qpos + p.window);
+  }
+  r.t0 = r.lo / kRows;
+  r.t1 = r.hi > r.lo ? (r.hi + kRows - 1) / kRows : r.t0;
+  // at least one tile per wave, else the split is not worth its workgroup
+  r.per = max((r.t1 - r.t0 + p.splits - 1) / p.splits, kDecWaves);
+  return r;
+}
+
+__device__ __forceinline__ float max_over_groups(float v) {     // lanes j, j + 16, j + 32, j + 48
+  v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
+}
+
+template <int W> struct VWord;                  // d / 16 bytes of a row
+template <> struct VWord<1> { typedef uint32_t type; };
+template <> struct VWord<2> { typedef u32x2 type; };
+template <> struct VWord<4> { typedef u32x4 type; };
+template <int W, typename T> __device__ __forceinline__ uint32_t word_of(const T& v, int i) {
+  if constexpr (W == 1) return v; else return v[i];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLaunch p) {
+  constexpr int kT = D / 16;                    // 16-column tiles of O^T
+  constexpr int kP = D / 64;                    // 16-byte pieces of a K row per lane
+  constexpr int kW = D / 64;                    // 32-bit words of a V row per lane
+  typedef typename VWord<kW>::type vword;
+  __shared__ float sO[2][D][17];
+  __shared__ float sML[2][2][16];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, g16 = lane >> 4;
+  const int G = p.H / p.c.H_kv, groups = (G + 15) / 16;
+  unsigned b = blockIdx.x;
+  const int split = b % p.splits;
+  b /= p.splits;
+  const int gt = b % groups;
+  b /= groups;
+  const int h = b % p.c.H_kv, n = b / p.c.H_kv;
+  int qpos;
+  const DecRange rg = dec_range(p, n, qpos);
+  if (p.kv_len[n] < 0) return;                  // a padding row
+  const int tb = rg.t0 + split * rg.per, te = min(tb + rg.per, rg.t1);
+  if (tb >= te && split > 0) return;            // (the join counts the splits that hold tiles)
+  const int hq = h * G + gt * 16 + j16;         // this lane's query head
+  const bool live = gt * 16 + j16 < G;
+  const int lg = p.c.page_log2, pmask = (1 << lg) - 1;
+
+  bf16x8 q[2 * kP];
+#pragma unroll
+  for (int s = 0; s < 2 * kP; ++s) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (live) w = *reinterpret_cast<const uint4*>(p.q + n * p.q_stride + (int64_t)hq * D + 64 * (s >> 1) + 16 * g16 + 8 * (s & 1));
+    q[s] = as_bf16x8(w);
+  }
+  const float c1 = p.softcap > 0.f ? p.scale / p.softcap * 2.0f * kLog2e : p.scale * kLog2e;
+  const float c2 = p.softcap * kLog2e;
+  const float slope = p.slopes && live ? p.slopes[hq] * kLog2e : 0.f;
+  const bool by_pos = p.c.pos && (p.slopes || p.window > 0);
+
+  float m = -INFINITY, l = 0.f;
+  f32x4 o[kT];
+#pragma unroll
+  for (int t = 0; t < kT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // page of the rows 16 g .. of tile t for this lane as a V (and score) lane, clamped into
+  // the sequence so that every address is a held row's
+  auto page_at = [&](int t, int g) __attribute__((always_inline)) {
+    return page_of(p.c, n, min(t * kRows + 16 * g, rg.hi - 1));
+  };
+  u32x4 kc[4][kP];
+  vword vc[16];
+  int kid = -1, vid = -1;                       // pages of the loaded K rows and V rows
+  auto load_k = [&](int t) __attribute__((always_inline)) {
+    kid = page_at(t, j16 >> 2);
+    const uint8_t* base = p.c.k + page_rows(p.c, max(kid, 0), h) * D;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int r = (t * kRows + 16 * (j16 >> 2) + 4 * s + (j16 & 3)) & pmask;
+#pragma unroll
+      for (int c = 0; c < kP; ++c)
+        kc[s][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (int64_t)r * D + 64 * c + 16 * g16));
+    }
+  };
+  auto load_v = [&](int t) __attribute__((always_inline)) {
+    vid = page_at(t, g16);
+    const uint8_t* base = p.c.v + page_rows(p.c, max(vid, 0), h) * D + (D / 16) * j16;
+    const int r0 = (t * kRows + 16 * g16) & pmask;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      vc[e] = __builtin_nontemporal_load(reinterpret_cast<const vword*>(base + (int64_t)(r0 + e) * D));
+  };
+
+  int t = tb + wave;
+  if (t < te) {
+    load_k(t);
+    load_v(t);
+  }
+#pragma unroll 1
+  for (; t < te; t += kDecWaves) {
+    // S^T = K Q^T, the K codes times their page's scale
+    const float ks = kid < 0 ? 1.f : p.c.k_scale[(int64_t)kid * p.c.H_kv + h];
+    const float vs = vid < 0 ? 1.f : p.c.v_scale[(int64_t)vid * p.c.H_kv + h];
+    const int64_t vrow = page_rows(p.c, max(vid, 0), h) + ((t * kRows + 16 * g16) & pmask);
+    const bool bad = vid < 0;
+    f32x4 s[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kP; ++c) {
+        s[x] = mfma1632(f8x8_to_op(kc[x][c][0], kc[x][c][1], ks), q[2 * c], s[x]);
+        s[x] = mfma1632(f8x8_to_op(kc[x][c][2], kc[x][c][3], ks), q[2 * c + 1], s[x]);
+      }
+    }
+    const bool more = t + kDecWaves < te;
+    if (more) load_k(t + kDecWaves);            // in flight over the softmax and the second product
+    const int r0 = t * kRows + 16 * g16;        // first of this lane's 16 rows
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[x][e] = p.softcap > 0.f ? capped(s[x][e], c1, c2) : s[x][e] * c1;
+    const bool partial = t * kRows < rg.lo || t * kRows + kRows > rg.hi || __any(bad);
+    unsigned hidden = 0;                        // bit 4 x + e: that row is not seen
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) hidden |= (bad || r0 + i < rg.lo || r0 + i >= rg.hi ? 1u : 0u) << i;
+    }
+    if (by_pos) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int4 kp = *reinterpret_cast<const int4*>(p.c.pos + vrow + 4 * x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int dist = abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w));
+          s[x][e] -= slope * (float)dist;
+          if (p.window > 0 && dist >= p.window) hidden |= 1u << (4 * x + e);
+        }
+      }
+    } else if (p.slopes) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] -= slope * (float)abs(qpos - (r0 + i));
+    }
+    if (__any(hidden != 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool off = hidden >> i & 1;
+        s[i >> 2][i & 3] = off ? -INFINITY : s[i >> 2][i & 3];
+        if (off) {                              // what the row holds must not meet a weight of 0
+          if constexpr (kW == 1) vc[i] = 0; else vc[i] = vword{};
+        }
+      }
+    }
+    if (p.accumulate && live) {
+      float* at = p.scores + ((int64_t)n * p.H + hq) * p.score_cap + r0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) *reinterpret_cast<f32x4*>(at + 4 * x) = s[x];
+    }
+    float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+#pragma unroll
+    for (int x = 1; x < 4; ++x) mx = fmaxf(mx, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
+    mx = fmaxf(m, max_over_groups(mx));
+    if (__any(mx > m)) {
+      const float f = __builtin_amdgcn_exp2f(m == mx ? 0.f : m - mx);
+      m = mx;
+      l *= f;
+#pragma unroll
+      for (int x = 0; x < kT; ++x) o[x] *= f;
+    }
+    const float base = m == -INFINITY ? 0.f : m;   // a column that has seen nothing yet
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[x][e] = __builtin_amdgcn_exp2f(s[x][e] - base);
+        l += s[x][e];
+      }
+    const bf16x8 p0 = pair_to_op(s[0], s[1]), p1 = pair_to_op(s[2], s[3]);
+    // O^T += V^T P^T
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      uint32_t tr[4][4];                        // [rows 4 i ..][column]: four rows of one column
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = word_of<kW>(vc[4 * i], w), a1 = word_of<kW>(vc[4 * i + 1], w);
+        const uint32_t a2 = word_of<kW>(vc[4 * i + 2], w), a3 = word_of<kW>(vc[4 * i + 3], w);
+        const uint32_t lo01 = __builtin_amdgcn_perm(a1, a0, 0x05010400), hi01 = __builtin_amdgcn_perm(a1, a0, 0x07030602);
+        const uint32_t lo23 = __builtin_amdgcn_perm(a3, a2, 0x05010400), hi23 = __builtin_amdgcn_perm(a3, a2, 0x07030602);
+        tr[i][0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100);
+        tr[i][1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302);
+        tr[i][2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100);
+        tr[i][3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        o[4 * w + c] = mfma1632(f8x8_to_op(tr[0][c], tr[1][c], vs), p0, o[4 * w + c]);
+        o[4 * w + c] = mfma1632(f8x8_to_op(tr[2][c], tr[3][c], vs), p1, o[4 * w + c]);
+      }
+    }
+    if (more) load_v(t + kDecWaves);
+  }
+
+  // Join the waves: waves 2, 3 hand theirs to waves 0, 1, then wave 1 to wave 0.
+  l = sum_over_groups(l);
+#pragma unroll
+  for (int step = 2; step; step >>= 1) {
+    if (wave >= step && wave < 2 * step) {
+      const int w = wave - step;
+      if (g16 == 0) {
+        sML[w][0][j16] = m;
+        sML[w][1][j16] = l;
+      }
+#pragma unroll
+      for (int x = 0; x < kT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sO[w][kT * (4 * g16 + e) + x][j16] = o[x][e];
+    }
+    __syncthreads();
+    if (wave < step) {
+      const float m2 = sML[wave][0][j16], l2 = sML[wave][1][j16], mn = fmaxf(m, m2);
+      const float f1 = mn == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      const float f2 = mn == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m2 - mn);
+      m = mn;
+      l = l * f1 + l2 * f2;
+#pragma unroll
+      for (int x = 0; x < kT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = o[x][e] * f1 + sO[wave][kT * (4 * g16 + e) + x][j16] * f2;
+    }
+    __syncthreads();
+  }
+  if (wave != 0 || !live) return;
+  const bool alone = rg.t1 - rg.t0 <= rg.per;   // no other split holds tiles
+  if (alone) {
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // (a NaN sum stays NaN)
+    u16* at = p.out + n * p.out_stride + (int64_t)hq * D;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)                 // columns kT (4 g + e) .. + kT - 1
+#pragma unroll
+      for (int x = 0; x < kT; x += 4)
+        *reinterpret_cast<uint2*>(at + kT * (4 * g16 + e) + x) =
+            make_uint2(cvt2(o[x][e] * inv, o[x + 1][e] * inv), cvt2(o[x + 2][e] * inv, o[x + 3][e] * inv));
+  } else {
+    float* at = p.part_o + (((int64_t)n * p.H + hq) * p.splits + split) * D;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int x = 0; x < kT; x += 4)
+        *reinterpret_cast<f32x4*>(at + kT * (4 * g16 + e) + x) = f32x4{o[x][e], o[x + 1][e], o[x + 2][e], o[x + 3][e]};
+  }
+  if ((!alone || p.accumulate) && g16 == 0) {
+    float* at = p.part_ml + (((int64_t)n * p.H + hq) * p.splits + split) * 2;
+    at[0] = m;
+    at[1] = l;
+  }
+}
+
+// Join: blockIdx.x = 0 .. H - 1: the partial outputs of one query head; the blocks behind
+// (accumulate): 1024 rows of one kv head, four per thread.
+constexpr int kAccRows = 4 * kDecThreads;
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDecodeLaunch p) {
+  __shared__ float sM[64], sInv[64];
+  __shared__ float sPart[kDecThreads];
+  const int tid = threadIdx.x, n = blockIdx.y;
+  int qpos;
+  const DecRange rg = dec_range(p, n, qpos);
+  if (p.kv_len[n] < 0) return;
+  const int tiles = rg.t1 - rg.t0, used = (tiles + rg.per - 1) / rg.per;   // splits that hold tiles
+  if ((int)blockIdx.x < p.H) {
+    if (used <= 1) return;                      // written by the first launch
+    const int64_t row = ((int64_t)n * p.H + blockIdx.x) * p.splits;
+    const float* ml = p.part_ml + row * 2;
+    float m = -INFINITY;
+    for (int s = 0; s < used; ++s) m = fmaxf(m, ml[2 * s]);
+    constexpr int kC = D / 4;                   // four columns per thread, kDecThreads / kC splits at a time
+    const int c = tid % kC, part = tid / kC;
+    float l = 0.f;
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    for (int s = part; s < used; s += kDecThreads / kC) {
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * s] - m);
+      l += ml[2 * s + 1] * f;
+      o += *reinterpret_cast<const f32x4*>(p.part_o + (row + s) * D + 4 * c) * f;
+    }
+    __shared__ f32x4 sAcc[kDecThreads];
+    sAcc[tid] = o;
+    sPart[tid] = l;
+    __syncthreads();
+    if (part == 0) {
+      for (int i = 1; i < kDecThreads / kC; ++i) {
+        o += sAcc[tid + i * kC];
+        l += sPart[tid + i * kC];
+      }
+      const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+      *reinterpret_cast<uint2*>(p.out + n * p.out_stride + (int64_t)blockIdx.x * D + 4 * c) =
+          make_uint2(cvt2(o[0] * inv, o[1] * inv), cvt2(o[2] * inv, o[3] * inv));
+    }
+    return;
+  }
+  // accumulated weights
+  const int G = p.H / p.c.H_kv;
+  const int blk = blockIdx.x - p.H, h = blk % p.c.H_kv;
+  const int64_t first = (int64_t)(blk / p.c.H_kv) * kAccRows + (int64_t)rg.t0 * kRows;
+  if (first >= rg.hi || used == 0) return;
+  const int r = (int)first + 4 * tid;
+  f32x4 w{0.f, 0.f, 0.f, 0.f};
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    const int gn = min(64, G - g0);
+    __syncthreads();
+    if (tid < gn) {
+      const float* ml = p.part_ml + ((int64_t)n * p.H + h * G + g0 + tid) * p.splits * 2;
+      float m = -INFINITY, l = 0.f;
+      for (int s = 0; s < used; ++s) m = fmaxf(m, ml[2 * s]);
+      if (m > -INFINITY)
+        for (int s = 0; s < used; ++s) l += ml[2 * s + 1] * __builtin_amdgcn_exp2f(ml[2 * s] - m);
+      sM[tid] = m > -INFINITY ? m : 0.f;
+      sInv[tid] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+    }
+    __syncthreads();
+    if (r < rg.hi)
+      for (int g = 0; g < gn; ++g) {
+        const f32x4 s = *reinterpret_cast<const f32x4*>(p.scores + ((int64_t)n * p.H + h * G + g0 + g) * p.score_cap + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(s[e] - sM[g]) * sInv[g];
+      }
+  }
+  if (r >= rg.hi) return;
+  const int id = page_of(p.c, n, r);
+  if (id < 0) return;
+  float* at = p.c.weight + page_rows(p.c, id, h) + (r & ((1 << p.c.page_log2) - 1));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (r + e >= rg.lo && r + e < rg.hi) at[e] += w[e];
+}
+
+template <int D>
+hipError_t launch_d(const AttnDecodeLaunch& p, int64_t max_rows, hipStream_t s) {
+  const int G = p.H / p.c.H_kv;
+  const int64_t blocks = (int64_t)p.splits * ((G + 15) / 16) * p.c.H_kv * p.N;
+  decode_kernel<D><<<dim3((unsigned)blocks), kDecThreads, 0, s>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (p.splits == 1 && !p.accumulate)) return e;
+  // (a range of max_rows rows can begin inside a tile)
+  const int64_t acc = p.accumulate ? (max_rows + kRows + kAccRows - 1) / kAccRows * p.c.H_kv : 0;
+  decode_join_kernel<D><<<dim3((unsigned)(p.H + acc), (unsigned)p.N), kDecThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Splits per (sequence, kv head, 16 query heads): enough workgroups for four on each CU,
+// none with less than two tiles per wave.
+int attn_decode_splits(int64_t N, int H, int H_kv, int64_t max_rows, int cus) {
+  const int64_t base = N * H_kv * ((H / H_kv + 15) / 16);
+  const int64_t want = (4 * (int64_t)cus + base - 1) / base;
+  const int64_t most = (max_rows + 2 * kDecWaves * kRows - 1) / (2 * kDecWaves * kRows);
+  int64_t s = want < most ? want : most;
+  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+}
+
+hipError_t launch_attn_decode(const AttnDecodeLaunch& p, hipStream_t s) {
+  const int64_t rows = (int64_t)p.c.table_width << p.c.page_log2;
+  switch (p.c.d) {
+    case 64: return launch_d<64>(p, rows, s);
+    case 128: return launch_d<128>(p, rows, s);
+    default: return launch_d<256>(p, rows, s);
+  }
+}
+
+}  // namespace gdn

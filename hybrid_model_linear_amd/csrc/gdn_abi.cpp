@@ -8,6 +8,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "attn_launch.h"
 #include "gdn_launch.h"
 
 namespace {
@@ -510,6 +511,11 @@ int conv_impl(const gdn_conv_args* a, bool update, void* stream) {
 }
 
 }  // namespace
+
+namespace gdn {   // for attn_abi.cpp
+int status_of_hip(hipError_t e) { return hip_status(e); }
+int current_device_cus() { return device_cus(); }
+}  // namespace gdn
 
 extern "C" {
 

@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 8
+#define GDN_ABI_VERSION 9
 
 typedef enum gdn_status {
   GDN_OK = 0,
@@ -395,6 +395,189 @@ int gdn_conv1d(const gdn_conv_args* args, void* stream);
  * (cu_seqlens, has_init ignored); slot[b] < 0 marks a padding row whose output row
  * and slot stay untouched.  One launch; out may be x itself (same rows). */
 int gdn_conv1d_update(const gdn_conv_args* args, void* stream);
+
+/* ---------------------------------------------------------------- softmax attention
+ * The full-attention half of the hybrid model: the layer that RadixAttention stands for
+ * on the radix_attention page (num_heads, num_kv_heads, head_dim, scaling, logit_cap,
+ * sliding_window_size; forward(q, k, v, forward_batch, save_kv_cache)), with its keys
+ * and values in a paged 8-bit cache.  With p_i, p_j the positions of a query and a key,
+ * query head h reading kv head h / (H / H_kv):
+ *     s_ij = scale q_i.k_j;  softcap > 0: s_ij = softcap tanh(s_ij / softcap);
+ *     slopes: s_ij -= slopes[h] |p_i - p_j|
+ *     o_i  = sum_j exp(s_ij) v_j / sum_j exp(s_ij)  over the keys j that i sees
+ * and o_i = 0 for a query that sees nothing.  bf16 inputs and outputs, d in {64, 128,
+ * 256}, fp32 scores, softmax statistics and sums; the softmax weights are rounded to
+ * bf16 for the product with the values.  A value that a query does not see does not
+ * reach it, whatever it holds (NaN and infinities too).
+ *
+ * The cache.  Pages of `page` rows; row r of a sequence is row r % page of the page
+ * block_table[n, r / page] (row stride table_stride, table_width entries per sequence).
+ * A cached value is code * scale: codes in OCP e4m3, the scale a power of two per (page,
+ * kv head), the smallest with max |x| <= 448 scale over the rows written, at least
+ * 2^-64.  Page ids are device data that the kernels bound: rows on a page outside
+ * [0, num_pages), and rows past table_width * page, are neither read nor written (as
+ * keys they are not seen). */
+typedef struct gdn_kv_cache {
+  void* k;               /* e4m3 [num_pages, H_kv, page, d], 16-byte aligned    */
+  void* v;               /* like k                                              */
+  float* k_scale;        /* fp32 [num_pages, H_kv]                              */
+  float* v_scale;
+  int32_t* pos;          /* int32 [num_pages, H_kv, page], 16-byte aligned: the rows' positions;
+                            NULL: a row's position is its index                 */
+  float* weight;         /* fp32 like pos: accumulated softmax weights; or NULL */
+  int64_t num_pages;
+  int32_t page;          /* 16, 32, 64 or 128                                   */
+  int32_t H_kv;
+  int32_t d;             /* 64, 128 or 256                                      */
+  int32_t _pad0;
+} gdn_kv_cache;
+
+/* gdn_kv_store: quantise the new tokens' keys and values into the cache.  Sequence n's
+ * tokens [cu_seqlens[n], cu_seqlens[n+1]) (cu_seqlens NULL: token n alone, T = N) become
+ * its rows cache_len[n], cache_len[n] + 1, ...; cache_len[n] < 0 skips the sequence.  A
+ * page that holds earlier rows of the sequence keeps the larger of its scale and the new
+ * rows' need; where the scale grows, the earlier codes are rounded to it.  A page that
+ * starts with the new rows takes their scale.  NaN and infinities are stored as NaN and
+ * do not count for the scale.  Rows behind the last one written are left as they are.
+ * With cache.pos the rows' positions become start[n], start[n] + 1, ... (start NULL:
+ * cache_len[n]); with cache.weight their weights become 0.  k, v: bf16 [T, H_kv, d],
+ * 16-byte aligned rows (strides multiples of 8).  Two sequences of one call must not
+ * write the same page.  One launch. */
+typedef struct gdn_kv_store_args {
+  gdn_kv_cache cache;
+  int32_t in_dtype;            /* GDN_BF16                         */
+  int32_t N;
+  int64_t T;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const int32_t* cu_seqlens;   /* [N + 1] or NULL                  */
+  const int32_t* cache_len;    /* [N] rows already held            */
+  const int32_t* start;        /* [N] or NULL                      */
+  const int32_t* block_table;  /* [N, table_width]                 */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t _pad0;
+} gdn_kv_store_args;
+int gdn_kv_store(const gdn_kv_store_args* args, void* stream);
+
+/* gdn_attn_extend: attention of packed new tokens (prefill, chunked prefill, verify) over
+ * their own keys and values and, with a cache (cache.k non-NULL), the cache_len[n] rows
+ * that sequence n already holds there (cache_len[n] < 0 skips the sequence: its output
+ * rows are left as they are).  Token i of sequence n has the position start[n] + i (start
+ * NULL: cache_len[n] + i, or i without a cache); a cached row has cache.pos, or its index.
+ * Token i sees its own sequence's token j when all of these hold:
+ *   - causal = 0, or j <= i, or j < visible[n] (prefix mask: the first visible[n] tokens
+ *     are seen by every token; NULL: none);
+ *   - window = 0, or |i - j| < window;
+ *   - doc = NULL, or doc[i] == doc[j] and doc[i] >= 0 (document mask over the packed
+ *     tokens; tokens with a negative id see nothing and are not seen).
+ * and a cached row when window = 0 or the positions are less than `window` apart.  doc
+ * cannot be combined with a cache (GDN_E_UNSUPPORTED).
+ *   q, out : bf16 [T, H, d]; k, v : bf16 [T, H_kv, d]; heads contiguous, 16-byte aligned
+ *   rows (strides multiples of 8, at most 2^22).
+ * cu_seqlens follows gdn_extend: cu_seqlens[N] <= T, rows behind the last sequence are
+ * not written.  out must not overlap an input.  The new tokens are not stored (gdn_kv_store).  One launch. */
+typedef struct gdn_attn_extend_args {
+  gdn_kv_cache cache;
+  int32_t in_dtype;            /* GDN_BF16                         */
+  int32_t out_dtype;           /* GDN_BF16                         */
+  int32_t N;
+  int32_t H, H_kv, d;
+  int64_t T;
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  void* out;
+  int64_t out_stride;
+  const int32_t* cu_seqlens;   /* [N + 1]                          */
+  const int32_t* cache_len;    /* [N]; required with a cache, NULL without */
+  const int32_t* start;        /* [N] or NULL                      */
+  const int32_t* block_table;  /* [N, table_width]                 */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t causal;
+  const int32_t* visible;      /* [N] or NULL                      */
+  const int32_t* doc;          /* [T] or NULL                      */
+  const float* slopes;         /* [H] or NULL                      */
+  int32_t window;              /* 0 = none                         */
+  float scale;
+  float softcap;               /* 0 = none                         */
+  int32_t _pad0;
+} gdn_attn_extend_args;
+int gdn_attn_extend(const gdn_attn_extend_args* args, void* stream);
+
+/* gdn_attn_decode: one token per sequence over the rows 0 .. kv_len[n] - 1 of the cache
+ * (its own row among them: gdn_kv_store first).  kv_len[n] = 0 writes zeros, kv_len[n] < 0
+ * marks a padding row: nothing of it is read or written.  The query's position is q_pos[n]
+ * (NULL: kv_len[n] - 1); with a window only rows closer than it are seen.  accumulate != 0
+ * adds to cache.weight of every row of the sequence the sum of the softmax weights that
+ * the kv head's H / H_kv query heads give it; sequences of one call must then not share
+ * pages.  max_kvlen is a host hint of the longest kv_len (0 = unknown): speed only.
+ * The rows are split over workgroups, whose partial results a second launch joins; they
+ * stand in a workspace of gdn_attn_decode_workspace_size bytes (0: none needed), 256-byte
+ * aligned, with any contents; calls in flight at once need their own. */
+typedef struct gdn_attn_decode_args {
+  gdn_kv_cache cache;
+  int32_t in_dtype;            /* GDN_BF16                         */
+  int32_t out_dtype;           /* GDN_BF16                         */
+  int32_t N;
+  int32_t H;
+  const void* q;               /* bf16 [N, H, d]                   */
+  int64_t q_stride;
+  void* out;                   /* bf16 [N, H, d]                   */
+  int64_t out_stride;
+  const int32_t* kv_len;       /* [N]                              */
+  const int32_t* q_pos;        /* [N] or NULL                      */
+  const int32_t* block_table;  /* [N, table_width]                 */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t max_kvlen;
+  const float* slopes;         /* [H] or NULL                      */
+  int32_t window;              /* 0 = none                         */
+  float scale;
+  float softcap;               /* 0 = none                         */
+  int32_t accumulate;
+  void* workspace;
+  int64_t workspace_bytes;
+} gdn_attn_decode_args;
+int gdn_attn_decode(const gdn_attn_decode_args* args, void* stream);
+/* Workspace bytes of a gdn_attn_decode call with these arguments, or minus the gdn_status
+ * it would return (the workspace fields are ignored).  Host-side, launches nothing. */
+int64_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
+
+/* gdn_kv_evict: cut every sequence to at most `budget` rows per kv head, in place.  Of a
+ * sequence of kv_len[n] > budget rows, each kv head keeps the rows with pos > (its largest
+ * pos) - recent, then those of largest weight; ties go to the lowest row, a NaN weight
+ * ranks below all others, and never more than `budget` rows are kept.  The kept rows at
+ * or past `budget` move, in order, into the dropped rows before it, in order, with their
+ * pos and weight; the others stay.  (Attention does not depend on the order of rows, only
+ * on their pos.)  The scale of a page that receives rows becomes the largest of its own
+ * and those of the rows' pages, and its rows before `budget` are rounded to it.
+ * new_len[n] = min(kv_len[n], budget) (may be kv_len itself; kv_len[n] < 0 is copied).
+ * Rows at or past new_len mean nothing afterwards.  The cache needs pos and weight.
+ * A sequence with an id out of range among its pages' first kv_len[n] rows is left as it
+ * is, with new_len[n] = kv_len[n].  Sequences must not share pages.  0 <= recent <= budget,
+ * budget >= 1 (a budget past the table's rows counts as those).  Two launches; workspace as for gdn_attn_decode. */
+typedef struct gdn_kv_evict_args {
+  gdn_kv_cache cache;
+  int32_t N;
+  int32_t budget;
+  int32_t recent;
+  int32_t table_width;
+  const int32_t* kv_len;       /* [N]                              */
+  int32_t* new_len;            /* [N]                              */
+  const int32_t* block_table;  /* [N, table_width]                 */
+  int64_t table_stride;
+  void* workspace;
+  int64_t workspace_bytes;
+} gdn_kv_evict_args;
+int gdn_kv_evict(const gdn_kv_evict_args* args, void* stream);
+int64_t gdn_kv_evict_workspace_size(const gdn_kv_evict_args* args);
 
 /* Device-side check of slot[0..n): *flag (device int32) receives 0 when every
  * non-negative slot is < num_slots and no non-negative slot repeats, 1 when one

@@ -24,6 +24,9 @@ The delta-off mode follows the parameter list of the flashinfer page
 "flashinfer.mamba.ssd_combined_fwd" (x, dt, A, B, C, D, z, dt_bias, dt_softplus,
 dt_limit, initial_states, return_final_states).
 
+oracle.attention holds the softmax-attention operators over the paged 8-bit cache,
+pinned by tests/test_oracle_attention.py.
+
 Parity pins: every function here is pinned by tests in tests/test_oracle_pins.py
 (closed forms, brute force, exact rational arithmetic, invariants).  No function
 is "parity unpinned".
@@ -31,5 +34,8 @@ is "parity unpinned".
 from .gdn import (softplus, sigmoid, gdn_gate, ssd_gate, l2_normalize, gdn_extend,
                   gdn_decode, apply_final_states, ssd_combined, causal_conv1d)
 
+from . import attention
+
 __all__ = ["softplus", "sigmoid", "gdn_gate", "ssd_gate", "l2_normalize", "gdn_extend",
-           "gdn_decode", "apply_final_states", "ssd_combined", "causal_conv1d"]
+           "gdn_decode", "apply_final_states", "ssd_combined", "causal_conv1d",
+           "attention"]
