@@ -9,15 +9,18 @@
 // sequence's (token, query head of the group) pairs, G = H / H_kv, so the heads of a group
 // share every K and V tile and short sequences still fill rows.  Each of its four waves
 // owns 32 rows:
-//   - S^T = K Q^T with 32x32x16 MFMA: a lane holds 32 of a 64-key tile's scores of one row
-//     (lane % 32), so the softmax is lane-local but for one exchange of the two halves.
+//   - S^T = K Q^T with 32x32x16 MFMA: a lane holds half of a tile's scores of one row (lane
+//     % 32), so the softmax is lane-local but for one exchange of the two halves.
 //   - O^T += V^T P^T: S^T's accumulator order is the B operand's once the 16 keys of a step
 //     are taken as 8 (2 u + (e >> 2)) + 4 half + (e & 3), and V^T comes from the row-major V
 //     tile by LDS transpose reads of 4 rows in that order.
-// K and V tiles of 64 keys stand in LDS as bf16, double-buffered, their 16-byte pieces
-// XOR-swizzled by row (operand and transpose reads without bank conflicts); the next
-// tile's rows are loaded into registers while this one is computed.  Cached rows become
-// bf16 times their page's power-of-two scale (exact) on the way into LDS.
+// K and V tiles of 64 keys stand in LDS as bf16, their 16-byte pieces XOR-swizzled by row
+// (operand and transpose reads without bank conflicts).  Up to d = 128 two workgroups fit
+// a CU and one's softmax runs under the other's products; at d = 256 one does (its output
+// alone takes 128 registers), and its products take twice as long as its softmax.  New tokens'
+// tiles are double-buffered and go from memory to LDS without passing through registers;
+// the swizzle is on the global side.  Cached rows arrive as codes the same way; the lane
+// that asked for a piece turns it into bf16 times its page's power-of-two scale (exact).
 // The weights are rounded to bf16 for the second product, their sum is not.
 #include "attn_common.h"
 
@@ -26,40 +29,65 @@ namespace {
 
 constexpr int kExtThreads = 256;
 constexpr int kBM = 128;      // rows of a workgroup
-constexpr int kBN = 64;       // keys of a tile
 constexpr int kFlags = 4096;  // document mask: key tiles whose overlap is looked up ahead
 
-// 16-byte piece c of row r of a [64][D] bf16 tile (element index).  Any 16 consecutive
-// rows of one piece, and any 4-row group of 4 pieces, cover all banks.
-template <int D>
-__device__ __forceinline__ int tidx(int r, int c) {
-  const int sw = D >= 128 ? ((r & 3) << 2 | (r >> 2 & 3)) : ((r >> 1 & 1) << 2 | (r >> 2 & 3));
-  return r * D + ((c ^ sw) << 3);
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4w;
+
+// LDS byte address (the 32-bit value of the pointer)
+template <typename T> __device__ __forceinline__ uint32_t lds_at(const T* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) T*)p;
+}
+__device__ __forceinline__ bf16x8 lds_op(uint32_t at) { return __builtin_bit_cast(bf16x8, *(lds_u32x4*)(uintptr_t)at); }
+__device__ __forceinline__ uint2 lds_tr(uint32_t at) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(uintptr_t)at));
 }
 
-struct ExtMask {                 // what decides whether row i sees key j (sequence-local tokens)
-  int vis;                       // keys below are seen by every row (INT_MAX: not causal)
-  int window;                    // 0: none
-  const int32_t* doc;            // of the sequence's tokens, or null
-};
-__device__ __forceinline__ bool ext_seen(const ExtMask& k, int i, int j, int di, int dj) {
-  bool ok = j <= i || j < k.vis;
-  if (k.window > 0) ok = ok && abs(i - j) < k.window;
-  if (k.doc) ok = ok && di == dj && di >= 0;
-  return ok;
+// Memory -> LDS, 16 bytes per lane: lane l's piece lands at `lds` + 16 l.  In inline
+// assembly because the compiler, which cannot tell the two tile buffers apart, would wait
+// for every load in flight before each LDS read; vm_wait() is the wait.
+__device__ __forceinline__ void to_lds(u32x4 rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void vm_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t uni(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+// Buffer descriptor of `bytes` bytes at p (both the same in every lane); reads past the
+// end give zeros.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return u32x4{uni((uint32_t)a), uni((uint32_t)(a >> 32)), uni(bytes), (unsigned)kBufWord3};
 }
 
-template <int D>
+// XOR of a row's 16-byte pieces in a [rows][D] bf16 tile: any 16 consecutive rows of one
+// piece, and any 4-row group of 4 pieces, cover all banks.
+template <int D> __device__ __forceinline__ int row_swz(int r) {
+  return D >= 128 ? ((r & 3) << 2 | (r >> 2 & 3)) : ((r >> 1 & 1) << 2 | (r >> 2 & 3));
+}
+
+template <int D, bool CACHED>
 __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(const AttnExtendLaunch p) {
+  constexpr int kBN = 64;                  // keys of a tile
+  constexpr int kN2 = kBN / 32;
+  constexpr int kS = 16 * kN2;             // scores per lane
   constexpr int kU = D / 16;               // k steps of S^T
   constexpr int kDT = D / 32;              // 32-column tiles of O^T
   constexpr int kPc = D / 8;               // 16-byte pieces of a bf16 row
-  constexpr int kSt = kBN * kPc / kExtThreads;   // pieces per thread of one tile (K or V)
-  __shared__ __attribute__((aligned(16))) u16 sK[2][kBN * D], sV[2][kBN * D];
+  constexpr int kTile = kBN * D * 2;       // bytes of a K or V tile
+  constexpr int kRpi = kWave / kPc;        // rows that one wave's load brings
+  constexpr int kLd = kBN / kRpi / 4;      // loads per wave and tile
+  constexpr int kKa = kU < 8 ? kU : 8, kVa = kDT < 4 ? kDT : 4;   // distinct operand addresses
+  __shared__ __attribute__((aligned(1024))) unsigned char sT[4 * kTile];   // K, V, K, V
   __shared__ unsigned sFlag[kFlags / 16];  // 2 bits per key tile: overlaps, all one document
   __shared__ int sDoc[2];
+  __shared__ __attribute__((aligned(16))) int sIds[4][64];
+  __shared__ unsigned sBad[2];             // rows of a tile that hold NaN or infinity
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, q32 = lane & 31, hh = lane >> 5;
+  const int tid = threadIdx.x, wave = (int)uni(threadIdx.x >> 6), lane = tid & 63, q32 = lane & 31, hh = lane >> 5;
   const int G = p.H / p.H_kv;
   // Heads fastest: consecutive workgroups go to the 8 XCDs in turn, so a head's tiles share
   // an L2.  Late tiles of a causal sequence see the most keys: they are launched first.
@@ -75,26 +103,24 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const int64_t tile = w - ((int64_t)t0 * G / kBM + n);
   const int64_t f0 = tile * kBM;
   if (tile < 0 || f0 >= (int64_t)L * G) return;
-  int P = p.cache_len ? p.cache_len[n] : 0;             // cached rows
+  int P = CACHED ? p.cache_len[n] : 0;                  // cached rows
   if (P < 0) return;
   const int start = p.start ? p.start[n] : P;           // position of token 0
-  const int lg = p.c.page_log2;
-  P = p.c.k ? (int)min((int64_t)P, (int64_t)p.c.table_width << lg) : 0;
+  const int lg = p.c.page_log2, pmask = (1 << lg) - 1;
+  if (CACHED) P = (int)min((int64_t)P, (int64_t)p.c.table_width << lg);
 
-  // this lane's row
+  // this lane's row, and the wave's and workgroup's tokens
   const int64_t f = f0 + wave * 32 + q32;
   const bool live = f < (int64_t)L * G;
-  const int ti = live ? (int)(f / G) : L - 1, g = live ? (int)(f % G) : 0;
+  const int ti = live ? (int)(f / G) : L - 1, g = live ? (int)(f - (int64_t)ti * G) : 0;
   const int hq = h * G + g;
-  const int ta = (int)(f0 / G), tz = (int)(min(f0 + kBM - 1, (int64_t)L * G - 1) / G);   // the workgroup's tokens
+  const int ta = (int)(f0 / G), tz = (int)(min(f0 + kBM - 1, (int64_t)L * G - 1) / G);
   const int64_t fw = f0 + wave * 32;
-  const int wa = (int)min(fw / G, (int64_t)L - 1), wz = (int)(min(fw + 31, (int64_t)L * G - 1) / G);   // the wave's
+  const int wa = (int)min(fw / G, (int64_t)L - 1), wz = (int)(min(fw + 31, (int64_t)L * G - 1) / G);
 
-  ExtMask mk;
-  mk.vis = p.causal ? (p.visible ? p.visible[n] : 0) : INT32_MAX;
-  mk.window = p.window;
-  mk.doc = p.doc ? p.doc + t0 : nullptr;
-  const int di = mk.doc ? mk.doc[ti] : 0;
+  const int vis = p.causal ? (p.visible ? p.visible[n] : 0) : INT32_MAX;   // keys below: seen by every row
+  const int32_t* doc = p.doc ? p.doc + t0 : nullptr;
+  const int di = doc ? doc[ti] : 0;
 
   bf16x8 q[kU];
 #pragma unroll
@@ -103,61 +129,29 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     if (live) x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(t0 + ti) * p.q_stride + (int64_t)hq * D + 16 * u + 8 * hh);
     q[u] = as_bf16x8(x);
   }
+  // Scores stay raw (q.k) until the exponent where nothing but a positive scale applies;
+  // otherwise they are brought to units of log2 first.
+  const bool raw = p.softcap == 0.f && !p.slopes && p.scale > 0.f;
   const float c1 = p.softcap > 0.f ? p.scale / p.softcap * 2.0f * kLog2e : p.scale * kLog2e;
   const float c2 = p.softcap * kLog2e;
+  const float cs = raw ? c1 : 1.f;
   const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
+  const float slack = 8.f / cs;            // the maximum in use may lag the true one by 2^8
 
-  // key tiles: cached ones, then the new tokens' [d0, d1)
-  const int c1t = (P + kBN - 1) / kBN;
-  int c0t = 0;
-  if (p.window > 0 && !p.c.pos && P > 0) {              // cached rows a window leaves out of every row
-    const int64_t first = (int64_t)start + ta - p.window + 1;
-    c0t = (int)min((int64_t)c1t, max((int64_t)0, first) / kBN);
-  }
-  int last = min(L, max(tz + 1, min(mk.vis, L)));       // keys [first, last) are seen by some row
-  int first = 0;
-  if (p.window > 0) {
-    first = (int)max((int64_t)0, (int64_t)ta - p.window + 1);
-    last = (int)min((int64_t)last, (int64_t)tz + p.window);
-  }
-  const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
-
-  // Document mask: which key tiles hold a document of this workgroup's rows.
-  if (mk.doc) {
-    for (int i = tid; i < kFlags / 16; i += kExtThreads) sFlag[i] = 0;
-    if (tid == 0) {
-      sDoc[0] = INT32_MAX;
-      sDoc[1] = -1;
-    }
-    __syncthreads();
-    for (int t = ta + tid; t <= tz; t += kExtThreads) {
-      const int d = mk.doc[t];
-      atomicMin(&sDoc[0], d);
-      atomicMax(&sDoc[1], d);
-    }
-    __syncthreads();
-    const int dmin = sDoc[0], dmax = sDoc[1];
-    for (int t = d0 + tid; t < min(d1, d0 + kFlags); t += kExtThreads) {
-      bool any = false, all = dmin == dmax;
-      for (int j = t * kBN; j < min(L, (t + 1) * kBN); ++j) {
-        const int d = mk.doc[j];
-        any = any || (d >= 0 && d >= dmin && d <= dmax);
-        all = all && d == dmin && d >= 0;
+  // operand addresses in the first tile pair; a tile is kTile bytes, a pair 2 kTile
+  uint32_t ka[kKa], va[2][kVa];
+  {
+    const uint32_t base = lds_at(sT);
+#pragma unroll
+    for (int u = 0; u < kKa; ++u) ka[u] = base + q32 * (2 * D) + (((2 * u + hh) ^ row_swz<D>(q32)) << 4);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int d = 0; d < kVa; ++d) {
+        const int r = 4 * hh + ((lane & 15) >> 2) + 8 * e, c = 4 * d + (lane >> 4 & 1) * 2 + ((lane & 3) >> 1);
+        va[e][d] = base + kTile + r * (2 * D) + ((c ^ row_swz<D>(r)) << 4) + 8 * (lane & 1);
       }
-      atomicOr(&sFlag[(t - d0) >> 4], (any ? 1u : 0u) << 2 * ((t - d0) & 15) | (all ? 2u : 0u) << 2 * ((t - d0) & 15));
-    }
-    __syncthreads();
   }
-  auto doc_flags = [&](int t) __attribute__((always_inline)) -> unsigned {
-    return t - d0 < kFlags ? sFlag[(t - d0) >> 4] >> 2 * ((t - d0) & 15) & 3 : 1u;
-  };
-  // Tiles in order: x in [c0t, c1t) cached, then c1t + (t - d0).  The next tile at or after x.
-  const int end = c1t + max(0, d1 - d0);
-  auto skip = [&](int x) __attribute__((always_inline)) {
-    if (mk.doc)
-      while (x < end && !(doc_flags(x - c1t + d0) & 1)) ++x;
-    return x;
-  };
 
   float m = -INFINITY, l = 0.f;
   f32x16 o[kDT];
@@ -166,235 +160,409 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[t][e] = 0.f;
 
-  u32x4 rk[kSt], rv[kSt];                  // the next tile's pieces
-  constexpr int kCp = D / 16;              // 16-code pieces of a cached row
-  constexpr int kCt = kBN * kCp / kExtThreads;   // per thread: 1 (D = 64), 2, 4
-  float rksc[kCt], rvsc[kCt];              // and their pages' scales
-  auto load = [&](int x) __attribute__((always_inline)) {
-    if (x < c1t) {
+  // The scores of the tile pair at byte offset `off` of sT.  Operand reads run a few steps
+  // ahead of the products (left alone, the compiler waits for each read before its MFMA).
+  auto scores = [&](uint32_t off, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    uint32_t at[kKa];
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) {
-        const int i = tid + s * kExtThreads, r = min(x * kBN + i / kCp, P - 1), c = i % kCp;
-        const int id = page_of(p.c, n, r);
-        const int64_t row = page_rows(p.c, max(id, 0), h) + (r & ((1 << lg) - 1));
-        rk[s] = *reinterpret_cast<const u32x4*>(p.c.k + row * D + 16 * c);
-        rv[s] = *reinterpret_cast<const u32x4*>(p.c.v + row * D + 16 * c);
-        const int64_t sc = (int64_t)max(id, 0) * p.H_kv + h;
-        rksc[s] = id < 0 ? 1.f : p.c.k_scale[sc];
-        rvsc[s] = id < 0 ? 1.f : p.c.v_scale[sc];
-        if (id < 0 || x * kBN + i / kCp >= P) {          // not held: finite, and masked below
-          rk[s] = u32x4{0, 0, 0, 0};
-          rv[s] = u32x4{0, 0, 0, 0};
-        }
-      }
-    } else {
-      const int j0 = (x - c1t + d0) * kBN, rows = min(kBN, L - j0);
-      // rows past the sequence read as zeros (buffer range)
-      const __amdgpu_buffer_rsrc_t bk = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<u16*>(p.k + (int64_t)(t0 + j0) * p.k_stride + (int64_t)h * D), (short)0,
-          (int)(((int64_t)(rows - 1) * p.k_stride + D) * 2), kBufWord3);
-      const __amdgpu_buffer_rsrc_t bv = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<u16*>(p.v + (int64_t)(t0 + j0) * p.v_stride + (int64_t)h * D), (short)0,
-          (int)(((int64_t)(rows - 1) * p.v_stride + D) * 2), kBufWord3);
+    for (int u = 0; u < kKa; ++u) at[u] = ka[u] + off;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int s = 0; s < kSt; ++s) {
-        const int i = tid + s * kExtThreads, r = i / kPc, c = i % kPc;
-        rk[s] = __builtin_amdgcn_raw_buffer_load_b128(bk, (int)((r * p.k_stride + c * 8) * 2), 0, 0);
-        rv[s] = __builtin_amdgcn_raw_buffer_load_b128(bv, (int)((r * p.v_stride + c * 8) * 2), 0, 0);
-      }
+    for (int t = 0; t < kN2; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int t = 0; t < kN2; ++t) s[t] = mfma32(lds_op(at[u & 7] + t * 32 * 2 * D + (u >> 3) * 256), q[u], s[t]);
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < kN2 * kU - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto to_log2 = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    if (p.softcap > 0.f) {
+#pragma unroll
+      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = capped(s[i >> 4][i & 15], c1, c2);
+    } else if (!raw) {
+#pragma unroll
+      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] *= c1;
     }
   };
-  auto land = [&](int x, int buf) __attribute__((always_inline)) {
-    if (x < c1t) {
+  // Key of score i of this lane within its tile
+  auto key = [&](int i) __attribute__((always_inline)) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * hh + (i & 3); };
+  // Bits of the scores whose keys lie in [lo, hi) of the tile.
+  auto seen_bits = [&](int lo, int hi) __attribute__((always_inline)) {
+    unsigned bits = 0;
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) {
-        const int i = tid + s * kExtThreads, r = i / kCp, c = i % kCp;
+    for (int t = 0; t < kN2; ++t) {
+      const int a = min(max(lo - 32 * t, 0), 32), b = min(max(hi - 32 * t, 0), 32);
+      unsigned x = (unsigned)(((1ull << b) - 1) & ~((1ull << a) - 1)) >> 4 * hh & 0x0f0f0f0fu;   // keys of this half
+      x = (x | x >> 4) & 0x00ff00ffu;
+      bits |= ((x | x >> 8) & 0xffffu) << 16 * t;
+    }
+    return bits;
+  };
+  auto bias = [&](f32x16 (&s)[kN2], int qrel) __attribute__((always_inline)) {   // qrel: query minus the tile's first key
+    const float dq = (float)(qrel - 4 * hh);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint2 a = f8x4_to_bf16(rk[s][2 * e], rksc[s]), b = f8x4_to_bf16(rk[s][2 * e + 1], rksc[s]);
-          *reinterpret_cast<uint4*>(&sK[buf][tidx<D>(r, 2 * c + e)]) = make_uint4(a.x, a.y, b.x, b.y);
-          const uint2 y = f8x4_to_bf16(rv[s][2 * e], rvsc[s]), z = f8x4_to_bf16(rv[s][2 * e + 1], rvsc[s]);
-          *reinterpret_cast<uint4*>(&sV[buf][tidx<D>(r, 2 * c + e)]) = make_uint4(y.x, y.y, z.x, z.y);
+    for (int i = 0; i < kS; ++i)
+      s[i >> 4][i & 15] -= slope * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
+  };
+  auto product = [&](uint32_t off, const f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    uint32_t at[2][kVa];
+#pragma unroll
+    for (int d = 0; d < kVa; ++d) {
+      at[0][d] = va[0][d] + off;
+      at[1][d] = va[1][d] + off;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < kN2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bf16x8 pb = acc_to_op(s[t], u);
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) {
+          const int imm = (32 * t + 16 * u) * 2 * D + (d >> 2) * 256;
+          o[d] = mfma32(join(lds_tr(at[0][d & 3] + imm), lds_tr(at[1][d & 3] + imm)), pb, o[d]);
         }
       }
-    } else {
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
-      for (int s = 0; s < kSt; ++s) {
-        const int i = tid + s * kExtThreads, r = i / kPc, c = i % kPc;
-        *reinterpret_cast<u32x4*>(&sK[buf][tidx<D>(r, c)]) = rk[s];
-        *reinterpret_cast<u32x4*>(&sV[buf][tidx<D>(r, c)]) = rv[s];
+    for (int i = 0; i < 2 * kN2 * kDT - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Softmax and second product; bit i of `hidden`: the row does not see key(i).
+  auto attend = [&](uint32_t off, f32x16 (&s)[kN2], unsigned hidden) __attribute__((always_inline)) {
+    const bool masked = __any(hidden != 0);
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int i = 1; i < kS; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
+    mx = half_max(mx);
+    if (__any(mx > m + slack || (m == -INFINITY && mx > m))) {
+      mx = fmaxf(m, mx);
+      const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : (m - mx) * cs);
+      m = mx;
+      l *= fct;
+#pragma unroll
+      for (int t = 0; t < kDT; ++t) o[t] *= fct;
+    }
+    const float base = m == -INFINITY ? 0.f : m * cs;
+    float ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+      s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -base));
+      ls += s[i >> 4][i & 15];
+    }
+    l += ls;
+    product(off, s);
+  };
+  // A masked weight is 0, and 0 times NaN or infinity would reach rows that do not see the
+  // key.  In a tile that some row sees only in part, scrub() looks at the V pieces that this
+  // thread wrote (or asked for), sets such values to zero in LDS and returns the rows that held any
+  // (the same in every thread); after the product, spill() adds them to the rows that see
+  // them, read again from where they came.
+  auto scrub = [&](auto piece, int pieces) __attribute__((always_inline)) -> unsigned long long {
+    bool odd = false;
+    for (int i = 0; i < pieces; ++i) {
+      const u32x4 v = *(lds_u32x4*)(uintptr_t)piece(i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd = odd || (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+    }
+    if (!__syncthreads_or(odd)) return 0;
+    if (tid < 2) sBad[tid] = 0;
+    __syncthreads();
+    for (int i = 0; i < pieces; ++i) {
+      const uint32_t at = piece(i);
+      u32x4 v = *(lds_u32x4*)(uintptr_t)at;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        unsigned x = v[e];
+        if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+        if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+        bad = bad || x != v[e];
+        v[e] = x;
+      }
+      if (bad) {
+        *(lds_u32x4w*)(uintptr_t)at = v;
+        const int r = (int)((at - lds_at(sT)) % kTile) / (2 * D);
+        atomicOr(&sBad[r >> 5], 1u << (r & 31));
+      }
+    }
+    __syncthreads();
+    return (unsigned long long)uni(sBad[1]) << 32 | uni(sBad[0]);
+  };
+  auto spill = [&](unsigned long long bad, unsigned hidden, auto value4) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (; bad; bad &= bad - 1) {
+      const int r = __builtin_ctzll(bad);
+      // row r of the tile is key(i) of the lanes of half (r >> 2) & 1
+      const unsigned hid = (unsigned)__shfl((int)hidden, q32 + 32 * (r >> 2 & 1), kWave);
+      const bool see = !(hid >> (16 * (r >> 5) + 4 * (r >> 3 & 3) + (r & 3)) & 1);
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) {
+        asm volatile("" ::: "memory");                  // (no loads ahead: this is the rare path)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const uint2 v = value4(r, 32 * d + 8 * r4 + 4 * hh);   // four bf16
+          const float x[4] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (see && (__float_as_uint(x[e]) & 0x7f800000u) == 0x7f800000u) o[d][4 * r4 + e] += x[e];
+        }
       }
     }
   };
 
-  int x = skip(c0t), buf = 0;
-  if (x < end) {
-    load(x);
-    land(x, 0);
-  }
-  __syncthreads();
+  // ---------------------------------------------------------------- cached rows
+  if constexpr (CACHED) {
+    constexpr int kCp = D / 16;                         // 16-code pieces of a row
+    constexpr int kCr = kWave / kCp;                    // rows that one wave's load brings
+    constexpr int kCt = kBN / kCr / 4;                  // loads per wave and tile
+    const int tiles = (P + kBN - 1) / kBN;
+    int x = 0;
+    if (p.window > 0 && !p.c.pos) {                     // rows that a window leaves out for every row
+      const int64_t first = (int64_t)start + ta - p.window + 1;
+      x = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
+    }
+    // Row this lane's load s brings from tile x, clamped into the held rows; page ids and
+    // scales are fetched a tile ahead.
+    auto row_of = [&](int x, int s) __attribute__((always_inline)) {
+      return min(x * kBN + (wave + 4 * s) * kCr + lane / kCp, P - 1);
+    };
+    int id[kCt];
+    int hid_id = -1;                                    // page of row x kBN + lane (its validity)
+    float ks[kCt], vs[kCt];
+    auto ids = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < kCt; ++s) id[s] = page_of(p.c, n, row_of(x, s));
+      const int r = x * kBN + lane;
+      hid_id = r < P ? page_of(p.c, n, r) : -1;
+    };
+    const uint32_t rawk = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K then V, kTile / 2 bytes each
+    auto fetch = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < kCt; ++s) {
+        const int pg = max(id[s], 0);
+        const int64_t row = page_rows(p.c, pg, h) + (row_of(x, s) & pmask);
+        to_lds(p.c.k + row * D + 16 * (lane % kCp), rawk + s * 4096);
+        to_lds(p.c.v + row * D + 16 * (lane % kCp), rawk + kTile / 2 + s * 4096);
+        const int64_t sc = (int64_t)pg * p.H_kv + h;
+        ks[s] = id[s] < 0 ? 0.f : p.c.k_scale[sc];      // (0: no row here)
+        vs[s] = id[s] < 0 ? 0.f : p.c.v_scale[sc];
+      }
+    };
+    if (x < tiles) {
+      ids(x);
+      fetch(x);
+    }
+    unsigned long long held = __ballot(hid_id >= 0);
 #pragma unroll 1
-  while (x < end) {
-    const int nx = skip(x + 1);
-    if (nx < end) load(nx);
-    const bool cached = x < c1t;
-    const int j0 = (cached ? x : x - c1t + d0) * kBN;    // first key: cached row or token
-    // does the wave see any of it, and all of it?
-    bool none = false, full;
-    if (cached) {
-      full = j0 + kBN <= P && p.window == 0;
-    } else {
-      full = j0 + kBN <= L && (j0 + kBN - 1 <= wa || j0 + kBN <= mk.vis);
-      none = j0 > wz && j0 >= mk.vis;
-      if (p.window > 0) {
-        full = full && wz - j0 < p.window && j0 + kBN - 1 - wa < p.window;
-        none = none || wa - (j0 + kBN - 1) >= p.window;
+    for (; x < tiles; ++x) {
+      vm_wait();                                        // this wave's codes have landed
+      lds_sync();                                       // nobody reads the last tile any more
+#pragma unroll
+      for (int s = 0; s < kCt; ++s) {
+        const int r = (wave + 4 * s) * kCr + lane / kCp, c = lane % kCp;
+        const bool in = x * kBN + r < P && ks[s] != 0.f;
+        const uint32_t at = rawk + s * 4096 + lane * 16;
+        const u32x4 k8 = *(lds_u32x4*)(uintptr_t)at, v8 = *(lds_u32x4*)(uintptr_t)(at + kTile / 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t to = lds_at(sT) + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4);
+          const uint2 a = f8x4_to_bf16(k8[2 * e], ks[s]), b = f8x4_to_bf16(k8[2 * e + 1], ks[s]);
+          const uint2 y = f8x4_to_bf16(v8[2 * e], vs[s]), z = f8x4_to_bf16(v8[2 * e + 1], vs[s]);
+          *(lds_u32x4w*)(uintptr_t)to = in ? u32x4{a.x, a.y, b.x, b.y} : u32x4{0, 0, 0, 0};
+          *(lds_u32x4w*)(uintptr_t)(to + kTile) = in ? u32x4{y.x, y.y, z.x, z.y} : u32x4{0, 0, 0, 0};
+        }
       }
-      if (mk.doc) full = full && (doc_flags(x - c1t + d0) & 2);
+      const unsigned long long now = held;
+      unsigned long long bad = 0;
+      // (rows that are not held are zeros; only a window hides a held row from some rows)
+      if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
+        bad = scrub([&](int i) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + lane / kCp) * 2 * D +
+                                        (((2 * (lane % kCp) + (i & 1)) ^ row_swz<D>((wave + 4 * (i >> 1)) * kCr + lane / kCp)) << 4); },
+                    2 * kCt);
+      lds_sync();
+      if (x + 1 < tiles) {
+        ids(x + 1);
+        fetch(x + 1);
+        held = __ballot(hid_id >= 0);
+      }
+      f32x16 s[kN2];
+      scores(0, s);
+      to_log2(s);
+      unsigned hidden = 0;
+      const int j0 = x * kBN;
+      if (now != ~0ull) {
+#pragma unroll
+        for (int i = 0; i < kS; i += 4) hidden |= ((unsigned)(~now >> key(i)) & 15u) << i;
+      }
+      if (p.c.pos && (p.slopes || p.window > 0)) {
+        const int qpos = start + ti;
+#pragma unroll
+        for (int i = 0; i < kS; i += 4) {
+          const int r = j0 + key(i), pg = r < P ? page_of(p.c, n, r) : -1;
+          int4 kp = make_int4(qpos, qpos, qpos, qpos);
+          if (pg >= 0) kp = *reinterpret_cast<const int4*>(p.c.pos + page_rows(p.c, pg, h) + (r & pmask));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int dist = abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w));
+            s[i >> 4][(i & 15) + e] -= slope * (float)dist;
+            if (p.window > 0 && dist >= p.window) hidden |= 1u << (i + e);
+          }
+        }
+      } else if (p.slopes || p.window > 0) {
+        const int qrel = start + ti - j0;
+        if (p.slopes) bias(s, qrel);
+        if (p.window > 0 && start + wz - j0 >= p.window) hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
+      }
+      attend(0, s, hidden);
+      if (bad)
+        spill(bad, hidden, [&](int r, int col) {
+          const int row = min(j0 + r, P - 1), pg = max(page_of(p.c, n, row), 0);
+          const uint32_t w4 = *reinterpret_cast<const uint32_t*>(p.c.v + (page_rows(p.c, pg, h) + (row & pmask)) * D + col);
+          return f8x4_to_bf16(w4, 1.f);
+        });
     }
-    if (!none) {
-      f32x16 s[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const bf16x8 a = as_bf16x8(*reinterpret_cast<const uint4*>(&sK[buf][tidx<D>(32 * t + q32, 2 * u + hh)]));
-          s[t] = mfma32(a, q[u], s[t]);
-        }
-      }
-      if (p.softcap > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = capped(s[i >> 4][i & 15], c1, c2);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] *= c1;
-      }
-      unsigned hidden = 0;                  // bit 16 t + e: key not seen by this lane's row
-      if (cached) {
-        if (p.window > 0 || p.slopes || !full) {
-          const int qpos = start + ti;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-              const int r = j0 + 32 * t + 8 * r4 + 4 * hh;        // four rows of one page
-              int4 kp = make_int4(r, r + 1, r + 2, r + 3);
-              const int id = r < P ? page_of(p.c, n, r) : -1;
-              if (p.c.pos && id >= 0)
-                kp = *reinterpret_cast<const int4*>(p.c.pos + page_rows(p.c, id, h) + (r & ((1 << lg) - 1)));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int dist = abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w));
-                s[t][4 * r4 + e] -= slope * (float)dist;
-                if (id < 0 || r + e >= P || (p.window > 0 && dist >= p.window)) hidden |= 1u << (16 * t + 4 * r4 + e);
-              }
-            }
-        } else {
-          // a full tile can still have a page out of range
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; r4 += 2)
-              if (page_of(p.c, n, j0 + 32 * t + 8 * r4) < 0) hidden |= 0xffu << (16 * t + 4 * r4);
-        }
-      } else {
-        if (p.slopes) {
-          const float dq = (float)(ti - j0 - 4 * hh);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            s[i >> 4][i & 15] -= slope * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
-        }
-        if (!full) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = j0 + 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * hh + (i & 3);
-            const int dj = mk.doc ? mk.doc[min(j, L - 1)] : 0;
-            if (j >= L || !ext_seen(mk, ti, j, di, dj)) hidden |= 1u << i;
-          }
-        }
-      }
-      const bool masked = __any(hidden != 0);
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
-      mx = fmaxf(m, half_max(mx));
-      if (__any(mx > m)) {
-        const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : m - mx);
-        m = mx;
-        l *= fct;
-#pragma unroll
-        for (int t = 0; t < kDT; ++t) o[t] *= fct;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      float ls = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(s[i >> 4][i & 15] - base);
-        ls += s[i >> 4][i & 15];
-      }
-      l += ls;
-      // A masked weight is 0, and 0 times NaN or infinity would reach rows that do not see
-      // the key: where a tile with hidden keys holds such a value, the product runs on
-      // cleaned operands and the values are added to the rows that see them.
-      unsigned long long dirty = 0;
-      if (masked) {
-        bool odd = false;
-#pragma unroll
-        for (int c = 0; c < kPc; ++c) {
-          const u32x4 vv = *reinterpret_cast<const u32x4*>(&sV[buf][tidx<D>(lane, c)]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            odd = odd || (vv[e] & 0x7f80u) == 0x7f80u || (vv[e] & 0x7f800000u) == 0x7f800000u;
-        }
-        dirty = __ballot(odd);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bf16x8 pb = acc_to_op(s[t], u);
-#pragma unroll
-          for (int d = 0; d < kDT; ++d) {
-            const int r = 32 * t + 16 * u + 4 * hh + ((lane & 15) >> 2), c = 4 * d + (lane >> 4 & 1) * 2 + ((lane & 3) >> 1);
-            uint2 a0 = tr_read(&sV[buf][tidx<D>(r, c) + 4 * (lane & 1)]);
-            uint2 a1 = tr_read(&sV[buf][tidx<D>(r + 8, c) + 4 * (lane & 1)]);
-            if (dirty) {
-              auto clean = [](unsigned v) {
-                if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-                if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
-                return v;
-              };
-              a0 = make_uint2(clean(a0.x), clean(a0.y));
-              a1 = make_uint2(clean(a1.x), clean(a1.y));
-            }
-            o[d] = mfma32(join(a0, a1), pb, o[d]);
-          }
-        }
-      for (unsigned long long left = dirty; left; left &= left - 1) {
-        const int r = __builtin_ctzll(left);
-        // key r of the tile sits in half (r >> 2) & 1, at bit 16 (r >> 5) + 4 (r >> 3 & 3) + (r & 3)
-        const unsigned hid = (unsigned)__shfl((int)hidden, q32 + 32 * (r >> 2 & 1), kWave);
-        if (hid >> (16 * (r >> 5) + 4 * (r >> 3 & 3) + (r & 3)) & 1) continue;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = 32 * d + acc_row(e, hh);
-            const float v = bf16_to_f32(sV[buf][tidx<D>(r, col >> 3) + (col & 7)]);
-            if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) o[d][e] += v;
-          }
-      }
+    lds_sync();
+  }
+
+  // ---------------------------------------------------------------- new tokens
+  int last = min(L, max(tz + 1, min(vis, L)));          // keys [first, last) are seen by some row
+  int first = 0;
+  if (p.window > 0) {
+    first = (int)max((int64_t)0, (int64_t)ta - p.window + 1);
+    last = (int)min((int64_t)last, (int64_t)tz + p.window);
+  }
+  const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
+  // Document mask: which key tiles hold a document of this workgroup's rows, a wave per tile.
+  if (doc) {
+    for (int i = tid; i < kFlags / 16; i += kExtThreads) sFlag[i] = 0;
+    if (tid == 0) {
+      sDoc[0] = INT32_MAX;
+      sDoc[1] = INT32_MIN;
     }
-    if (nx < end) land(nx, buf ^ 1);
     __syncthreads();
-    buf ^= 1;
-    x = nx;
+    for (int t = ta + tid; t <= tz; t += kExtThreads) {
+      atomicMin(&sDoc[0], doc[t]);
+      atomicMax(&sDoc[1], doc[t]);
+    }
+    __syncthreads();
+    const int dmin = sDoc[0], dmax = sDoc[1], lim = min(d1, d0 + kFlags);
+    constexpr int kAhead = 4;
+    for (int t = d0 + wave * kAhead; t < lim; t += 4 * kAhead) {
+      int v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = (t + i) * kBN + lane;
+        v[i] = j < L ? doc[j] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const bool any = __any(v[i] >= 0 && v[i] >= dmin && v[i] <= dmax);
+        const bool all = dmin == dmax && __all(v[i] >= 0 && v[i] == dmin);
+        if (lane == 0 && t + i < lim)
+          atomicOr(&sFlag[(t + i - d0) >> 4], (any ? 1u : 0u) << 2 * ((t + i - d0) & 15) | (all ? 2u : 0u) << 2 * ((t + i - d0) & 15));
+      }
+    }
+    __syncthreads();
+  }
+  auto doc_flags = [&](int t) __attribute__((always_inline)) -> unsigned {
+    return t - d0 < kFlags ? uni(sFlag[(t - d0) >> 4]) >> 2 * ((t - d0) & 15) & 3 : 1u;
+  };
+  auto next = [&](int t) __attribute__((always_inline)) {   // the next tile at or after t to look at
+    if (doc)
+      while (t < d1 && !(doc_flags(t) & 1)) ++t;
+    return t;
+  };
+  // Loads of tile t: this lane's piece of each of the wave's loads.  (Piece l % kPc of row
+  // r in LDS is the row's piece (l % kPc) ^ swizzle(r); rows past the sequence read as zeros.)
+  const uint32_t kst = (uint32_t)p.k_stride * 2, vst = (uint32_t)p.v_stride * 2;   // bytes
+  const uint32_t ldsw = uni(lds_at(sT) + wave * 1024);
+  auto fetch = [&](int t, uint32_t off) __attribute__((always_inline)) {
+    const int j0 = t * kBN, rows = min(kBN, L - j0);
+    const u32x4 bk = buffer_of(p.k + (int64_t)(t0 + j0) * p.k_stride + (int64_t)h * D, (rows - 1) * kst + 2 * D);
+    const u32x4 bv = buffer_of(p.v + (int64_t)(t0 + j0) * p.v_stride + (int64_t)h * D, (rows - 1) * vst + 2 * D);
+#pragma unroll
+    for (int s = 0; s < kLd; ++s) {
+      const int r = (wave + 4 * s) * kRpi + lane / kPc;
+      const uint32_t c = (uint32_t)((lane % kPc) ^ row_swz<D>(r)) << 4;
+      to_lds(bk, r * kst + c, ldsw + off + s * 4096);
+      to_lds(bv, r * vst + c, ldsw + off + kTile + s * 4096);
+    }
+  };
+  int t = next(d0);
+  uint32_t off = 0;
+  if (t < d1) fetch(t, 0);
+#pragma unroll 1
+  while (t < d1) {
+    const int nx = next(t + 1);
+    vm_wait();                                          // this wave's share of the tile has landed
+    lds_sync();                                         // everyone's has, and nobody reads the other pair
+    if (nx < d1) fetch(nx, off ^ (2 * kTile));
+    const int j0 = t * kBN, je = j0 + kBN - 1;
+    // do these tokens' rows see all of the tile?  does the wave see any of it?
+    const bool one_doc = !doc || (doc_flags(t) & 2);
+    auto all_of = [&](int a, int z) __attribute__((always_inline)) {
+      return one_doc && je < L && (je <= a || je < vis) && (p.window == 0 || (z - j0 < p.window && je - a < p.window));
+    };
+    const bool full = all_of(wa, wz);
+    const bool none = (j0 > wz && j0 >= vis) || (p.window > 0 && wa - je >= p.window);
+    unsigned long long bad = 0;
+    if (!all_of(ta, tz))
+      bad = scrub([&](int i) { return ldsw + off + kTile + i * 4096 + lane * 16; }, kLd);
+    if (!none) {
+      f32x16 s[kN2];
+      scores(off, s);
+      to_log2(s);
+      if (p.slopes) bias(s, ti - j0);
+      unsigned hidden = 0;
+      if (!full) {
+        // seen keys are a range: below the row's own or the prefix, inside the window
+        int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
+        if (p.window > 0) {
+          lo = ti - j0 - p.window + 1;
+          hi = min(hi, ti - j0 + p.window);
+        }
+        hidden = ~seen_bits(lo, hi);
+        if (doc) {                                      // the wave's own copy of the tile's ids
+          const int j = j0 + lane;
+          sIds[wave][lane] = j < L ? doc[j] : -1;
+          lds_order();
+#pragma unroll
+          for (int i = 0; i < kS; i += 4) {
+            const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i)]);
+            if (di < 0 || dj.x != di) hidden |= 1u << i;
+            if (di < 0 || dj.y != di) hidden |= 2u << i;
+            if (di < 0 || dj.z != di) hidden |= 4u << i;
+            if (di < 0 || dj.w != di) hidden |= 8u << i;
+          }
+          lds_order();
+        }
+      }
+      attend(off, s, hidden);
+      if (bad)
+        spill(bad, hidden, [&](int r, int col) {
+          return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(j0 + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
+        });
+    }
+    off ^= 2 * kTile;
+    t = nx;
   }
 
   l += __shfl_xor(l, 32, kWave);
@@ -409,17 +577,25 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
           make_uint2(cvt2(o[d][4 * r4] * inv, o[d][4 * r4 + 1] * inv), cvt2(o[d][4 * r4 + 2] * inv, o[d][4 * r4 + 3] * inv));
 }
 
+template <int D>
+hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
+  const int64_t slots = p.T * (p.H / p.H_kv) / kBM + p.N;
+  const dim3 grid((unsigned)(slots * p.H_kv));
+  if (p.c.k)
+    extend_kernel<D, true><<<grid, kExtThreads, 0, s>>>(p);
+  else
+    extend_kernel<D, false><<<grid, kExtThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_attn_extend(const AttnExtendLaunch& p, hipStream_t s) {
-  const int64_t slots = p.T * (p.H / p.H_kv) / kBM + p.N;
-  const dim3 grid((unsigned)(slots * p.H_kv));
   switch (p.d) {
-    case 64: extend_kernel<64><<<grid, kExtThreads, 0, s>>>(p); break;
-    case 128: extend_kernel<128><<<grid, kExtThreads, 0, s>>>(p); break;
-    default: extend_kernel<256><<<grid, kExtThreads, 0, s>>>(p); break;
+    case 64: return launch_d<64>(p, s);
+    case 128: return launch_d<128>(p, s);
+    default: return launch_d<256>(p, s);
   }
-  return hipGetLastError();
 }
 
 }  // namespace gdn
