@@ -201,7 +201,8 @@ int gdn_attn_extend(const gdn_attn_extend_args* a, void* stream) {
       overlap(a->out, out_bytes, a->v, rows_bytes(a->T, a->v_stride, (int64_t)a->H_kv * a->d)))
     return GDN_E_SHAPE;
   if (a->N == 0 || a->T == 0) return GDN_OK;
-  if ((a->T * (a->H / a->H_kv) / 128 + a->N) * a->H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
+  const int64_t rows = a->T * (a->H / a->H_kv);          // (token, head of a group) rows: 32-bit in the kernel
+  if (rows > INT32_MAX - 1024 || (rows / 128 + a->N) * a->H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.T = a->T;
   p.H = a->H;

@@ -59,7 +59,13 @@ __device__ __forceinline__ float capped(float x, float f1x2log2e, float f2) {
   return fmaf(-2.0f * f2, __builtin_amdgcn_rcpf(1.0f + e), f2);
 }
 
-// max / sum over the two 32-lane halves
-__device__ __forceinline__ float half_max(float v) { return fmaxf(v, __shfl_xor(v, 32, kWave)); }
+// Maximum over the two 32-lane halves, in every lane: the swap leaves one half's value of
+// the pair in each result.  (Two registers: the instruction exchanges them in place.)
+__device__ __forceinline__ float half_max(float v) {
+  unsigned a = __float_as_uint(v), b = a;
+  asm volatile("" : "+v"(b));
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
 
 }  // namespace gdn

@@ -15,12 +15,16 @@
 //     are taken as 8 (2 u + (e >> 2)) + 4 half + (e & 3), and V^T comes from the row-major V
 //     tile by LDS transpose reads of 4 rows in that order.
 // K and V tiles of 64 keys stand in LDS as bf16, their 16-byte pieces XOR-swizzled by row
-// (operand and transpose reads without bank conflicts).  Up to d = 128 two workgroups fit
-// a CU and one's softmax runs under the other's products; at d = 256 one does (its output
-// alone takes 128 registers), and its products take twice as long as its softmax.  New tokens'
-// tiles are double-buffered and go from memory to LDS without passing through registers;
-// the swizzle is on the global side.  Cached rows arrive as codes the same way; the lane
-// that asked for a piece turns it into bf16 times its page's power-of-two scale (exact).
+// (operand and transpose reads without bank conflicts).  New tokens' tiles are
+// double-buffered and go from memory to LDS without passing through registers; the swizzle
+// is on the global side.  Cached rows arrive as codes the same way; the lane that asked
+// for a piece turns it into bf16 times its page's power-of-two scale (exact).
+// The loop is a tile deep: while the matrix units form the scores of the next tile, the
+// vector units turn this tile's into weights; then, under the second product, they look
+// for the next tile's maximum.  (One after the other, both kept the SIMDs busy 44% of the
+// time each with hardly any overlap, even with two workgroups on a CU: 944 TFLOP/s at
+// 8 x 4096 tokens, 32 / 8 heads, d = 128.)  Up to d = 128 two workgroups fit a CU; at d =
+// 256 one does (its output alone takes 128 registers).
 // The weights are rounded to bf16 for the second product, their sum is not.
 #include "attn_common.h"
 
@@ -92,17 +96,16 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   // Heads fastest: consecutive workgroups go to the 8 XCDs in turn, so a head's tiles share
   // an L2.  Late tiles of a causal sequence see the most keys: they are launched first.
   const int h = blockIdx.x % p.H_kv;
-  const int64_t w = (int64_t)(gridDim.x / p.H_kv) - 1 - blockIdx.x / p.H_kv;
+  const int w = (int)(gridDim.x / p.H_kv) - 1 - (int)(blockIdx.x / p.H_kv);
   // slot w -> (sequence n, tile): sequence n's tiles begin at floor(cu[n] G / 128) + n
   int lo = 0, hi = p.N;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((int64_t)p.cu[mid] * G / kBM + mid <= w) lo = mid; else hi = mid;
+    if (p.cu[mid] * G / kBM + mid <= w) lo = mid; else hi = mid;
   }
   const int n = lo, t0 = p.cu[n], L = p.cu[n + 1] - t0;
-  const int64_t tile = w - ((int64_t)t0 * G / kBM + n);
-  const int64_t f0 = tile * kBM;
-  if (tile < 0 || f0 >= (int64_t)L * G) return;
+  const int rows = L * G, f0 = (w - (t0 * G / kBM + n)) * kBM;   // (T G stays below 2^31)
+  if (f0 < 0 || f0 >= rows) return;
   int P = CACHED ? p.cache_len[n] : 0;                  // cached rows
   if (P < 0) return;
   const int start = p.start ? p.start[n] : P;           // position of token 0
@@ -110,14 +113,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   if (CACHED) P = (int)min((int64_t)P, (int64_t)p.c.table_width << lg);
 
   // this lane's row, and the wave's and workgroup's tokens
-  const int64_t f = f0 + wave * 32 + q32;
-  const bool live = f < (int64_t)L * G;
-  const int ti = live ? (int)(f / G) : L - 1, g = live ? (int)(f - (int64_t)ti * G) : 0;
+  const int f = f0 + wave * 32 + q32;
+  const bool live = f < rows;
+  const int ti = live ? (int)((unsigned)f / (unsigned)G) : L - 1, g = live ? f - ti * G : 0;
   const int hq = h * G + g;
-  const int ta = (int)(f0 / G), tz = (int)(min(f0 + kBM - 1, (int64_t)L * G - 1) / G);
-  const int64_t fw = f0 + wave * 32;
-  const int wa = (int)min(fw / G, (int64_t)L - 1), wz = (int)(min(fw + 31, (int64_t)L * G - 1) / G);
-
+  const int ta = (int)uni((unsigned)f0 / (unsigned)G), tz = (int)uni((unsigned)(min(f0 + kBM, rows) - 1) / (unsigned)G);
+  const int wa = __builtin_amdgcn_readlane(ti, 0), wz = __builtin_amdgcn_readlane(ti, 63);   // (a dead row counts as the last token)
   const int vis = p.causal ? (p.visible ? p.visible[n] : 0) : INT32_MAX;   // keys below: seen by every row
   const int32_t* doc = p.doc ? p.doc + t0 : nullptr;
   const int di = doc ? doc[ti] : 0;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
   const float slack = 8.f / cs;            // the maximum in use may lag the true one by 2^8
 
-  // operand addresses in the first tile pair; a tile is kTile bytes, a pair 2 kTile
+  // operand addresses in the first K and V tile (kTile bytes each: K, V, K, V)
   uint32_t ka[kKa], va[2][kVa];
   {
     const uint32_t base = lds_at(sT);
@@ -153,36 +154,134 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       }
   }
 
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, base = 0.f, l = 0.f;   // base: m in units of log2, 0 while nothing is seen
   f32x16 o[kDT];
 #pragma unroll
   for (int t = 0; t < kDT; ++t)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[t][e] = 0.f;
+  bf16x8 pb[2 * kN2];                      // the weights as operands, 16 keys each
 
-  // The scores of the tile pair at byte offset `off` of sT.  Operand reads run a few steps
-  // ahead of the products (left alone, the compiler waits for each read before its MFMA).
-  auto scores = [&](uint32_t off, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
-    uint32_t at[kKa];
+  constexpr int kNS = kN2 * kU, kNP = 2 * kN2 * kDT;   // MFMAs of a tile's scores and of its product
+  constexpr int kRing = 4;                 // operands in flight
+  auto k_op = [&](int i, uint32_t koff) __attribute__((always_inline)) {   // operand i of the K tile at koff
+    const int t = i % kN2, u = i / kN2;
+    return lds_op(ka[u & 7] + (koff + t * 32 * 2 * D + (u >> 3) * 256));
+  };
+  auto v_op = [&](int i, uint32_t voff) __attribute__((always_inline)) {
+    const int k = i / kDT, d = i % kDT;
+    const uint32_t imm = voff + 16 * k * 2 * D + (d >> 2) * 256;
+    return join(lds_tr(va[0][d & 3] + imm), lds_tr(va[1][d & 3] + imm));
+  };
+  // One MFMA of the scores, and the read that its operand slot is free for.
+  auto score = [&](int i, uint32_t koff, f32x16 (&s)[kN2], bf16x8 (&a)[kRing]) __attribute__((always_inline)) {
+    f32x16 zero;
 #pragma unroll
-    for (int u = 0; u < kKa; ++u) at[u] = ka[u] + off;
+    for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+    s[i % kN2] = mfma32(a[i % kRing], q[i / kN2], i < kN2 ? zero : s[i % kN2]);
+    if (i + kRing < kNS) a[i % kRing] = k_op(i + kRing, koff);
+  };
+  auto scores = [&](uint32_t koff, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    bf16x8 a[kRing];
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) a[i] = k_op(i, koff);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int t = 0; t < kN2; ++t)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[t][e] = 0.f;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int t = 0; t < kN2; ++t) s[t] = mfma32(lds_op(at[u & 7] + t * 32 * 2 * D + (u >> 3) * 256), q[u], s[t]);
-    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-#pragma unroll
-    for (int i = 0; i < kN2 * kU - 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    for (int i = 0; i < kNS; ++i) {
+      score(i, koff, s, a);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+  };
+  // Score i of this lane -> weight, its part of the sum, and every eighth an operand.
+  float ls[2];
+  auto weight = [&](int i, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    const float x = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -base));
+    s[i >> 4][i & 15] = x;
+    ls[i & 1] = i < 2 ? x : ls[i & 1] + x;
+    if ((i & 7) == 7) pb[i >> 3] = acc_to_op(s[i >> 4], i >> 3 & 1);
+  };
+  auto weights = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kS; ++i) weight(i, s);
+    l += ls[0] + ls[1];
+  };
+  // O^T += V^T P^T with the V tile `voff` bytes behind the first.
+  auto product = [&](uint32_t voff) __attribute__((always_inline)) {
+    bf16x8 a[kRing];
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) a[i] = v_op(i, voff);
     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kNP; ++i) {
+      o[i % kDT] = mfma32(a[i % kRing], pb[i / kDT], o[i % kDT]);
+      if (i + kRing < kNP) a[i % kRing] = v_op(i + kRing, voff);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto tile_max = [&](const f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+    float a = s[0][0];
+#pragma unroll
+    for (int i = 1; i < kS; ++i) a = fmaxf(a, s[i >> 4][i & 15]);
+    return a;
+  };
+  // Makes m hold for a tile whose largest score in this lane is mx.
+  auto raise = [&](float mx) __attribute__((always_inline)) {
+    mx = half_max(mx);
+    if (__any(mx > m + slack)) {
+      mx = fmaxf(m, mx);
+      const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : (m - mx) * cs);
+      m = mx;
+      base = m == -INFINITY ? 0.f : m * cs;
+      l *= fct;
+#pragma unroll
+      for (int t = 0; t < kDT; ++t) o[t] *= fct;
+    }
+  };
+  auto hide = [&](f32x16 (&s)[kN2], unsigned hidden) __attribute__((always_inline)) {
+    if (__any(hidden != 0)) {
+#pragma unroll
+      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
+    }
+  };
+  // One step: weights of the tile in s under the scores of the next (s2), then this tile's
+  // product under the next one's maximum.  load(0), load(1) start the loads of later tiles;
+  // finish(s2) brings the new scores to their final form (cap, bias, mask).  The order is fixed here, an MFMA and its share of vector work at a time
+  // with operands kRing MFMAs ahead: left alone, the compiler waits for each read before
+  // its MFMA and puts the vector work behind them all.
+  auto step = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t koff, uint32_t voff, auto load,
+                  auto finish) __attribute__((always_inline)) {
+    bf16x8 a[kRing];
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) a[i] = k_op(i, koff);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kNS; ++i) {
+      score(i, koff, s2, a);
+#pragma unroll
+      for (int e = i * kS / kNS; e < (i + 1) * kS / kNS; ++e) weight(e, s);
+      if (i < 2) load(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    l += ls[0] + ls[1];
+    // (formed here: the compiler would sink them behind the branches of finish)
+#pragma unroll
+    for (int i = 0; i < 2 * kN2; ++i) asm volatile("" : "+v"(pb[i]));
+    asm volatile("" : "+v"(l));
+    finish(s2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) a[i] = v_op(i, voff);
+    __builtin_amdgcn_sched_barrier(0);
+    float mx = s2[0][0];
+#pragma unroll
+    for (int i = 0; i < kNP; ++i) {
+      o[i % kDT] = mfma32(a[i % kRing], pb[i / kDT], o[i % kDT]);
+      if (i + kRing < kNP) a[i % kRing] = v_op(i + kRing, voff);
+#pragma unroll
+      for (int e = i * kS / kNP; e < (i + 1) * kS / kNP; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    raise(mx);
   };
   auto to_log2 = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
     if (p.softcap > 0.f) {
@@ -193,11 +292,18 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] *= c1;
     }
   };
-  // Key of score i of this lane within its tile
-  auto key = [&](int i) __attribute__((always_inline)) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * hh + (i & 3); };
+  // A copy of v that the compiler cannot see through: what the paths below compute from it
+  // is computed there, and not kept in registers over the whole loop.
+  auto opaque = [](int v) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  // Key of score i of a lane of half hh within its tile
+  auto key = [](int i, int hh) __attribute__((always_inline)) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * hh + (i & 3); };
   // Bits of the scores whose keys lie in [lo, hi) of the tile.
   auto seen_bits = [&](int lo, int hi) __attribute__((always_inline)) {
     unsigned bits = 0;
+    const int hh = opaque(lane) >> 5;
 #pragma unroll
     for (int t = 0; t < kN2; ++t) {
       const int a = min(max(lo - 32 * t, 0), 32), b = min(max(hi - 32 * t, 0), 32);
@@ -208,75 +314,21 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     return bits;
   };
   auto bias = [&](f32x16 (&s)[kN2], int qrel) __attribute__((always_inline)) {   // qrel: query minus the tile's first key
-    const float dq = (float)(qrel - 4 * hh);
+    const float dq = (float)(qrel - 4 * (opaque(lane) >> 5));
 #pragma unroll
     for (int i = 0; i < kS; ++i)
       s[i >> 4][i & 15] -= slope * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
-  };
-  auto product = [&](uint32_t off, const f32x16 (&s)[kN2]) __attribute__((always_inline)) {
-    uint32_t at[2][kVa];
-#pragma unroll
-    for (int d = 0; d < kVa; ++d) {
-      at[0][d] = va[0][d] + off;
-      at[1][d] = va[1][d] + off;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int t = 0; t < kN2; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 pb = acc_to_op(s[t], u);
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) {
-          const int imm = (32 * t + 16 * u) * 2 * D + (d >> 2) * 256;
-          o[d] = mfma32(join(lds_tr(at[0][d & 3] + imm), lds_tr(at[1][d & 3] + imm)), pb, o[d]);
-        }
-      }
-    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
-#pragma unroll
-    for (int i = 0; i < 2 * kN2 * kDT - 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  // Softmax and second product; bit i of `hidden`: the row does not see key(i).
-  auto attend = [&](uint32_t off, f32x16 (&s)[kN2], unsigned hidden) __attribute__((always_inline)) {
-    const bool masked = __any(hidden != 0);
-    if (masked) {
-#pragma unroll
-      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
-    }
-    float mx = s[0][0];
-#pragma unroll
-    for (int i = 1; i < kS; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
-    mx = half_max(mx);
-    if (__any(mx > m + slack || (m == -INFINITY && mx > m))) {
-      mx = fmaxf(m, mx);
-      const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : (m - mx) * cs);
-      m = mx;
-      l *= fct;
-#pragma unroll
-      for (int t = 0; t < kDT; ++t) o[t] *= fct;
-    }
-    const float base = m == -INFINITY ? 0.f : m * cs;
-    float ls = 0.f;
-#pragma unroll
-    for (int i = 0; i < kS; ++i) {
-      s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -base));
-      ls += s[i >> 4][i & 15];
-    }
-    l += ls;
-    product(off, s);
   };
   // A masked weight is 0, and 0 times NaN or infinity would reach rows that do not see the
   // key.  In a tile that some row sees only in part, scrub() looks at the V pieces that this
   // thread wrote (or asked for), sets such values to zero in LDS and returns the rows that held any
   // (the same in every thread); after the product, spill() adds them to the rows that see
   // them, read again from where they came.
-  auto scrub = [&](auto piece, int pieces) __attribute__((always_inline)) -> unsigned long long {
+  auto scrub = [&](auto piece_of, int pieces) __attribute__((always_inline)) -> unsigned long long {
     bool odd = false;
+    const int ln = opaque(lane);
+    auto piece = [&](int i) __attribute__((always_inline)) { return piece_of(i, ln); };
+#pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
       const u32x4 v = *(lds_u32x4*)(uintptr_t)piece(i);
 #pragma unroll
@@ -285,6 +337,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     if (!__syncthreads_or(odd)) return 0;
     if (tid < 2) sBad[tid] = 0;
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
       const uint32_t at = piece(i);
       u32x4 v = *(lds_u32x4*)(uintptr_t)at;
@@ -307,6 +360,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     return (unsigned long long)uni(sBad[1]) << 32 | uni(sBad[0]);
   };
   auto spill = [&](unsigned long long bad, unsigned hidden, auto value4) __attribute__((always_inline)) {
+    const int ln = opaque(lane), q32 = ln & 31, hh = ln >> 5;
 #pragma unroll 1
     for (; bad; bad &= bad - 1) {
       const int r = __builtin_ctzll(bad);
@@ -339,84 +393,50 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       const int64_t first = (int64_t)start + ta - p.window + 1;
       x = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
     }
-    // Row this lane's load s brings from tile x, clamped into the held rows; page ids and
-    // scales are fetched a tile ahead.
+    // Row this lane's load s brings from tile x, clamped into the held rows; page ids are
+    // fetched two tiles ahead, scales one.
     auto row_of = [&](int x, int s) __attribute__((always_inline)) {
       return min(x * kBN + (wave + 4 * s) * kCr + lane / kCp, P - 1);
     };
-    int id[kCt];
-    int hid_id = -1;                                    // page of row x kBN + lane (its validity)
-    float ks[kCt], vs[kCt];
-    auto ids = [&](int x) __attribute__((always_inline)) {
+    // Codes of a tile: K and V, kTile / 2 bytes each, behind the first K and V tiles.
+    const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);
+    auto fetch = [&](const uint8_t* src, uint32_t to, const int (&id)[kCt], int x) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) id[s] = page_of(p.c, n, row_of(x, s));
-      const int r = x * kBN + lane;
-      hid_id = r < P ? page_of(p.c, n, r) : -1;
+      for (int s = 0; s < kCt; ++s)
+        to_lds(src + (page_rows(p.c, max(id[s], 0), h) + (row_of(x, s) & pmask)) * D + 16 * (lane % kCp), to + s * 4096);
     };
-    const uint32_t rawk = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K then V, kTile / 2 bytes each
-    auto fetch = [&](int x) __attribute__((always_inline)) {
+    auto scales = [&](const float* src, float (&sc)[kCt], const int (&id)[kCt]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) {
-        const int pg = max(id[s], 0);
-        const int64_t row = page_rows(p.c, pg, h) + (row_of(x, s) & pmask);
-        to_lds(p.c.k + row * D + 16 * (lane % kCp), rawk + s * 4096);
-        to_lds(p.c.v + row * D + 16 * (lane % kCp), rawk + kTile / 2 + s * 4096);
-        const int64_t sc = (int64_t)pg * p.H_kv + h;
-        ks[s] = id[s] < 0 ? 0.f : p.c.k_scale[sc];      // (0: no row here)
-        vs[s] = id[s] < 0 ? 0.f : p.c.v_scale[sc];
-      }
+      for (int s = 0; s < kCt; ++s) sc[s] = id[s] < 0 ? 0.f : src[(int64_t)id[s] * p.H_kv + h];   // (0: no row here)
     };
-    if (x < tiles) {
-      ids(x);
-      fetch(x);
-    }
-    unsigned long long held = __ballot(hid_id >= 0);
-#pragma unroll 1
-    for (; x < tiles; ++x) {
-      vm_wait();                                        // this wave's codes have landed
-      lds_sync();                                       // nobody reads the last tile any more
+    auto convert = [&](uint32_t from, uint32_t to, const float (&sc)[kCt], int x) __attribute__((always_inline)) {
 #pragma unroll
       for (int s = 0; s < kCt; ++s) {
         const int r = (wave + 4 * s) * kCr + lane / kCp, c = lane % kCp;
-        const bool in = x * kBN + r < P && ks[s] != 0.f;
-        const uint32_t at = rawk + s * 4096 + lane * 16;
-        const u32x4 k8 = *(lds_u32x4*)(uintptr_t)at, v8 = *(lds_u32x4*)(uintptr_t)(at + kTile / 2);
+        const bool in = x * kBN + r < P && sc[s] != 0.f;
+        const u32x4 w = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t to = lds_at(sT) + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4);
-          const uint2 a = f8x4_to_bf16(k8[2 * e], ks[s]), b = f8x4_to_bf16(k8[2 * e + 1], ks[s]);
-          const uint2 y = f8x4_to_bf16(v8[2 * e], vs[s]), z = f8x4_to_bf16(v8[2 * e + 1], vs[s]);
-          *(lds_u32x4w*)(uintptr_t)to = in ? u32x4{a.x, a.y, b.x, b.y} : u32x4{0, 0, 0, 0};
-          *(lds_u32x4w*)(uintptr_t)(to + kTile) = in ? u32x4{y.x, y.y, z.x, z.y} : u32x4{0, 0, 0, 0};
+          const uint2 a = f8x4_to_bf16(w[2 * e], sc[s]), b = f8x4_to_bf16(w[2 * e + 1], sc[s]);
+          *(lds_u32x4w*)(uintptr_t)(lds_at(sT) + to + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4)) =
+              in ? u32x4{a.x, a.y, b.x, b.y} : u32x4{0, 0, 0, 0};
         }
       }
-      const unsigned long long now = held;
-      unsigned long long bad = 0;
-      // (rows that are not held are zeros; only a window hides a held row from some rows)
-      if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
-        bad = scrub([&](int i) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + lane / kCp) * 2 * D +
-                                        (((2 * (lane % kCp) + (i & 1)) ^ row_swz<D>((wave + 4 * (i >> 1)) * kCr + lane / kCp)) << 4); },
-                    2 * kCt);
-      lds_sync();
-      if (x + 1 < tiles) {
-        ids(x + 1);
-        fetch(x + 1);
-        held = __ballot(hid_id >= 0);
-      }
-      f32x16 s[kN2];
-      scores(0, s);
+    };
+    // Cap, bias and mask of tile x's scores; returns the hidden keys.
+    auto finish = [&](f32x16 (&s)[kN2], int x, unsigned long long now) __attribute__((always_inline)) -> unsigned {
       to_log2(s);
       unsigned hidden = 0;
-      const int j0 = x * kBN;
+      const int j0 = x * kBN, oh = opaque(lane) >> 5;
       if (now != ~0ull) {
 #pragma unroll
-        for (int i = 0; i < kS; i += 4) hidden |= ((unsigned)(~now >> key(i)) & 15u) << i;
+        for (int i = 0; i < kS; i += 4) hidden |= ((unsigned)(~now >> key(i, oh)) & 15u) << i;
       }
       if (p.c.pos && (p.slopes || p.window > 0)) {
         const int qpos = start + ti;
 #pragma unroll
         for (int i = 0; i < kS; i += 4) {
-          const int r = j0 + key(i), pg = r < P ? page_of(p.c, n, r) : -1;
+          const int r = j0 + key(i, oh), pg = r < P ? page_of(p.c, n, r) : -1;
           int4 kp = make_int4(qpos, qpos, qpos, qpos);
           if (pg >= 0) kp = *reinterpret_cast<const int4*>(p.c.pos + page_rows(p.c, pg, h) + (r & pmask));
 #pragma unroll
@@ -431,13 +451,95 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         if (p.slopes) bias(s, qrel);
         if (p.window > 0 && start + wz - j0 >= p.window) hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
       }
-      attend(0, s, hidden);
-      if (bad)
+      hide(s, hidden);
+      return hidden;
+    };
+    // K runs a tile ahead of V: idv, vs, vheld belong to tile x, idk, ks, kheld to x + 1.
+    int idk[kCt], idv[kCt], idn[kCt];
+    float ks[kCt], vs[kCt];
+    unsigned long long kheld;
+    auto ids = [&](int (&id)[kCt], int x) __attribute__((always_inline)) -> unsigned long long {
+#pragma unroll
+      for (int s = 0; s < kCt; ++s) id[s] = page_of(p.c, n, row_of(x, s));
+      const int r = x * kBN + lane;
+      return __ballot(r < P && page_of(p.c, n, r) >= 0);
+    };
+    if (x < tiles) {
+      kheld = ids(idv, x);
+      scales(p.c.k_scale, ks, idv);
+      fetch(p.c.k, raws, idv, x);
+      vm_wait();
+      convert(raws, 0, ks, x);
+      lds_sync();
+      fetch(p.c.v, raws + kTile / 2, idv, x);
+      scales(p.c.v_scale, vs, idv);
+      unsigned long long nheld = ids(idk, x + 1);       // (rows past the end are clamped)
+      scales(p.c.k_scale, ks, idk);
+      fetch(p.c.k, raws, idk, x + 1);
+      f32x16 s0[kN2], s1[kN2];
+      scores(0, s0);
+      unsigned hidden = finish(s0, x, kheld);
+      kheld = nheld;
+      raise(tile_max(s0));
+      nheld = ids(idn, x + 2);
+      auto top = [&](bool more) __attribute__((always_inline)) -> unsigned long long {
+        vm_wait();                                      // this wave's codes have landed
+        lds_sync();                                     // nobody reads the last tiles any more
+        convert(raws + kTile / 2, kTile, vs, x);
+        if (more) convert(raws, 0, ks, x + 1);
+        unsigned long long bad = 0;
+        // (rows that are not held are zeros; only a window hides a held row from some rows)
+        if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
+          bad = scrub([&](int i, int ln) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + ln / kCp) * 2 * D +
+                                                  (((2 * (ln % kCp) + (i & 1)) ^ row_swz<D>((wave + 4 * (i >> 1)) * kCr + ln / kCp)) << 4); },
+                      2 * kCt);
+        lds_sync();
+        return bad;
+      };
+      auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
         spill(bad, hidden, [&](int r, int col) {
-          const int row = min(j0 + r, P - 1), pg = max(page_of(p.c, n, row), 0);
+          const int row = min(x * kBN + r, P - 1), pg = max(page_of(p.c, n, row), 0);
           const uint32_t w4 = *reinterpret_cast<const uint32_t*>(p.c.v + (page_rows(p.c, pg, h) + (row & pmask)) * D + col);
           return f8x4_to_bf16(w4, 1.f);
         });
+      };
+      auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2]) __attribute__((always_inline)) {
+        const unsigned long long bad = top(true);
+        const unsigned long long now = kheld;
+        kheld = nheld;
+        unsigned hid2 = 0;
+        const auto load = [&](int i) __attribute__((always_inline)) {
+          if (i == 0) {
+            fetch(p.c.v, raws + kTile / 2, idk, x + 1);
+            scales(p.c.v_scale, vs, idk);
+          } else {
+            fetch(p.c.k, raws, idn, x + 2);
+            scales(p.c.k_scale, ks, idn);
+#pragma unroll
+            for (int s = 0; s < kCt; ++s) idk[s] = idn[s];
+            nheld = ids(idn, x + 3);
+          }
+        };
+        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x + 1, now); });
+        if (bad) dirty(bad);
+        hidden = hid2;
+        ++x;
+      };
+#pragma unroll 1
+      while (x + 1 < tiles) {
+        one(s0, s1);
+        if (x + 1 >= tiles) {
+#pragma unroll
+          for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
+          break;
+        }
+        one(s1, s0);
+      }
+      const unsigned long long bad = top(false);
+      weights(s0);
+      product(0u);
+      if (bad) dirty(bad);
+      vm_wait();                                        // (the last tile's spare loads)
     }
     lds_sync();
   }
@@ -494,75 +596,122 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   // r in LDS is the row's piece (l % kPc) ^ swizzle(r); rows past the sequence read as zeros.)
   const uint32_t kst = (uint32_t)p.k_stride * 2, vst = (uint32_t)p.v_stride * 2;   // bytes
   const uint32_t ldsw = uni(lds_at(sT) + wave * 1024);
-  auto fetch = [&](int t, uint32_t off) __attribute__((always_inline)) {
-    const int j0 = t * kBN, rows = min(kBN, L - j0);
-    const u32x4 bk = buffer_of(p.k + (int64_t)(t0 + j0) * p.k_stride + (int64_t)h * D, (rows - 1) * kst + 2 * D);
-    const u32x4 bv = buffer_of(p.v + (int64_t)(t0 + j0) * p.v_stride + (int64_t)h * D, (rows - 1) * vst + 2 * D);
+  const int fr = wave * kRpi + lane / kPc;              // row of the wave's first load; the next ones 4 kRpi further
+  const uint32_t fc = (uint32_t)((lane % kPc) ^ row_swz<D>(fr)) << 4;
+  auto fetch = [&](const char* src, uint32_t st, uint32_t row0, int t, uint32_t to) __attribute__((always_inline)) {
+    const int left = min(kBN, L - t * kBN);             // (none behind the last tile: zeros)
+    const u32x4 rs = buffer_of(src + (int64_t)(t * kBN) * st, left > 0 ? (left - 1) * st + 2 * D : 0);
 #pragma unroll
-    for (int s = 0; s < kLd; ++s) {
-      const int r = (wave + 4 * s) * kRpi + lane / kPc;
-      const uint32_t c = (uint32_t)((lane % kPc) ^ row_swz<D>(r)) << 4;
-      to_lds(bk, r * kst + c, ldsw + off + s * 4096);
-      to_lds(bv, r * vst + c, ldsw + off + kTile + s * 4096);
+    for (int s = 0; s < kLd; ++s)                       // (8 rows on, the swizzle's bit 1 flips)
+      to_lds(rs, row0 + s * (4 * kRpi * st) + (4 * kRpi * s & 8 ? fc ^ 32 : fc), ldsw + to + s * 4096);
+  };
+  const uint32_t rowk = fr * kst, rowv = fr * vst;
+  const char* const ksrc = (const char*)(p.k + (int64_t)t0 * p.k_stride + (int64_t)h * D);
+  const char* const vsrc = (const char*)(p.v + (int64_t)t0 * p.v_stride + (int64_t)h * D);
+  auto fetch_k = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(ksrc, kst, rowk, t, to); };
+  auto fetch_v = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(vsrc, vst, rowv, t, to + kTile); };
+  // Tiles [wf, wl) are seen whole by all rows of the wave, [gf, gl) by the workgroup's
+  // (documents aside): seen keys are a range, below the row's own or the prefix, inside the
+  // window.
+  auto whole = [&](int a, int z, int& from, int& to) __attribute__((always_inline)) {
+    int hi = min(max(a + 1, min(vis, L)), L);
+    from = 0;
+    if (p.window > 0) {
+      hi = (int)min((int64_t)hi, (int64_t)a + p.window);
+      from = (max(z - p.window + 1, 0) + kBN - 1) / kBN;
     }
+    to = hi / kBN;
+  };
+  int wf, wl, gf, gl;
+  whole(wa, wz, wf, wl);
+  whole(ta, tz, gf, gl);
+  auto all_of = [&](int t, int from, int to) __attribute__((always_inline)) {
+    return t >= from && t < to && (!doc || (doc_flags(t) & 2));
+  };
+  auto finish = [&](f32x16 (&s)[kN2], int t) __attribute__((always_inline)) -> unsigned {
+    const int j0 = t * kBN;
+    to_log2(s);
+    if (p.slopes) bias(s, ti - j0);
+    unsigned hidden = 0;
+    if (!all_of(t, wf, wl)) {
+      int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
+      if (p.window > 0) {
+        lo = ti - j0 - p.window + 1;
+        hi = min(hi, ti - j0 + p.window);
+      }
+      hidden = ~seen_bits(lo, hi);
+      if (doc) {                                        // the wave's own copy of the tile's ids
+        const int ol = opaque(lane), oh = ol >> 5, j = j0 + ol;
+        sIds[wave][ol] = j < L ? doc[j] : -1;
+        lds_order();
+#pragma unroll
+        for (int i = 0; i < kS; i += 4) {
+          const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i, oh)]);
+          if (di < 0 || dj.x != di) hidden |= 1u << i;
+          if (di < 0 || dj.y != di) hidden |= 2u << i;
+          if (di < 0 || dj.z != di) hidden |= 4u << i;
+          if (di < 0 || dj.w != di) hidden |= 8u << i;
+        }
+        lds_order();
+      }
+      hide(s, hidden);
+    }
+    return hidden;
   };
   int t = next(d0);
-  uint32_t off = 0;
-  if (t < d1) fetch(t, 0);
-#pragma unroll 1
-  while (t < d1) {
-    const int nx = next(t + 1);
-    vm_wait();                                          // this wave's share of the tile has landed
-    lds_sync();                                         // everyone's has, and nobody reads the other pair
-    if (nx < d1) fetch(nx, off ^ (2 * kTile));
-    const int j0 = t * kBN, je = j0 + kBN - 1;
-    // do these tokens' rows see all of the tile?  does the wave see any of it?
-    const bool one_doc = !doc || (doc_flags(t) & 2);
-    auto all_of = [&](int a, int z) __attribute__((always_inline)) {
-      return one_doc && je < L && (je <= a || je < vis) && (p.window == 0 || (z - j0 < p.window && je - a < p.window));
+  if (t < d1) {
+    int nx = next(t + 1), n2 = nx < d1 ? next(nx + 1) : nx;   // the tiles after t
+    fetch_k(t, 0);
+    vm_wait();
+    lds_sync();
+    fetch_v(t, 0);
+    fetch_k(nx, 2 * kTile);
+    f32x16 s0[kN2], s1[kN2];
+    scores(0, s0);
+    unsigned hidden = finish(s0, t);
+    raise(tile_max(s0));
+    // Tile t (scores in s, V `kV` bytes behind the first), the next one's K in the other pair.
+    auto top = [&](uint32_t kV) __attribute__((always_inline)) -> unsigned long long {
+      vm_wait();                                        // this wave's share has landed
+      lds_sync();                                       // everyone's has, and nobody reads the last tiles
+      if (all_of(t, gf, gl)) return 0;
+      return scrub([&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, kLd);
     };
-    const bool full = all_of(wa, wz);
-    const bool none = (j0 > wz && j0 >= vis) || (p.window > 0 && wa - je >= p.window);
-    unsigned long long bad = 0;
-    if (!all_of(ta, tz))
-      bad = scrub([&](int i) { return ldsw + off + kTile + i * 4096 + lane * 16; }, kLd);
-    if (!none) {
-      f32x16 s[kN2];
-      scores(off, s);
-      to_log2(s);
-      if (p.slopes) bias(s, ti - j0);
-      unsigned hidden = 0;
-      if (!full) {
-        // seen keys are a range: below the row's own or the prefix, inside the window
-        int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
-        if (p.window > 0) {
-          lo = ti - j0 - p.window + 1;
-          hi = min(hi, ti - j0 + p.window);
-        }
-        hidden = ~seen_bits(lo, hi);
-        if (doc) {                                      // the wave's own copy of the tile's ids
-          const int j = j0 + lane;
-          sIds[wave][lane] = j < L ? doc[j] : -1;
-          lds_order();
+    auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
+      spill(bad, hidden, [&](int r, int col) {
+        return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
+      });
+    };
+    auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], auto par) __attribute__((always_inline)) {
+      constexpr int kV = decltype(par)::value * 2 * kTile, kK = 2 * kTile - kV;
+      const unsigned long long bad = top(kV);
+      unsigned hid2 = 0;
+      const auto load = [&](int i) __attribute__((always_inline)) {
+        if (i == 0) fetch_k(n2, kV); else fetch_v(nx, kK);
+      };
+      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx); });
+      if (bad) dirty(bad);
+      hidden = hid2;
+      t = nx;
+      nx = n2;
+      n2 = n2 < d1 ? next(n2 + 1) : n2;
+    };
+    uint32_t off = 0;
+#pragma unroll 1
+    while (nx < d1) {
+      one(s0, s1, Par<0>{});
+      if (nx >= d1) {
+        off = 2 * kTile;
 #pragma unroll
-          for (int i = 0; i < kS; i += 4) {
-            const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i)]);
-            if (di < 0 || dj.x != di) hidden |= 1u << i;
-            if (di < 0 || dj.y != di) hidden |= 2u << i;
-            if (di < 0 || dj.z != di) hidden |= 4u << i;
-            if (di < 0 || dj.w != di) hidden |= 8u << i;
-          }
-          lds_order();
-        }
+        for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
+        break;
       }
-      attend(off, s, hidden);
-      if (bad)
-        spill(bad, hidden, [&](int r, int col) {
-          return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(j0 + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
-        });
+      one(s1, s0, Par<1>{});
     }
-    off ^= 2 * kTile;
-    t = nx;
+    const unsigned long long bad = top(off);
+    weights(s0);
+    product(off);
+    if (bad) dirty(bad);
   }
 
   l += __shfl_xor(l, 32, kWave);
