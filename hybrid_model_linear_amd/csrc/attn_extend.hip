@@ -86,11 +86,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   constexpr int kLd = kBN / kRpi / 4;      // loads per wave and tile
   constexpr int kKa = kU < 8 ? kU : 8, kVa = kDT < 4 ? kDT : 4;   // distinct operand addresses
   __shared__ __attribute__((aligned(1024))) unsigned char sT[4 * kTile];   // K, V, K, V
-  __shared__ unsigned sFlag[kFlags / 16];  // 2 bits per key tile: overlaps, all one document
-  __shared__ int sDoc[2];
+  __shared__ unsigned char sFlag[kFlags];  // per key tile: 1 overlaps the rows' documents, 2 is all of their one
+  __shared__ int sDoc[2], sOdd;
   __shared__ __attribute__((aligned(16))) int sIds[4][64];
   __shared__ unsigned sBad[2];             // rows of a tile that hold NaN or infinity
 
+  if (threadIdx.x == 0) sOdd = -1;         // (read after a barrier at least)
   const int tid = threadIdx.x, wave = (int)uni(threadIdx.x >> 6), lane = tid & 63, q32 = lane & 31, hh = lane >> 5;
   const int G = p.H / p.H_kv;
   // Heads fastest: consecutive workgroups go to the 8 XCDs in turn, so a head's tiles share
@@ -319,22 +320,26 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     for (int i = 0; i < kS; ++i)
       s[i >> 4][i & 15] -= slope * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
   };
+  typedef u16 u16x2 __attribute__((ext_vector_type(2)));
   // A masked weight is 0, and 0 times NaN or infinity would reach rows that do not see the
   // key.  In a tile that some row sees only in part, scrub() looks at the V pieces that this
   // thread wrote (or asked for), sets such values to zero in LDS and returns the rows that held any
   // (the same in every thread); after the product, spill() adds them to the rows that see
   // them, read again from where they came.
-  auto scrub = [&](auto piece_of, int pieces) __attribute__((always_inline)) -> unsigned long long {
-    bool odd = false;
+  auto scrub = [&](int tile, auto piece_of, auto count) __attribute__((always_inline)) -> unsigned long long {
+    constexpr int pieces = decltype(count)::value;
     const int ln = opaque(lane);
     auto piece = [&](int i) __attribute__((always_inline)) { return piece_of(i, ln); };
-#pragma unroll 1
+    u16x2 top = {0, 0};                                 // largest magnitude bits of each half word
+#pragma unroll
     for (int i = 0; i < pieces; ++i) {
       const u32x4 v = *(lds_u32x4*)(uintptr_t)piece(i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) odd = odd || (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+      for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[e] & 0x7fff7fffu));
     }
-    if (!__syncthreads_or(odd)) return 0;
+    if (__any(top.x >= 0x7f80 || top.y >= 0x7f80) && lane == 0) sOdd = tile;   // (each tile is looked at once)
+    lds_sync();
+    if ((int)uni((unsigned)sOdd) != tile) return 0;
     if (tid < 2) sBad[tid] = 0;
     __syncthreads();
 #pragma unroll 1
@@ -393,41 +398,77 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       const int64_t first = (int64_t)start + ta - p.window + 1;
       x = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
     }
-    // Row this lane's load s brings from tile x, clamped into the held rows; page ids are
-    // fetched two tiles ahead, scales one.
-    auto row_of = [&](int x, int s) __attribute__((always_inline)) {
-      return min(x * kBN + (wave + 4 * s) * kCr + lane / kCp, P - 1);
+    // A load brings 4, 8 or 16 rows of one page, so page ids, addresses and scales are the
+    // same in every lane of a wave.  Lane l holds id (-1: not there) and scales of page pb + l
+    // of the sequence, 64 pages at a time; a tile's are read out of the lanes.
+    int pb = 0, pid = -1;
+    float pks = 0.f, pvs = 0.f;
+    auto pages = [&](int first) __attribute__((always_inline)) {
+      pb = first;
+      const int j = first + lane;
+      pid = j < ((P + pmask) >> lg) ? page_of(p.c, n, (int)min((int64_t)j << lg, (int64_t)INT32_MAX)) : -1;
+      const int64_t at = (int64_t)max(pid, 0) * p.H_kv + h;
+      pks = p.c.k_scale[at];
+      pvs = p.c.v_scale[at];
     };
-    // Codes of a tile: K and V, kTile / 2 bytes each, behind the first K and V tiles.
-    const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);
-    auto fetch = [&](const uint8_t* src, uint32_t to, const int (&id)[kCt], int x) __attribute__((always_inline)) {
-#pragma unroll
-      for (int s = 0; s < kCt; ++s)
-        to_lds(src + (page_rows(p.c, max(id[s], 0), h) + (row_of(x, s) & pmask)) * D + 16 * (lane % kCp), to + s * 4096);
-    };
-    auto scales = [&](const float* src, float (&sc)[kCt], const int (&id)[kCt]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int s = 0; s < kCt; ++s) sc[s] = id[s] < 0 ? 0.f : src[(int64_t)id[s] * p.H_kv + h];   // (0: no row here)
-    };
-    auto convert = [&](uint32_t from, uint32_t to, const float (&sc)[kCt], int x) __attribute__((always_inline)) {
+    // Tile x's pages start at lane ...; the next block of pages is read once a tile (of the two
+    // that are ahead of tile x) passes the end.
+    auto lane_of = [&](int row) __attribute__((always_inline)) { return (row >> lg) - pb; };
+    const uint32_t rlane = (uint32_t)(lane / kCp) * D + 16 * (lane % kCp);   // this lane's piece of a load
+    const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K and V, kTile / 2 bytes each, behind the first tiles
+    auto fetch = [&](const uint8_t* src, uint32_t to, int x) __attribute__((always_inline)) {
 #pragma unroll
       for (int s = 0; s < kCt; ++s) {
-        const int r = (wave + 4 * s) * kCr + lane / kCp, c = lane % kCp;
-        const bool in = x * kBN + r < P && sc[s] != 0.f;
-        const u32x4 w = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
+        const int r = x * kBN + (wave + 4 * s) * kCr;
+        const int id = __builtin_amdgcn_readlane(pid, lane_of(r) & 63);
+        const u32x4 rs = buffer_of(src + ((((int64_t)max(id, 0) * p.H_kv + h) << lg) + (r & pmask)) * D, kCr * D);
+        to_lds(rs, rlane, to + s * 4096);
+      }
+    };
+    // Codes of tile x -> bf16 (rows that are not held -> zeros).
+    auto convert = [&](uint32_t from, uint32_t to, float lane_scale, int x) __attribute__((always_inline)) {
+      const int c = lane % kCp;
+#pragma unroll
+      for (int s = 0; s < kCt; ++s) {
+        const int r0 = (wave + 4 * s) * kCr, r = r0 + lane / kCp, pl = lane_of(x * kBN + r0) & 63;
+        const float sc = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(lane_scale), pl));
+        u32x4 w = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
+        if (x * kBN + kBN > P || __builtin_amdgcn_readlane(pid, pl) < 0) {
+          if (x * kBN + r >= P || __builtin_amdgcn_readlane(pid, pl) < 0) w = u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint2 a = f8x4_to_bf16(w[2 * e], sc[s]), b = f8x4_to_bf16(w[2 * e + 1], sc[s]);
+          const uint2 a = f8x4_to_bf16(w[2 * e], sc), b = f8x4_to_bf16(w[2 * e + 1], sc);
           *(lds_u32x4w*)(uintptr_t)(lds_at(sT) + to + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4)) =
-              in ? u32x4{a.x, a.y, b.x, b.y} : u32x4{0, 0, 0, 0};
+              u32x4{a.x, a.y, b.x, b.y};
         }
       }
     };
+    // Bit r: row x kBN + r is held.
+    auto held = [&](int x) __attribute__((always_inline)) -> unsigned long long {
+      unsigned long long bits = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                     // 16 rows lie on one page
+        const int left = P - x * kBN - 16 * i;
+        if (left > 0 && __builtin_amdgcn_readlane(pid, lane_of(x * kBN + 16 * i) & 63) >= 0)
+          bits |= (left >= 16 ? 0xffffull : (1ull << left) - 1) << 16 * i;
+      }
+      return bits;
+    };
     // Cap, bias and mask of tile x's scores; returns the hidden keys.
     auto finish = [&](f32x16 (&s)[kN2], int x, unsigned long long now) __attribute__((always_inline)) -> unsigned {
-      to_log2(s);
       unsigned hidden = 0;
       const int j0 = x * kBN, oh = opaque(lane) >> 5;
+      if (p.slopes && p.softcap == 0.f && !p.c.pos && start + ta >= j0 + kBN) {
+        // the tile lies before every row: one line, -slope (q - k)
+        const float b0 = -slope * (float)(start + ti - j0 - 4 * oh);
+#pragma unroll
+        for (int i = 0; i < kS; ++i)
+          s[i >> 4][i & 15] = fmaf(s[i >> 4][i & 15], c1, fmaf(slope, (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)), b0));
+      } else {
+        to_log2(s);
+        if (p.slopes && !p.c.pos) bias(s, start + ti - j0);
+      }
       if (now != ~0ull) {
 #pragma unroll
         for (int i = 0; i < kS; i += 4) hidden |= ((unsigned)(~now >> key(i, oh)) & 15u) << i;
@@ -446,53 +487,40 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
             if (p.window > 0 && dist >= p.window) hidden |= 1u << (i + e);
           }
         }
-      } else if (p.slopes || p.window > 0) {
+      } else if (p.window > 0 && start + wz - j0 >= p.window) {
         const int qrel = start + ti - j0;
-        if (p.slopes) bias(s, qrel);
-        if (p.window > 0 && start + wz - j0 >= p.window) hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
+        hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
       }
       hide(s, hidden);
       return hidden;
     };
-    // K runs a tile ahead of V: idv, vs, vheld belong to tile x, idk, ks, kheld to x + 1.
-    int idk[kCt], idv[kCt], idn[kCt];
-    float ks[kCt], vs[kCt];
-    unsigned long long kheld;
-    auto ids = [&](int (&id)[kCt], int x) __attribute__((always_inline)) -> unsigned long long {
-#pragma unroll
-      for (int s = 0; s < kCt; ++s) id[s] = page_of(p.c, n, row_of(x, s));
-      const int r = x * kBN + lane;
-      return __ballot(r < P && page_of(p.c, n, r) >= 0);
-    };
     if (x < tiles) {
-      kheld = ids(idv, x);
-      scales(p.c.k_scale, ks, idv);
-      fetch(p.c.k, raws, idv, x);
+      // K runs a tile ahead of V; x + 2 is the furthest tile whose pages are looked at
+      auto ahead = [&](int x) __attribute__((always_inline)) {
+        if (lane_of(min((x + 3) * kBN, P) - 1) >= kWave) pages((x * kBN) >> lg);
+      };
+      pages((x * kBN) >> lg);
+      fetch(p.c.k, raws, x);
       vm_wait();
-      convert(raws, 0, ks, x);
+      convert(raws, 0, pks, x);
       lds_sync();
-      fetch(p.c.v, raws + kTile / 2, idv, x);
-      scales(p.c.v_scale, vs, idv);
-      unsigned long long nheld = ids(idk, x + 1);       // (rows past the end are clamped)
-      scales(p.c.k_scale, ks, idk);
-      fetch(p.c.k, raws, idk, x + 1);
+      fetch(p.c.v, raws + kTile / 2, x);
+      fetch(p.c.k, raws, min(x + 1, tiles - 1));
       f32x16 s0[kN2], s1[kN2];
       scores(0, s0);
-      unsigned hidden = finish(s0, x, kheld);
-      kheld = nheld;
+      unsigned hidden = finish(s0, x, held(x));
       raise(tile_max(s0));
-      nheld = ids(idn, x + 2);
       auto top = [&](bool more) __attribute__((always_inline)) -> unsigned long long {
         vm_wait();                                      // this wave's codes have landed
         lds_sync();                                     // nobody reads the last tiles any more
-        convert(raws + kTile / 2, kTile, vs, x);
-        if (more) convert(raws, 0, ks, x + 1);
+        convert(raws + kTile / 2, kTile, pvs, x);
+        if (more) convert(raws, 0, pks, x + 1);
         unsigned long long bad = 0;
         // (rows that are not held are zeros; only a window hides a held row from some rows)
         if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
-          bad = scrub([&](int i, int ln) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + ln / kCp) * 2 * D +
+          bad = scrub(-2 - x, [&](int i, int ln) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + ln / kCp) * 2 * D +
                                                   (((2 * (ln % kCp) + (i & 1)) ^ row_swz<D>((wave + 4 * (i >> 1)) * kCr + ln / kCp)) << 4); },
-                      2 * kCt);
+                      Par<2 * kCt>{});
         lds_sync();
         return bad;
       };
@@ -505,22 +533,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       };
       auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2]) __attribute__((always_inline)) {
         const unsigned long long bad = top(true);
-        const unsigned long long now = kheld;
-        kheld = nheld;
         unsigned hid2 = 0;
+        ahead(x);
         const auto load = [&](int i) __attribute__((always_inline)) {
-          if (i == 0) {
-            fetch(p.c.v, raws + kTile / 2, idk, x + 1);
-            scales(p.c.v_scale, vs, idk);
-          } else {
-            fetch(p.c.k, raws, idn, x + 2);
-            scales(p.c.k_scale, ks, idn);
-#pragma unroll
-            for (int s = 0; s < kCt; ++s) idk[s] = idn[s];
-            nheld = ids(idn, x + 3);
-          }
+          if (i == 0) fetch(p.c.v, raws + kTile / 2, x + 1); else fetch(p.c.k, raws, min(x + 2, tiles - 1));
         };
-        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x + 1, now); });
+        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x + 1, held(x + 1)); });
         if (bad) dirty(bad);
         hidden = hid2;
         ++x;
@@ -552,21 +570,25 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     last = (int)min((int64_t)last, (int64_t)tz + p.window);
   }
   const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
-  // Document mask: which key tiles hold a document of this workgroup's rows, a wave per tile.
+  // Document mask: which key tiles hold a document of this workgroup's rows, a wave per
+  // tile.  (Rows with a negative id see nothing: they take part as they come and give
+  // zeros in the end.)
   if (doc) {
-    for (int i = tid; i < kFlags / 16; i += kExtThreads) sFlag[i] = 0;
     if (tid == 0) {
       sDoc[0] = INT32_MAX;
-      sDoc[1] = INT32_MIN;
+      sDoc[1] = -1;
     }
     __syncthreads();
     for (int t = ta + tid; t <= tz; t += kExtThreads) {
-      atomicMin(&sDoc[0], doc[t]);
-      atomicMax(&sDoc[1], doc[t]);
+      const int d = doc[t];
+      if (d >= 0) {
+        atomicMin(&sDoc[0], d);
+        atomicMax(&sDoc[1], d);
+      }
     }
     __syncthreads();
     const int dmin = sDoc[0], dmax = sDoc[1], lim = min(d1, d0 + kFlags);
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     for (int t = d0 + wave * kAhead; t < lim; t += 4 * kAhead) {
       int v[kAhead];
 #pragma unroll
@@ -577,19 +599,34 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const bool any = __any(v[i] >= 0 && v[i] >= dmin && v[i] <= dmax);
-        const bool all = dmin == dmax && __all(v[i] >= 0 && v[i] == dmin);
-        if (lane == 0 && t + i < lim)
-          atomicOr(&sFlag[(t + i - d0) >> 4], (any ? 1u : 0u) << 2 * ((t + i - d0) & 15) | (all ? 2u : 0u) << 2 * ((t + i - d0) & 15));
+        const bool all = dmin == dmax && __all(v[i] == dmin);
+        if (lane == 0 && t + i < lim) sFlag[t + i - d0] = (any ? 1 : 0) | (all ? 2 : 0);
       }
     }
     __syncthreads();
   }
-  auto doc_flags = [&](int t) __attribute__((always_inline)) -> unsigned {
-    return t - d0 < kFlags ? uni(sFlag[(t - d0) >> 4]) >> 2 * ((t - d0) & 15) & 3 : 1u;
-  };
-  auto next = [&](int t) __attribute__((always_inline)) {   // the next tile at or after t to look at
-    if (doc)
-      while (t < d1 && !(doc_flags(t) & 1)) ++t;
+  // The next tile at or after t to look at, and whether it is all of the rows' one document:
+  // flags of 64 tiles from fb on are held as bits.  (Tiles past the table are looked at.)
+  int fb = -kWave;
+  unsigned long long fany = 0, fall = 0;
+  auto next = [&](int t, bool& all) __attribute__((always_inline)) {
+    all = true;
+    if (!doc) return t;
+    while (t < d1) {
+      if (t >= fb + kWave) {
+        fb = t;
+        const int i = t - d0 + lane, flag = t + lane < d1 ? (i < kFlags ? (int)sFlag[i] : 1) : 0;
+        fany = __ballot(flag & 1);
+        fall = __ballot(flag & 2);
+      }
+      const unsigned long long left = fany >> (t - fb);
+      if (left) {
+        t += __builtin_ctzll(left);
+        all = fall >> (t - fb) & 1;
+        return t;
+      }
+      t = fb + kWave;
+    }
     return t;
   };
   // Loads of tile t: this lane's piece of each of the wave's loads.  (Piece l % kPc of row
@@ -625,32 +662,29 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   int wf, wl, gf, gl;
   whole(wa, wz, wf, wl);
   whole(ta, tz, gf, gl);
-  auto all_of = [&](int t, int from, int to) __attribute__((always_inline)) {
-    return t >= from && t < to && (!doc || (doc_flags(t) & 2));
-  };
-  auto finish = [&](f32x16 (&s)[kN2], int t) __attribute__((always_inline)) -> unsigned {
+  auto finish = [&](f32x16 (&s)[kN2], int t, bool all) __attribute__((always_inline)) -> unsigned {
     const int j0 = t * kBN;
     to_log2(s);
     if (p.slopes) bias(s, ti - j0);
     unsigned hidden = 0;
-    if (!all_of(t, wf, wl)) {
+    if (t < wf || t >= wl || !all) {
       int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
       if (p.window > 0) {
         lo = ti - j0 - p.window + 1;
         hi = min(hi, ti - j0 + p.window);
       }
       hidden = ~seen_bits(lo, hi);
-      if (doc) {                                        // the wave's own copy of the tile's ids
+      if (!all) {                                       // the wave's own copy of the tile's ids
         const int ol = opaque(lane), oh = ol >> 5, j = j0 + ol;
         sIds[wave][ol] = j < L ? doc[j] : -1;
         lds_order();
 #pragma unroll
         for (int i = 0; i < kS; i += 4) {
           const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i, oh)]);
-          if (di < 0 || dj.x != di) hidden |= 1u << i;
-          if (di < 0 || dj.y != di) hidden |= 2u << i;
-          if (di < 0 || dj.z != di) hidden |= 4u << i;
-          if (di < 0 || dj.w != di) hidden |= 8u << i;
+          if (dj.x != di) hidden |= 1u << i;
+          if (dj.y != di) hidden |= 2u << i;
+          if (dj.z != di) hidden |= 4u << i;
+          if (dj.w != di) hidden |= 8u << i;
         }
         lds_order();
       }
@@ -658,9 +692,10 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     }
     return hidden;
   };
-  int t = next(d0);
+  bool all_t, all_x, all_2;                                      // (all of one document: tiles t, nx, n2)
+  int t = next(d0, all_t);
   if (t < d1) {
-    int nx = next(t + 1), n2 = nx < d1 ? next(nx + 1) : nx;   // the tiles after t
+    int nx = next(t + 1, all_x), n2 = next(nx + 1, all_2);    // the tiles after t
     fetch_k(t, 0);
     vm_wait();
     lds_sync();
@@ -668,14 +703,14 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     fetch_k(nx, 2 * kTile);
     f32x16 s0[kN2], s1[kN2];
     scores(0, s0);
-    unsigned hidden = finish(s0, t);
+    unsigned hidden = finish(s0, t, all_t);
     raise(tile_max(s0));
     // Tile t (scores in s, V `kV` bytes behind the first), the next one's K in the other pair.
     auto top = [&](uint32_t kV) __attribute__((always_inline)) -> unsigned long long {
       vm_wait();                                        // this wave's share has landed
       lds_sync();                                       // everyone's has, and nobody reads the last tiles
-      if (all_of(t, gf, gl)) return 0;
-      return scrub([&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, kLd);
+      if (t >= gf && t < gl && all_t) return 0;
+      return scrub(t, [&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, Par<kLd>{});
     };
     auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
       spill(bad, hidden, [&](int r, int col) {
@@ -689,12 +724,14 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       const auto load = [&](int i) __attribute__((always_inline)) {
         if (i == 0) fetch_k(n2, kV); else fetch_v(nx, kK);
       };
-      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx); });
+      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx, all_x); });
       if (bad) dirty(bad);
       hidden = hid2;
       t = nx;
+      all_t = all_x;
       nx = n2;
-      n2 = n2 < d1 ? next(n2 + 1) : n2;
+      all_x = all_2;
+      n2 = next(n2 + 1, all_2);
     };
     uint32_t off = 0;
 #pragma unroll 1
@@ -716,7 +753,14 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
-  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // nothing seen: zeros; a NaN sum stays NaN
+  float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // nothing seen: zeros; a NaN sum stays NaN
+  if (doc && di < 0) {                                  // a row outside of all documents
+    inv = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+  }
   u16* at = p.out + (int64_t)(t0 + ti) * p.out_stride + (int64_t)hq * D;
 #pragma unroll
   for (int d = 0; d < kDT; ++d)
