@@ -25,6 +25,8 @@
 // time each with hardly any overlap, even with two workgroups on a CU: 944 TFLOP/s at
 // 8 x 4096 tokens, 32 / 8 heads, d = 128.)  Up to d = 128 two workgroups fit a CU; at d =
 // 256 one does (its output alone takes 128 registers).
+// Keys are taken from the last to the first, the new tokens before the cached: with a
+// distance bias the nearest keys set the maximum at once and the sums are not rescaled again.
 // The weights are rounded to bf16 for the second product, their sum is not.
 #include "attn_common.h"
 
@@ -387,16 +389,206 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     }
   };
 
+  // ---------------------------------------------------------------- new tokens
+  int last = min(L, max(tz + 1, min(vis, L)));          // keys [first, last) are seen by some row
+  int first = 0;
+  if (p.window > 0) {
+    first = (int)max((int64_t)0, (int64_t)ta - p.window + 1);
+    last = (int)min((int64_t)last, (int64_t)tz + p.window);
+  }
+  const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
+  // Document mask: which key tiles hold a document of this workgroup's rows, a wave per
+  // tile.  (Rows with a negative id see nothing: they take part as they come and give
+  // zeros in the end.)
+  if (doc) {
+    if (tid == 0) {
+      sDoc[0] = INT32_MAX;
+      sDoc[1] = -1;
+    }
+    __syncthreads();
+    for (int t = ta + tid; t <= tz; t += kExtThreads) {
+      const int d = doc[t];
+      if (d >= 0) {
+        atomicMin(&sDoc[0], d);
+        atomicMax(&sDoc[1], d);
+      }
+    }
+    __syncthreads();
+    const int dmin = sDoc[0], dmax = sDoc[1], lim = min(d1 - d0, kFlags);
+    constexpr int kAhead = 8;
+    for (int y = wave * kAhead; y < lim; y += 4 * kAhead) {
+      int v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = (d1 - 1 - y - i) * kBN + lane;
+        v[i] = j >= 0 && j < L ? doc[j] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const bool any = __any(v[i] >= 0 && v[i] >= dmin && v[i] <= dmax);
+        const bool all = dmin == dmax && __all(v[i] == dmin);
+        if (lane == 0 && y + i < lim) sFlag[y + i] = (any ? 1 : 0) | (all ? 2 : 0);
+      }
+    }
+    __syncthreads();
+  }
+  // The next tile at or before t to look at, and whether it is all of the rows' one document:
+  // flags of the 64 tiles from fb down are held as bits.  (Tiles past the table are looked at.)
+  int fb = INT32_MAX;
+  unsigned long long fany = 0, fall = 0;
+  auto next = [&](int t, bool& all) __attribute__((always_inline)) {
+    all = true;
+    if (!doc) return t;
+    while (t >= d0) {
+      if (t <= fb - kWave) {
+        fb = t;
+        const int i = d1 - 1 - t + lane, flag = t - lane >= d0 ? (i < kFlags ? (int)sFlag[i] : 1) : 0;
+        fany = __ballot(flag & 1);
+        fall = __ballot(flag & 2);
+      }
+      const unsigned long long left = fany >> (fb - t);
+      if (left) {
+        t -= __builtin_ctzll(left);
+        all = fall >> (fb - t) & 1;
+        return t;
+      }
+      t = fb - kWave;
+    }
+    return t;
+  };
+  // Loads of tile t: this lane's piece of each of the wave's loads.  (Piece l % kPc of row
+  // r in LDS is the row's piece (l % kPc) ^ swizzle(r); rows past the sequence read as zeros.)
+  const uint32_t kst = (uint32_t)p.k_stride * 2, vst = (uint32_t)p.v_stride * 2;   // bytes
+  const uint32_t ldsw = uni(lds_at(sT) + wave * 1024);
+  const int fr = wave * kRpi + lane / kPc;              // row of the wave's first load; the next ones 4 kRpi further
+  const uint32_t fc = (uint32_t)((lane % kPc) ^ row_swz<D>(fr)) << 4;
+  auto fetch = [&](const char* src, uint32_t st, uint32_t row0, int t, uint32_t to) __attribute__((always_inline)) {
+    const int left = t >= d0 ? min(kBN, L - t * kBN) : 0;   // (behind the last tile nothing: zeros)
+    const u32x4 rs = buffer_of(src + (int64_t)(t * kBN) * st, left > 0 ? (left - 1) * st + 2 * D : 0);
+#pragma unroll
+    for (int s = 0; s < kLd; ++s)                       // (8 rows on, the swizzle's bit 1 flips)
+      to_lds(rs, row0 + s * (4 * kRpi * st) + (4 * kRpi * s & 8 ? fc ^ 32 : fc), ldsw + to + s * 4096);
+  };
+  const uint32_t rowk = fr * kst, rowv = fr * vst;
+  const char* const ksrc = (const char*)(p.k + (int64_t)t0 * p.k_stride + (int64_t)h * D);
+  const char* const vsrc = (const char*)(p.v + (int64_t)t0 * p.v_stride + (int64_t)h * D);
+  auto fetch_k = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(ksrc, kst, rowk, t, to); };
+  auto fetch_v = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(vsrc, vst, rowv, t, to + kTile); };
+  // Tiles [wf, wl) are seen whole by all rows of the wave, [gf, gl) by the workgroup's
+  // (documents aside): seen keys are a range, below the row's own or the prefix, inside the
+  // window.
+  auto whole = [&](int a, int z, int& from, int& to) __attribute__((always_inline)) {
+    int hi = min(max(a + 1, min(vis, L)), L);
+    from = 0;
+    if (p.window > 0) {
+      hi = (int)min((int64_t)hi, (int64_t)a + p.window);
+      from = (max(z - p.window + 1, 0) + kBN - 1) / kBN;
+    }
+    to = hi / kBN;
+  };
+  int wf, wl, gf, gl;
+  whole(wa, wz, wf, wl);
+  whole(ta, tz, gf, gl);
+  auto finish = [&](f32x16 (&s)[kN2], int t, bool all) __attribute__((always_inline)) -> unsigned {
+    const int j0 = t * kBN;
+    to_log2(s);
+    if (p.slopes) bias(s, ti - j0);
+    unsigned hidden = 0;
+    if (t < wf || t >= wl || !all) {
+      int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
+      if (p.window > 0) {
+        lo = ti - j0 - p.window + 1;
+        hi = min(hi, ti - j0 + p.window);
+      }
+      hidden = ~seen_bits(lo, hi);
+      if (!all) {                                       // the wave's own copy of the tile's ids
+        const int ol = opaque(lane), oh = ol >> 5, j = j0 + ol;
+        sIds[wave][ol] = j < L ? doc[j] : -1;
+        lds_order();
+#pragma unroll
+        for (int i = 0; i < kS; i += 4) {
+          const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i, oh)]);
+          if (dj.x != di) hidden |= 1u << i;
+          if (dj.y != di) hidden |= 2u << i;
+          if (dj.z != di) hidden |= 4u << i;
+          if (dj.w != di) hidden |= 8u << i;
+        }
+        lds_order();
+      }
+      hide(s, hidden);
+    }
+    return hidden;
+  };
+  bool all_t, all_x, all_2;                                      // (all of one document: tiles t, nx, n2)
+  int t = next(d1 - 1, all_t);
+  if (t >= d0) {
+    int nx = next(t - 1, all_x), n2 = next(nx - 1, all_2);    // the tiles after t
+    fetch_k(t, 0);
+    vm_wait();
+    lds_sync();
+    fetch_v(t, 0);
+    fetch_k(nx, 2 * kTile);
+    f32x16 s0[kN2], s1[kN2];
+    scores(0, s0);
+    unsigned hidden = finish(s0, t, all_t);
+    raise(tile_max(s0));
+    // Tile t (scores in s, V `kV` bytes behind the first), the next one's K in the other pair.
+    auto top = [&](uint32_t kV) __attribute__((always_inline)) -> unsigned long long {
+      vm_wait();                                        // this wave's share has landed
+      lds_sync();                                       // everyone's has, and nobody reads the last tiles
+      if (t >= gf && t < gl && all_t) return 0;
+      return scrub(t, [&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, Par<kLd>{});
+    };
+    auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
+      spill(bad, hidden, [&](int r, int col) {
+        return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
+      });
+    };
+    auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], auto par) __attribute__((always_inline)) {
+      constexpr int kV = decltype(par)::value * 2 * kTile, kK = 2 * kTile - kV;
+      const unsigned long long bad = top(kV);
+      unsigned hid2 = 0;
+      const auto load = [&](int i) __attribute__((always_inline)) {
+        if (i == 0) fetch_k(n2, kV); else fetch_v(nx, kK);
+      };
+      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx, all_x); });
+      if (bad) dirty(bad);
+      hidden = hid2;
+      t = nx;
+      all_t = all_x;
+      nx = n2;
+      all_x = all_2;
+      n2 = next(n2 - 1, all_2);
+    };
+    uint32_t off = 0;
+#pragma unroll 1
+    while (nx >= d0) {
+      one(s0, s1, Par<0>{});
+      if (nx < d0) {
+        off = 2 * kTile;
+#pragma unroll
+        for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
+        break;
+      }
+      one(s1, s0, Par<1>{});
+    }
+    const unsigned long long bad = top(off);
+    weights(s0);
+    product(off);
+    if (bad) dirty(bad);
+  }
+
   // ---------------------------------------------------------------- cached rows
   if constexpr (CACHED) {
+    lds_sync();                                         // the new tokens' tiles are read
     constexpr int kCp = D / 16;                         // 16-code pieces of a row
     constexpr int kCr = kWave / kCp;                    // rows that one wave's load brings
     constexpr int kCt = kBN / kCr / 4;                  // loads per wave and tile
     const int tiles = (P + kBN - 1) / kBN;
-    int x = 0;
+    int x0 = 0, x = tiles - 1;                          // tiles x, x - 1, ... x0
     if (p.window > 0 && !p.c.pos) {                     // rows that a window leaves out for every row
       const int64_t first = (int64_t)start + ta - p.window + 1;
-      x = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
+      x0 = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
     }
     // A load brings 4, 8 or 16 rows of one page, so page ids, addresses and scales are the
     // same in every lane of a wave.  Lane l holds id (-1: not there) and scales of page pb + l
@@ -411,8 +603,6 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       pks = p.c.k_scale[at];
       pvs = p.c.v_scale[at];
     };
-    // Tile x's pages start at lane ...; the next block of pages is read once a tile (of the two
-    // that are ahead of tile x) passes the end.
     auto lane_of = [&](int row) __attribute__((always_inline)) { return (row >> lg) - pb; };
     const uint32_t rlane = (uint32_t)(lane / kCp) * D + 16 * (lane % kCp);   // this lane's piece of a load
     const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K and V, kTile / 2 bytes each, behind the first tiles
@@ -494,18 +684,19 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       hide(s, hidden);
       return hidden;
     };
-    if (x < tiles) {
-      // K runs a tile ahead of V; x + 2 is the furthest tile whose pages are looked at
+    if (x >= x0) {
+      // K runs a tile ahead of V; x - 2 is the furthest tile whose pages are looked at
+      auto block = [&](int x) __attribute__((always_inline)) { pages(max(((x * kBN + kBN - 1) >> lg) - (kWave - 1), 0)); };
       auto ahead = [&](int x) __attribute__((always_inline)) {
-        if (lane_of(min((x + 3) * kBN, P) - 1) >= kWave) pages((x * kBN) >> lg);
+        if (lane_of(max(x - 2, x0) * kBN) < 0) block(x);
       };
-      pages((x * kBN) >> lg);
+      block(x);
       fetch(p.c.k, raws, x);
       vm_wait();
       convert(raws, 0, pks, x);
       lds_sync();
       fetch(p.c.v, raws + kTile / 2, x);
-      fetch(p.c.k, raws, min(x + 1, tiles - 1));
+      fetch(p.c.k, raws, max(x - 1, x0));
       f32x16 s0[kN2], s1[kN2];
       scores(0, s0);
       unsigned hidden = finish(s0, x, held(x));
@@ -514,7 +705,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         vm_wait();                                      // this wave's codes have landed
         lds_sync();                                     // nobody reads the last tiles any more
         convert(raws + kTile / 2, kTile, pvs, x);
-        if (more) convert(raws, 0, pks, x + 1);
+        if (more) convert(raws, 0, pks, x - 1);
         unsigned long long bad = 0;
         // (rows that are not held are zeros; only a window hides a held row from some rows)
         if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
@@ -536,17 +727,17 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         unsigned hid2 = 0;
         ahead(x);
         const auto load = [&](int i) __attribute__((always_inline)) {
-          if (i == 0) fetch(p.c.v, raws + kTile / 2, x + 1); else fetch(p.c.k, raws, min(x + 2, tiles - 1));
+          if (i == 0) fetch(p.c.v, raws + kTile / 2, x - 1); else fetch(p.c.k, raws, max(x - 2, x0));
         };
-        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x + 1, held(x + 1)); });
+        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x - 1, held(x - 1)); });
         if (bad) dirty(bad);
         hidden = hid2;
-        ++x;
+        --x;
       };
 #pragma unroll 1
-      while (x + 1 < tiles) {
+      while (x > x0) {
         one(s0, s1);
-        if (x + 1 >= tiles) {
+        if (x <= x0) {
 #pragma unroll
           for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
           break;
@@ -559,196 +750,6 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       if (bad) dirty(bad);
       vm_wait();                                        // (the last tile's spare loads)
     }
-    lds_sync();
-  }
-
-  // ---------------------------------------------------------------- new tokens
-  int last = min(L, max(tz + 1, min(vis, L)));          // keys [first, last) are seen by some row
-  int first = 0;
-  if (p.window > 0) {
-    first = (int)max((int64_t)0, (int64_t)ta - p.window + 1);
-    last = (int)min((int64_t)last, (int64_t)tz + p.window);
-  }
-  const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
-  // Document mask: which key tiles hold a document of this workgroup's rows, a wave per
-  // tile.  (Rows with a negative id see nothing: they take part as they come and give
-  // zeros in the end.)
-  if (doc) {
-    if (tid == 0) {
-      sDoc[0] = INT32_MAX;
-      sDoc[1] = -1;
-    }
-    __syncthreads();
-    for (int t = ta + tid; t <= tz; t += kExtThreads) {
-      const int d = doc[t];
-      if (d >= 0) {
-        atomicMin(&sDoc[0], d);
-        atomicMax(&sDoc[1], d);
-      }
-    }
-    __syncthreads();
-    const int dmin = sDoc[0], dmax = sDoc[1], lim = min(d1, d0 + kFlags);
-    constexpr int kAhead = 8;
-    for (int t = d0 + wave * kAhead; t < lim; t += 4 * kAhead) {
-      int v[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = (t + i) * kBN + lane;
-        v[i] = j < L ? doc[j] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const bool any = __any(v[i] >= 0 && v[i] >= dmin && v[i] <= dmax);
-        const bool all = dmin == dmax && __all(v[i] == dmin);
-        if (lane == 0 && t + i < lim) sFlag[t + i - d0] = (any ? 1 : 0) | (all ? 2 : 0);
-      }
-    }
-    __syncthreads();
-  }
-  // The next tile at or after t to look at, and whether it is all of the rows' one document:
-  // flags of 64 tiles from fb on are held as bits.  (Tiles past the table are looked at.)
-  int fb = -kWave;
-  unsigned long long fany = 0, fall = 0;
-  auto next = [&](int t, bool& all) __attribute__((always_inline)) {
-    all = true;
-    if (!doc) return t;
-    while (t < d1) {
-      if (t >= fb + kWave) {
-        fb = t;
-        const int i = t - d0 + lane, flag = t + lane < d1 ? (i < kFlags ? (int)sFlag[i] : 1) : 0;
-        fany = __ballot(flag & 1);
-        fall = __ballot(flag & 2);
-      }
-      const unsigned long long left = fany >> (t - fb);
-      if (left) {
-        t += __builtin_ctzll(left);
-        all = fall >> (t - fb) & 1;
-        return t;
-      }
-      t = fb + kWave;
-    }
-    return t;
-  };
-  // Loads of tile t: this lane's piece of each of the wave's loads.  (Piece l % kPc of row
-  // r in LDS is the row's piece (l % kPc) ^ swizzle(r); rows past the sequence read as zeros.)
-  const uint32_t kst = (uint32_t)p.k_stride * 2, vst = (uint32_t)p.v_stride * 2;   // bytes
-  const uint32_t ldsw = uni(lds_at(sT) + wave * 1024);
-  const int fr = wave * kRpi + lane / kPc;              // row of the wave's first load; the next ones 4 kRpi further
-  const uint32_t fc = (uint32_t)((lane % kPc) ^ row_swz<D>(fr)) << 4;
-  auto fetch = [&](const char* src, uint32_t st, uint32_t row0, int t, uint32_t to) __attribute__((always_inline)) {
-    const int left = min(kBN, L - t * kBN);             // (none behind the last tile: zeros)
-    const u32x4 rs = buffer_of(src + (int64_t)(t * kBN) * st, left > 0 ? (left - 1) * st + 2 * D : 0);
-#pragma unroll
-    for (int s = 0; s < kLd; ++s)                       // (8 rows on, the swizzle's bit 1 flips)
-      to_lds(rs, row0 + s * (4 * kRpi * st) + (4 * kRpi * s & 8 ? fc ^ 32 : fc), ldsw + to + s * 4096);
-  };
-  const uint32_t rowk = fr * kst, rowv = fr * vst;
-  const char* const ksrc = (const char*)(p.k + (int64_t)t0 * p.k_stride + (int64_t)h * D);
-  const char* const vsrc = (const char*)(p.v + (int64_t)t0 * p.v_stride + (int64_t)h * D);
-  auto fetch_k = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(ksrc, kst, rowk, t, to); };
-  auto fetch_v = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(vsrc, vst, rowv, t, to + kTile); };
-  // Tiles [wf, wl) are seen whole by all rows of the wave, [gf, gl) by the workgroup's
-  // (documents aside): seen keys are a range, below the row's own or the prefix, inside the
-  // window.
-  auto whole = [&](int a, int z, int& from, int& to) __attribute__((always_inline)) {
-    int hi = min(max(a + 1, min(vis, L)), L);
-    from = 0;
-    if (p.window > 0) {
-      hi = (int)min((int64_t)hi, (int64_t)a + p.window);
-      from = (max(z - p.window + 1, 0) + kBN - 1) / kBN;
-    }
-    to = hi / kBN;
-  };
-  int wf, wl, gf, gl;
-  whole(wa, wz, wf, wl);
-  whole(ta, tz, gf, gl);
-  auto finish = [&](f32x16 (&s)[kN2], int t, bool all) __attribute__((always_inline)) -> unsigned {
-    const int j0 = t * kBN;
-    to_log2(s);
-    if (p.slopes) bias(s, ti - j0);
-    unsigned hidden = 0;
-    if (t < wf || t >= wl || !all) {
-      int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
-      if (p.window > 0) {
-        lo = ti - j0 - p.window + 1;
-        hi = min(hi, ti - j0 + p.window);
-      }
-      hidden = ~seen_bits(lo, hi);
-      if (!all) {                                       // the wave's own copy of the tile's ids
-        const int ol = opaque(lane), oh = ol >> 5, j = j0 + ol;
-        sIds[wave][ol] = j < L ? doc[j] : -1;
-        lds_order();
-#pragma unroll
-        for (int i = 0; i < kS; i += 4) {
-          const int4 dj = *reinterpret_cast<const int4*>(&sIds[wave][key(i, oh)]);
-          if (dj.x != di) hidden |= 1u << i;
-          if (dj.y != di) hidden |= 2u << i;
-          if (dj.z != di) hidden |= 4u << i;
-          if (dj.w != di) hidden |= 8u << i;
-        }
-        lds_order();
-      }
-      hide(s, hidden);
-    }
-    return hidden;
-  };
-  bool all_t, all_x, all_2;                                      // (all of one document: tiles t, nx, n2)
-  int t = next(d0, all_t);
-  if (t < d1) {
-    int nx = next(t + 1, all_x), n2 = next(nx + 1, all_2);    // the tiles after t
-    fetch_k(t, 0);
-    vm_wait();
-    lds_sync();
-    fetch_v(t, 0);
-    fetch_k(nx, 2 * kTile);
-    f32x16 s0[kN2], s1[kN2];
-    scores(0, s0);
-    unsigned hidden = finish(s0, t, all_t);
-    raise(tile_max(s0));
-    // Tile t (scores in s, V `kV` bytes behind the first), the next one's K in the other pair.
-    auto top = [&](uint32_t kV) __attribute__((always_inline)) -> unsigned long long {
-      vm_wait();                                        // this wave's share has landed
-      lds_sync();                                       // everyone's has, and nobody reads the last tiles
-      if (t >= gf && t < gl && all_t) return 0;
-      return scrub(t, [&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, Par<kLd>{});
-    };
-    auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
-      spill(bad, hidden, [&](int r, int col) {
-        return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
-      });
-    };
-    auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], auto par) __attribute__((always_inline)) {
-      constexpr int kV = decltype(par)::value * 2 * kTile, kK = 2 * kTile - kV;
-      const unsigned long long bad = top(kV);
-      unsigned hid2 = 0;
-      const auto load = [&](int i) __attribute__((always_inline)) {
-        if (i == 0) fetch_k(n2, kV); else fetch_v(nx, kK);
-      };
-      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx, all_x); });
-      if (bad) dirty(bad);
-      hidden = hid2;
-      t = nx;
-      all_t = all_x;
-      nx = n2;
-      all_x = all_2;
-      n2 = next(n2 + 1, all_2);
-    };
-    uint32_t off = 0;
-#pragma unroll 1
-    while (nx < d1) {
-      one(s0, s1, Par<0>{});
-      if (nx >= d1) {
-        off = 2 * kTile;
-#pragma unroll
-        for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
-        break;
-      }
-      one(s1, s0, Par<1>{});
-    }
-    const unsigned long long bad = top(off);
-    weights(s0);
-    product(off);
-    if (bad) dirty(bad);
   }
 
   l += __shfl_xor(l, 32, kWave);
