@@ -590,57 +590,82 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       const int64_t first = (int64_t)start + ta - p.window + 1;
       x0 = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
     }
-    // A load brings 4, 8 or 16 rows of one page, so page ids, addresses and scales are the
-    // same in every lane of a wave.  Lane l holds id (-1: not there) and scales of page pb + l
-    // of the sequence, 64 pages at a time; a tile's are read out of the lanes.
-    int pb = 0, pid = -1;
+    // A load brings 4, 8 or 16 rows of one page, so page addresses and scales are the same in
+    // every lane of a wave.  Lane l holds those of page pb + l of the sequence (byte offset of
+    // the page's rows, -1: not there), 64 pages at a time; a tile's are read out of the lanes,
+    // once where a page holds whole tiles.
+    const bool big = lg >= 6;
+    int pb = 0;
+    int64_t poff = -1;
     float pks = 0.f, pvs = 0.f;
     auto pages = [&](int first) __attribute__((always_inline)) {
       pb = first;
-      const int j = first + lane;
-      pid = j < ((P + pmask) >> lg) ? page_of(p.c, n, (int)min((int64_t)j << lg, (int64_t)INT32_MAX)) : -1;
-      const int64_t at = (int64_t)max(pid, 0) * p.H_kv + h;
+      const int j = first + lane, id = j < ((P + pmask) >> lg) ? page_of(p.c, n, j << lg) : -1;
+      const int64_t at = (int64_t)max(id, 0) * p.H_kv + h;
+      poff = id < 0 ? -1 : (at << lg) * D;
       pks = p.c.k_scale[at];
       pvs = p.c.v_scale[at];
     };
     auto lane_of = [&](int row) __attribute__((always_inline)) { return (row >> lg) - pb; };
+    auto off_of = [&](int pl) __attribute__((always_inline)) -> int64_t {   // (-1: not there)
+      return (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(poff >> 32), pl & 63) << 32 |
+                       (unsigned)__builtin_amdgcn_readlane((int)poff, pl & 63));
+    };
     const uint32_t rlane = (uint32_t)(lane / kCp) * D + 16 * (lane % kCp);   // this lane's piece of a load
     const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K and V, kTile / 2 bytes each, behind the first tiles
     auto fetch = [&](const uint8_t* src, uint32_t to, int x) __attribute__((always_inline)) {
+      if (big) {
+        const int64_t off = max(off_of(lane_of(x * kBN)), (int64_t)0);
+        const u32x4 rs = buffer_of(src + off + ((x * kBN) & pmask) * D, kBN * D);
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) {
-        const int r = x * kBN + (wave + 4 * s) * kCr;
-        const int id = __builtin_amdgcn_readlane(pid, lane_of(r) & 63);
-        const u32x4 rs = buffer_of(src + ((((int64_t)max(id, 0) * p.H_kv + h) << lg) + (r & pmask)) * D, kCr * D);
-        to_lds(rs, rlane, to + s * 4096);
+        for (int s = 0; s < kCt; ++s) to_lds(rs, rlane + (wave + 4 * s) * (kCr * D), to + s * 4096);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kCt; ++s) {
+          const int r = x * kBN + (wave + 4 * s) * kCr;
+          const int64_t off = max(off_of(lane_of(r)), (int64_t)0);
+          to_lds(buffer_of(src + off + (r & pmask) * D, kCr * D), rlane, to + s * 4096);
+        }
       }
     };
+    auto lane_f = [&](float v, int pl) __attribute__((always_inline)) {
+      return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), pl & 63));
+    };
     // Codes of tile x -> bf16 (rows that are not held -> zeros).
+    auto put = [&](const u32x4& w, float sc, uint32_t to, int r, int c) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint2 a = f8x4_to_bf16(w[2 * e], sc), b = f8x4_to_bf16(w[2 * e + 1], sc);
+        *(lds_u32x4w*)(uintptr_t)(lds_at(sT) + to + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4)) =
+            u32x4{a.x, a.y, b.x, b.y};
+      }
+    };
     auto convert = [&](uint32_t from, uint32_t to, float lane_scale, int x) __attribute__((always_inline)) {
-      const int c = lane % kCp;
+      const int c = lane % kCp, pl = lane_of(x * kBN);
+      u32x4 w[kCt];
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) {
-        const int r0 = (wave + 4 * s) * kCr, r = r0 + lane / kCp, pl = lane_of(x * kBN + r0) & 63;
-        const float sc = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(lane_scale), pl));
-        u32x4 w = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
-        if (x * kBN + kBN > P || __builtin_amdgcn_readlane(pid, pl) < 0) {
-          if (x * kBN + r >= P || __builtin_amdgcn_readlane(pid, pl) < 0) w = u32x4{0, 0, 0, 0};
-        }
+      for (int s = 0; s < kCt; ++s) w[s] = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
+      if (big && x * kBN + kBN <= P && off_of(pl) >= 0) {
+        const float sc = lane_f(lane_scale, pl);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint2 a = f8x4_to_bf16(w[2 * e], sc), b = f8x4_to_bf16(w[2 * e + 1], sc);
-          *(lds_u32x4w*)(uintptr_t)(lds_at(sT) + to + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4)) =
-              u32x4{a.x, a.y, b.x, b.y};
+        for (int s = 0; s < kCt; ++s) put(w[s], sc, to, (wave + 4 * s) * kCr + lane / kCp, c);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kCt; ++s) {
+          const int r0 = (wave + 4 * s) * kCr, r = r0 + lane / kCp, l0 = lane_of(x * kBN + r0);
+          if (off_of(l0) < 0 || x * kBN + r >= P) w[s] = u32x4{0, 0, 0, 0};
+          put(w[s], lane_f(lane_scale, l0), to, r, c);
         }
       }
     };
     // Bit r: row x kBN + r is held.
     auto held = [&](int x) __attribute__((always_inline)) -> unsigned long long {
+      if (big && x * kBN + kBN <= P && off_of(lane_of(x * kBN)) >= 0) return ~0ull;
       unsigned long long bits = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {                     // 16 rows lie on one page
         const int left = P - x * kBN - 16 * i;
-        if (left > 0 && __builtin_amdgcn_readlane(pid, lane_of(x * kBN + 16 * i) & 63) >= 0)
+        if (left > 0 && off_of(lane_of(x * kBN + 16 * i)) >= 0)
           bits |= (left >= 16 ? 0xffffull : (1ull << left) - 1) << 16 * i;
       }
       return bits;
