@@ -14,33 +14,137 @@ checks tensors, allocates what the caller did not supply and passes pointers.
 from __future__ import annotations
 
 import ctypes as ct
-from dataclasses import dataclass
 
 import torch
 
-from . import _i32, _lib, _mode_kind, _on_gpu, _ptr, _rows, _same_rows, _stream, _is_target_verify
+from . import _lib, _is_target_verify, _mode_kind
 from ._lib import GDN_BF16
 
 _PAGES = (16, 32, 64, 128)
+_NO_CACHE = _lib.KVCacheArgs()
 
 
-@dataclass
+# ------------------------------------------------------------------ helpers
+# (A decode step is a few microseconds of GPU work: the checks below look at each tensor
+# once, and arguments go into their struct in one positional call.)
+def _place(first, *ts) -> int:
+    """Device index that all given tensors share."""
+    i = first.get_device()
+    if i < 0:
+        raise ValueError("all tensors must live on the GPU")
+    for t in ts:
+        if t is not None and t.get_device() != i:
+            raise ValueError("all tensors must live on the GPU" if t.get_device() < 0
+                             else "all tensors must be on the same device")
+    return i
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vec(t, name: str, n: int, dtype=torch.int32):
+    """Address of a contiguous vector of n elements, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _heads(t, name: str, n: int, heads: int, d: int) -> int:
+    """Token stride of a bf16 [n, heads, d] view whose heads are contiguous."""
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be bf16, got {t.dtype}")
+    if t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name} must have contiguous heads (strides {st})")
+    return st[0] if n > 1 else heads * d
+
+
+def _table(t, n: int) -> tuple[int, int]:
+    """(row stride, width) of a block table."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 [{n}, width] with unit column stride, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    w = t.shape[1]
+    return (t.stride(0) if n > 1 else w), w
+
+
+def _run(name: str, fn, args, i: int) -> None:
+    """The call on device i's current stream."""
+    if torch.cuda.current_device() == i:
+        st = fn(ct.byref(args), torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(ct.byref(args), torch._C._cuda_getCurrentRawStream(i))
+    if st:
+        _lib.check(name, st)
+
+
+def _need(name: str, fn, args, i: int) -> int:
+    """A workspace query on device i."""
+    if torch.cuda.current_device() == i:
+        need = fn(ct.byref(args))
+    else:
+        with torch.cuda.device(i):
+            need = fn(ct.byref(args))
+    if need < 0:
+        _lib.check(name, int(-need))
+    return need
+
+
+def _attach(name: str, fn, args, i: int, workspace):
+    """Attach a call's workspace: the caller's uint8 tensor, or a fresh allocation."""
+    if workspace is None:
+        need = _need(name, fn, args, i)
+        if need == 0:
+            return None
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", i))
+    elif workspace.dtype is not torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
+            or workspace.get_device() != i:
+        raise ValueError("workspace must be a contiguous uint8 vector on the call's device")
+    args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+# ------------------------------------------------------------------ the cache
 class KVCache:
-    """The tensors of a paged 8-bit key/value cache (gdn_kv_cache): k, v float8_e4m3fn
-    [num_pages, H_kv, page, d]; k_scale, v_scale fp32 [num_pages, H_kv], powers of two (a
-    cached value is code * scale); optional pos int32 and weight fp32 [num_pages, H_kv,
-    page]: the rows' positions and the softmax weights accumulated on them (an eviction
+    """The tensors of a paged 8-bit key/value cache (gdn_kv_cache), checked once: k, v
+    float8_e4m3fn [num_pages, H_kv, page, d]; k_scale, v_scale fp32 [num_pages, H_kv], powers
+    of two (a cached value is code * scale); optional pos int32 and weight fp32 [num_pages,
+    H_kv, page]: the rows' positions and the softmax weights accumulated on them (an eviction
     needs both)."""
-    k: torch.Tensor
-    v: torch.Tensor
-    k_scale: torch.Tensor
-    v_scale: torch.Tensor
-    pos: torch.Tensor | None = None
-    weight: torch.Tensor | None = None
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_pos", "_weight", "_args", "_device")
 
-    @property
-    def page(self) -> int:
-        return self.k.shape[2]
+    def __init__(self, k, v, k_scale, v_scale, pos=None, weight=None):
+        shape = k.shape
+        if len(shape) != 4 or k.dtype is not torch.float8_e4m3fn or not k.is_contiguous():
+            raise ValueError("cache.k must be contiguous float8_e4m3fn [num_pages, H_kv, page, d]")
+        pages, H_kv, page, d = shape
+        if v.shape != shape or v.dtype is not torch.float8_e4m3fn or not v.is_contiguous():
+            raise ValueError("cache.v must be like cache.k")
+        for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype is not torch.float32 or t.shape != (pages, H_kv) or not t.is_contiguous():
+                raise ValueError(f"cache.{nm} must be contiguous fp32 [{pages}, {H_kv}]")
+        for t, nm, dt in ((pos, "pos", torch.int32), (weight, "weight", torch.float32)):
+            if t is not None and (t.dtype is not dt or t.shape != (pages, H_kv, page) or not t.is_contiguous()):
+                raise ValueError(f"cache.{nm} must be contiguous {dt} [{pages}, {H_kv}, {page}]")
+        self._device = _place(k, v, k_scale, v_scale, pos, weight)
+        self._k, self._v, self._k_scale, self._v_scale, self._pos, self._weight = k, v, k_scale, v_scale, pos, weight
+        self._args = _lib.KVCacheArgs(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _at(pos),
+                                      _at(weight), pages, page, H_kv, d, 0)
+
+    # (fixed, since the calls use the addresses taken above)
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    pos = property(lambda self: self._pos)
+    weight = property(lambda self: self._weight)
+    page = property(lambda self: self._args.page)
 
 
 def kv_cache(num_pages: int, H_kv: int, d: int, page: int = 64, *, track: bool = False,
@@ -56,54 +160,6 @@ def kv_cache(num_pages: int, H_kv: int, d: int, page: int = 64, *, track: bool =
                    torch.zeros(rows, dtype=torch.float32, device=device) if track else None)
 
 
-def _cache_args(c: KVCache, track: bool = False) -> _lib.KVCacheArgs:
-    k = c.k
-    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or not k.is_contiguous():
-        raise ValueError("cache.k must be contiguous float8_e4m3fn [num_pages, H_kv, page, d]")
-    pages, H_kv, page, d = k.shape
-    if c.v.shape != k.shape or c.v.dtype != k.dtype or not c.v.is_contiguous():
-        raise ValueError("cache.v must be like cache.k")
-    for t, nm in ((c.k_scale, "k_scale"), (c.v_scale, "v_scale")):
-        if t.shape != (pages, H_kv) or t.dtype != torch.float32 or not t.is_contiguous():
-            raise ValueError(f"cache.{nm} must be contiguous fp32 [{pages}, {H_kv}]")
-    for t, nm, dt in ((c.pos, "pos", torch.int32), (c.weight, "weight", torch.float32)):
-        if t is None:
-            if track:
-                raise ValueError(f"this call needs cache.{nm} (kv_cache(track=True))")
-        elif t.shape != (pages, H_kv, page) or t.dtype != dt or not t.is_contiguous():
-            raise ValueError(f"cache.{nm} must be contiguous {dt} [{pages}, {H_kv}, {page}]")
-    return _lib.KVCacheArgs(_ptr(k), _ptr(c.v), _ptr(c.k_scale), _ptr(c.v_scale), _ptr(c.pos), _ptr(c.weight),
-                            pages, page, H_kv, d)
-
-
-def _cache_device(c: KVCache, *ts):
-    return _on_gpu(c.k, c.v, c.k_scale, c.v_scale, c.pos, c.weight, *ts)
-
-
-def _table(t: torch.Tensor, n: int) -> tuple[int, int]:
-    """(row stride, width) of a block table."""
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be int32 [{n}, width] with unit column stride, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-    return (t.stride(0) if n > 1 else t.shape[1]), t.shape[1]
-
-
-def _bf16(**ts):
-    for nm, t in ts.items():
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"{nm} must be bf16")
-
-
-def _slopes(t, H):
-    if t is not None and (t.dtype != torch.float32 or t.shape != (H,) or not t.is_contiguous()):
-        raise ValueError(f"slopes must be contiguous fp32 [{H}]")
-
-
-def _stride(t, name, heads, d):
-    s = _rows(t, name, heads, d)
-    return s if t.shape[0] > 1 else heads * d
-
-
 def kv_store(k, v, cu_seqlens, cache: KVCache, block_table, cache_len, *, start=None) -> None:
     """Quantise the new tokens' keys and values (k, v bf16 [T, H_kv, d]) into the cache: the
     tokens of sequence n (cu_seqlens int32 [N+1]; None: one token per sequence) become its
@@ -111,27 +167,19 @@ def kv_store(k, v, cu_seqlens, cache: KVCache, block_table, cache_len, *, start=
     width]).  start int32 [N]: the first token's position (default cache_len), for a cache
     that keeps positions.  cache_len[n] < 0 skips the sequence."""
     lib = _lib.load()
-    dev = _cache_device(cache, k, v, cu_seqlens, block_table, cache_len, start)
-    ca = _cache_args(cache)
-    T, N = k.shape[0], cache_len.shape[0]
-    _same_rows(T, "the tokens of k", v=v)
-    _bf16(k=k, v=v)
-    _i32(cache_len, "cache_len", N)
-    if cu_seqlens is not None:
-        _i32(cu_seqlens, "cu_seqlens", N + 1)
-    elif T != N:
+    ca = cache._args
+    T, N, H_kv, d = k.shape[0], cache_len.shape[0], ca.H_kv, ca.d
+    i = _place(cache._k, k, v, cu_seqlens, block_table, cache_len, start)
+    if cu_seqlens is None and T != N:
         raise ValueError(f"without cu_seqlens there is one token per sequence: {T} tokens, {N} sequences")
-    if start is not None:
-        _i32(start, "start", N)
     ts, tw = _table(block_table, N)
-    args = _lib.KVStoreArgs(cache=ca, in_dtype=GDN_BF16, N=N, T=T, k=_ptr(k), k_stride=_stride(k, "k", ca.H_kv, ca.d),
-                            v=_ptr(v), v_stride=_stride(v, "v", ca.H_kv, ca.d), cu_seqlens=_ptr(cu_seqlens),
-                            cache_len=_ptr(cache_len), start=_ptr(start), block_table=_ptr(block_table),
-                            table_stride=ts, table_width=tw)
-    with torch.cuda.device(dev):
-        _lib.check("gdn_kv_store", lib.gdn_kv_store(ct.byref(args), _stream(dev)))
+    args = _lib.KVStoreArgs(ca, GDN_BF16, N, T, k.data_ptr(), _heads(k, "k", T, H_kv, d), v.data_ptr(),
+                            _heads(v, "v", T, H_kv, d), _vec(cu_seqlens, "cu_seqlens", N + 1),
+                            _vec(cache_len, "cache_len", N), _vec(start, "start", N), block_table.data_ptr(), ts, tw)
+    _run("gdn_kv_store", lib.gdn_kv_store, args, i)
 
 
+# ------------------------------------------------------------------ attention
 def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0, slopes=None,
                 window: int = 0, doc=None, visible=None, cache: KVCache | None = None, block_table=None,
                 cache_len=None, start=None, out=None):
@@ -149,88 +197,45 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
     lib = _lib.load()
     T, H, d = q.shape
     H_kv, N = k.shape[1], cu_seqlens.shape[0] - 1
-    ts_all = (q, k, v, cu_seqlens, slopes, doc, visible, block_table, cache_len, start, out)
-    args = _lib.AttnExtendArgs()
     if cache is not None:
         if block_table is None or cache_len is None:
             raise ValueError("a cache needs block_table and cache_len")
-        dev = _cache_device(cache, *ts_all)
-        args.cache = _cache_args(cache)
-        args.table_stride, args.table_width = _table(block_table, N)
-        _i32(cache_len, "cache_len", N)
+        ca = cache._args
+        i = _place(cache._k, q, k, v, cu_seqlens, slopes, doc, visible, block_table, cache_len, start, out)
+        ts, tw = _table(block_table, N)
     else:
         if block_table is not None or cache_len is not None:
             raise ValueError("block_table and cache_len need a cache")
-        dev = _on_gpu(*ts_all)
-    _same_rows(T, "the tokens of q", k=k, v=v, out=out, doc=doc)
-    _bf16(q=q, k=k, v=v)
-    _i32(cu_seqlens, "cu_seqlens", N + 1)
-    for t, nm, n in ((visible, "visible", N), (start, "start", N), (doc, "doc", T)):
-        if t is not None:
-            _i32(t, nm, n)
-    _slopes(slopes, H)
+        ca, ts, tw = _NO_CACHE, 0, 0
+        i = _place(q, k, v, cu_seqlens, slopes, doc, visible, start, out)
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-    _bf16(out=out)
-    args.in_dtype = args.out_dtype = GDN_BF16
-    args.N, args.H, args.H_kv, args.d, args.T = N, H, H_kv, d, T
-    args.q, args.q_stride = _ptr(q), _stride(q, "q", H, d)
-    args.k, args.k_stride = _ptr(k), _stride(k, "k", H_kv, d)
-    args.v, args.v_stride = _ptr(v), _stride(v, "v", H_kv, d)
-    args.out, args.out_stride = _ptr(out), _stride(out, "out", H, d)
-    args.cu_seqlens, args.cache_len, args.start = _ptr(cu_seqlens), _ptr(cache_len), _ptr(start)
-    args.block_table, args.causal = _ptr(block_table), int(bool(causal))
-    args.visible, args.doc, args.slopes = _ptr(visible), _ptr(doc), _ptr(slopes)
-    args.window, args.softcap = int(window), float(softcap)
-    args.scale = float(d ** -0.5 if scale is None else scale)
-    with torch.cuda.device(dev):
-        _lib.check("gdn_attn_extend", lib.gdn_attn_extend(ct.byref(args), _stream(dev)))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    args = _lib.AttnExtendArgs(
+        ca, GDN_BF16, GDN_BF16, N, H, H_kv, d, T, q.data_ptr(), _heads(q, "q", T, H, d), k.data_ptr(),
+        _heads(k, "k", T, H_kv, d), v.data_ptr(), _heads(v, "v", T, H_kv, d), out.data_ptr(),
+        _heads(out, "out", T, H, d), _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(cache_len, "cache_len", N),
+        _vec(start, "start", N), _at(block_table), ts, tw, 1 if causal else 0, _vec(visible, "visible", N),
+        _vec(doc, "doc", T), _vec(slopes, "slopes", H, torch.float32), window, d ** -0.5 if scale is None else scale,
+        softcap)
+    _run("gdn_attn_extend", lib.gdn_attn_extend, args, i)
     return out
-
-
-def _workspace_for(lib_size, fn, args, dev, workspace):
-    """Attach a call's workspace: the caller's uint8 tensor, or a fresh allocation."""
-    if workspace is None:
-        need = lib_size(ct.byref(args))
-        if need < 0:
-            _lib.check(fn, int(-need))
-        if need == 0:
-            return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
-            or workspace.device != dev:
-        raise ValueError("workspace must be a contiguous uint8 vector on the call's device")
-    args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel()
-    return workspace
 
 
 def _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate, max_kvlen, out):
     N, H, d = q.shape
-    dev = _cache_device(cache, q, block_table, kv_len, slopes, q_pos, out)
-    args = _lib.AttnDecodeArgs()
-    args.cache = ca = _cache_args(cache)
-    if accumulate and cache.weight is None:
+    ca = cache._args
+    i = _place(cache._k, q, block_table, kv_len, slopes, q_pos, out)
+    if accumulate and cache._weight is None:
         raise ValueError("accumulate needs cache.weight (kv_cache(track=True))")
     if ca.d != d:
         raise ValueError(f"q must be [N, H, {ca.d}], got {tuple(q.shape)}")
-    _bf16(q=q)
-    _i32(kv_len, "kv_len", N)
-    if q_pos is not None:
-        _i32(q_pos, "q_pos", N)
-    _slopes(slopes, H)
-    args.in_dtype = args.out_dtype = GDN_BF16
-    args.N, args.H = N, H
-    args.q, args.q_stride = _ptr(q), _stride(q, "q", H, d)
-    if out is not None:
-        _same_rows(N, "one token per sequence of q", out=out)
-        _bf16(out=out)
-        args.out, args.out_stride = _ptr(out), _stride(out, "out", H, d)
-    args.kv_len, args.q_pos, args.block_table = _ptr(kv_len), _ptr(q_pos), _ptr(block_table)
-    args.table_stride, args.table_width = _table(block_table, N)
-    args.max_kvlen, args.slopes, args.window = int(max_kvlen), _ptr(slopes), int(window)
-    args.scale = float(d ** -0.5 if scale is None else scale)
-    args.softcap, args.accumulate = float(softcap), int(bool(accumulate))
-    return args, dev
+    ts, tw = _table(block_table, N)
+    # (a query of the workspace reads no buffer: an aligned stand-in for the output)
+    o, os = (256, H * d) if out is None else (out.data_ptr(), _heads(out, "out", N, H, d))
+    return _lib.AttnDecodeArgs(
+        ca, GDN_BF16, GDN_BF16, N, H, q.data_ptr(), _heads(q, "q", N, H, d), o, os, _vec(kv_len, "kv_len", N),
+        _vec(q_pos, "q_pos", N), block_table.data_ptr(), ts, tw, max_kvlen, _vec(slopes, "slopes", H, torch.float32),
+        window, d ** -0.5 if scale is None else scale, softcap, 1 if accumulate else 0, None, 0), i
 
 
 def attn_decode(q, cache: KVCache, block_table, kv_len, *, scale=None, softcap: float = 0.0, slopes=None,
@@ -246,12 +251,11 @@ def attn_decode(q, cache: KVCache, block_table, kv_len, *, scale=None, softcap: 
     lib = _lib.load()
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    args, dev = _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate,
-                             max_kvlen, out)
-    with torch.cuda.device(dev):
-        ws = _workspace_for(lib.gdn_attn_decode_workspace_size, "gdn_attn_decode", args, dev, workspace)
-        _lib.check("gdn_attn_decode", lib.gdn_attn_decode(ct.byref(args), _stream(dev)))
-        del ws
+    args, i = _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate,
+                           max_kvlen, out)
+    ws = _attach("gdn_attn_decode", lib.gdn_attn_decode_workspace_size, args, i, workspace)
+    _run("gdn_attn_decode", lib.gdn_attn_decode, args, i)
+    del ws
     return out
 
 
@@ -260,29 +264,21 @@ def attn_decode_workspace_size(q, cache: KVCache, block_table, kv_len, *, scale=
                                max_kvlen: int = 0) -> int:
     """Bytes of workspace attn_decode wants for these arguments (0: none)."""
     lib = _lib.load()
-    args, dev = _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate,
-                             max_kvlen, None)
-    # the host-side query reads no buffer: an aligned stand-in for the output
-    args.out, args.out_stride = ct.c_void_p(256), q.shape[1] * q.shape[2]
-    with torch.cuda.device(dev):
-        need = lib.gdn_attn_decode_workspace_size(ct.byref(args))
-    if need < 0:
-        _lib.check("gdn_attn_decode_workspace_size", int(-need))
-    return int(need)
+    args, i = _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate,
+                           max_kvlen, None)
+    return _need("gdn_attn_decode_workspace_size", lib.gdn_attn_decode_workspace_size, args, i)
 
 
+# ------------------------------------------------------------------ eviction
 def _evict_args(cache, block_table, kv_len, budget, recent, new_len):
-    dev = _cache_device(cache, block_table, kv_len, new_len)
+    i = _place(cache._k, block_table, kv_len, new_len)
+    if cache._pos is None or cache._weight is None:
+        raise ValueError("an eviction needs cache.pos and cache.weight (kv_cache(track=True))")
     N = kv_len.shape[0]
-    _i32(kv_len, "kv_len", N)
-    args = _lib.KVEvictArgs()
-    args.cache = _cache_args(cache, track=True)
-    args.N, args.budget, args.recent, args.kv_len = N, int(budget), int(recent), _ptr(kv_len)
-    args.block_table = _ptr(block_table)
-    args.table_stride, args.table_width = _table(block_table, N)
-    if new_len is not None:
-        args.new_len = _ptr(_i32(new_len, "new_len", N))
-    return args, dev
+    ts, tw = _table(block_table, N)
+    # (a query of the workspace reads no buffer: an aligned stand-in for the new lengths)
+    return _lib.KVEvictArgs(cache._args, N, budget, recent, tw, _vec(kv_len, "kv_len", N),
+                            256 if new_len is None else _vec(new_len, "new_len", N), block_table.data_ptr(), ts, None, 0), i
 
 
 def kv_evict(cache: KVCache, block_table, kv_len, budget: int, *, recent: int = 0, new_len=None,
@@ -295,25 +291,21 @@ def kv_evict(cache: KVCache, block_table, kv_len, budget: int, *, recent: int = 
     lib = _lib.load()
     if new_len is None:
         new_len = torch.empty_like(kv_len)
-    args, dev = _evict_args(cache, block_table, kv_len, budget, recent, new_len)
-    with torch.cuda.device(dev):
-        ws = _workspace_for(lib.gdn_kv_evict_workspace_size, "gdn_kv_evict", args, dev, workspace)
-        _lib.check("gdn_kv_evict", lib.gdn_kv_evict(ct.byref(args), _stream(dev)))
-        del ws
+    args, i = _evict_args(cache, block_table, kv_len, budget, recent, new_len)
+    ws = _attach("gdn_kv_evict", lib.gdn_kv_evict_workspace_size, args, i, workspace)
+    _run("gdn_kv_evict", lib.gdn_kv_evict, args, i)
+    del ws
     return new_len
 
 
 def kv_evict_workspace_size(cache: KVCache, block_table, kv_len, budget: int, *, recent: int = 0) -> int:
     """Bytes of workspace kv_evict wants for these arguments."""
     lib = _lib.load()
-    args, _ = _evict_args(cache, block_table, kv_len, budget, recent, None)
-    args.new_len = ct.c_void_p(256)          # (not read by the query)
-    need = lib.gdn_kv_evict_workspace_size(ct.byref(args))
-    if need < 0:
-        _lib.check("gdn_kv_evict_workspace_size", int(-need))
-    return int(need)
+    args, i = _evict_args(cache, block_table, kv_len, budget, recent, None)
+    return _need("gdn_kv_evict_workspace_size", lib.gdn_kv_evict_workspace_size, args, i)
 
 
+# ------------------------------------------------------------------ layer call
 def forward_attn(layer, forward_batch, q, k, v, save_kv_cache: bool = True):
     """Full-attention layer call of a hybrid model (pymllm RadixAttention.forward), the
     counterpart of forward_gdn: stores the new tokens in the layer's cache and attends.
