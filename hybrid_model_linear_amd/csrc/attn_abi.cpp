@@ -95,7 +95,7 @@ int plan_decode(const gdn_attn_decode_args* a, gdn::AttnDecodeLaunch& p, int64_t
   p.score_cap = (rows + 63) / 64 * 64;
   if (a->max_kvlen > 0 && a->max_kvlen < rows) rows = a->max_kvlen;
   if (a->window > 0 && !a->cache.pos && a->window < rows) rows = a->window;
-  p.splits = gdn::attn_decode_splits(a->N, a->H, p.c.H_kv, rows, gdn::current_device_cus());
+  gdn::plan_attn_decode(p, rows, gdn::current_device_cus());
   if ((int64_t)p.splits * ((a->H / p.c.H_kv + 15) / 16) * p.c.H_kv * a->N > kMaxGrid) return GDN_E_UNSUPPORTED;
   const int64_t heads = (int64_t)a->N * a->H;
   auto part = [&](int64_t floats) {

@@ -4,16 +4,18 @@
 //
 // Bound by HBM: 2 d bytes of codes per row and kv head against 4 d H / H_kv flop.  The
 // H / H_kv query heads of a kv head share the rows, so they are the 16 columns of one
-// 16x16x32 MFMA tile and every code is read once.  A wave takes 64 rows at a time with no
-// LDS in the loop:
-//   - S^T = K Q^T.  Row 4 g + r of tile t (t = 0..3) is row 16 g + 4 t + r of the 64, so that
-//     lane (query j, group g) ends up with the scores of the 16 consecutive rows 16 g ..
-//     16 g + 15: one page (pages hold 16 rows at least), and in the order in which the B
-//     operand of P wants them.  The d axis of K is taken in 16-byte pieces straight from
-//     memory (Q is read in the same order).
-//   - O^T = V^T P^T.  Lane (j, g) loads d / 16 bytes of each of its group's 16 rows and
-//     transposes 4 x 4 bytes at a time with byte permutes: it then holds 16 rows of each of
+// 16x16x32 MFMA tile and every code is read once.  A wave takes R = 64 rows at a time (32 at
+// d = 256, whose codes would take the registers of its second wave per SIMD) with no LDS in
+// the loop:
+//   - S^T = K Q^T.  Row 4 g + r of tile t is row R / 4 g + 4 t + r of the R, so that lane
+//     (query j, group g) ends up with the scores of R / 4 consecutive rows: one page (pages
+//     hold 16 rows at least), and in the order in which the B operand of P wants them.  The d
+//     axis of K is taken in 16-byte pieces straight from memory (Q is read in the same order).
+//   - O^T = V^T P^T.  Lane (j, g) loads d / 16 bytes of each of its group's rows and
+//     transposes 4 x 4 bytes at a time with byte permutes: it then holds the rows of each of
 //     its d / 16 columns, the A operand's order.
+// The next tile's K is loaded when this one's scores are formed, its V when the product is,
+// page ids a tile before that.
 // Codes become bf16 times their page's power-of-two scale, which is exact; the products
 // are summed in fp32.  The weights p are rounded to bf16 for the second product (2^-9 of
 // each weight at most, as the output's own rounding); their sum and the accumulated
@@ -28,9 +30,10 @@ namespace {
 
 constexpr int kDecThreads = 256;
 constexpr int kDecWaves = kDecThreads / kWave;
-constexpr int kRows = 64;                       // rows of a wave's tile
+constexpr int kChunk = 64;                      // unit of the split over rows
+constexpr int kRanked = 512;                    // sequences that are taken in order of length
 
-// The 64-row tiles [t0, t1) that hold rows a sequence's query can see, and how many each
+// The 64-row chunks [t0, t1) that hold rows a sequence's query can see, and how many each
 // split takes.
 struct DecRange {
   int lo, hi;                                   // rows [lo, hi)
@@ -47,11 +50,47 @@ __device__ __forceinline__ DecRange dec_range(const AttnDecodeLaunch& p, int n, 
     r.lo = max(0, (int)max((int64_t)qpos - p.window + 1, (int64_t)-1));
     r.hi = (int)min((int64_t)r.hi, (int64_t)qpos + p.window);
   }
-  r.t0 = r.lo / kRows;
-  r.t1 = r.hi > r.lo ? (r.hi + kRows - 1) / kRows : r.t0;
-  // at least one tile per wave, else the split is not worth its workgroup
-  r.per = max((r.t1 - r.t0 + p.splits - 1) / p.splits, kDecWaves);
+  r.t0 = r.lo / kChunk;
+  r.t1 = r.hi > r.lo ? (r.hi + kChunk - 1) / kChunk : r.t0;
+  r.per = max((r.t1 - r.t0 + p.splits - 1) / p.splits, p.min_chunks);
   return r;
+}
+
+// The sequence of rank `pos` of N <= kRanked in order of length (0 the longest; in steps of
+// an eighth bit and more: the lengths' top seven bits, equal ones by index), found by every
+// wave for itself: the lanes hold all keys (which are distinct), and the answer's key is
+// built bit by bit from the top, each bit kept if more than `pos` keys are at least as large.
+// (Every workgroup does this, so it has to be short: a count over all pairs through LDS cost
+// 256 x 2048 rows 25 us of 220, whole lengths in 64-bit keys 19.)
+__device__ __forceinline__ int nth_longest(const int32_t* len, int N, int pos, int lane) {
+  constexpr int kPer = kRanked / kWave;
+  unsigned key[kPer], top = 1;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = i * kWave + lane;
+    key[i] = i * kWave < N && j < N ? (unsigned)max(len[j], 0) : 0;
+    top = max(top, key[i]);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, o, kWave));
+  const int shift = max(25 - __builtin_clz(__builtin_amdgcn_readfirstlane((int)top)), 0);
+  const int ib = 32 - __builtin_clz(N);                  // an index takes ib bits (and none is 0)
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = i * kWave + lane;
+    key[i] = j < N ? key[i] >> shift << ib | (unsigned)(N - j) : 0;
+  }
+  unsigned found = 0;
+#pragma unroll 1
+  for (unsigned bit = 1u << (ib + 6); bit; bit >>= 1) {
+    const unsigned want = found | bit;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i * kWave < N) count += __builtin_popcountll(__ballot(key[i] >= want));
+    if (count > pos) found = want;
+  }
+  return N - (int)(found & ((1u << ib) - 1));
 }
 
 __device__ __forceinline__ float max_over_groups(float v) {     // lanes j, j + 16, j + 32, j + 48
@@ -72,7 +111,10 @@ template <int W, typename T> __device__ __forceinline__ uint32_t word_of(const T
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLaunch p) {
+__global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecodeLaunch p) {
+  constexpr int kR = D == 256 ? 32 : 64;        // rows of a wave's tile
+  constexpr int kG = kR / 4;                    // rows of a lane group
+  constexpr int kTS = kR / 16;                  // 16-row tiles of S^T
   constexpr int kT = D / 16;                    // 16-column tiles of O^T
   constexpr int kP = D / 64;                    // 16-byte pieces of a K row per lane
   constexpr int kW = D / 64;                    // 32-bit words of a V row per lane
@@ -86,12 +128,16 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
   b /= p.splits;
   const int gt = b % groups;
   b /= groups;
-  const int h = b % p.c.H_kv, n = b / p.c.H_kv;
+  const int h = b % p.c.H_kv;
+  int n = b / p.c.H_kv;
+  if (p.ranked) n = nth_longest(p.kv_len, p.N, n, lane);
   int qpos;
   const DecRange rg = dec_range(p, n, qpos);
   if (p.kv_len[n] < 0) return;                  // a padding row
-  const int tb = rg.t0 + split * rg.per, te = min(tb + rg.per, rg.t1);
-  if (tb >= te && split > 0) return;            // (the join counts the splits that hold tiles)
+  // this split's tiles of kR rows
+  const int c0 = rg.t0 + split * rg.per;
+  const int tb = c0 * (kChunk / kR), te = min((int)min((int64_t)c0 + rg.per, (int64_t)rg.t1) * (kChunk / kR), (rg.hi + kR - 1) / kR);
+  if (tb >= te && split > 0) return;            // (the join counts the splits that hold chunks)
   const int hq = h * G + gt * 16 + j16;         // this lane's query head
   const bool live = gt * 16 + j16 < G;
   const int lg = p.c.page_log2, pmask = (1 << lg) - 1;
@@ -113,49 +159,59 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
 #pragma unroll
   for (int t = 0; t < kT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // page of the rows 16 g .. of tile t for this lane as a V (and score) lane, clamped into
-  // the sequence so that every address is a held row's
+  // The page of the rows kG g .. of tile t, clamped into the sequence so that every address is
+  // a held row's (-1: out of range).
   auto page_at = [&](int t, int g) __attribute__((always_inline)) {
-    return page_of(p.c, n, min(t * kRows + 16 * g, rg.hi - 1));
+    return page_of(p.c, n, min(t * kR + kG * g, rg.hi - 1));
   };
-  u32x4 kc[4][kP];
-  vword vc[16];
-  int kid = -1, vid = -1;                       // pages of the loaded K rows and V rows
-  auto load_k = [&](int t) __attribute__((always_inline)) {
-    kid = page_at(t, j16 >> 2);
-    const uint8_t* base = p.c.k + page_rows(p.c, max(kid, 0), h) * D;
+  u32x4 kc[kTS][kP];
+  vword vc[kG];
+  int kid = -1, vid = -1;                       // pages of this lane's K rows and V rows: the next tile's to load
+  int cur = -1;                                 // V page of the tile that is computed
+  float ks = 1.f, vs = 1.f, ksn = 1.f, vsn = 1.f;
+  auto load_k = [&](int t) __attribute__((always_inline)) {   // (and the scales of both)
+    const int64_t row = page_rows(p.c, max(kid, 0), h);
+    const uint8_t* base = p.c.k + row * D + 16 * g16;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int r = (t * kRows + 16 * (j16 >> 2) + 4 * s + (j16 & 3)) & pmask;
+    for (int s = 0; s < kTS; ++s) {
+      const uint32_t r = (t * kR + kG * (j16 >> 2) + 4 * s + (j16 & 3)) & pmask;
 #pragma unroll
       for (int c = 0; c < kP; ++c)
-        kc[s][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (int64_t)r * D + 64 * c + 16 * g16));
+        kc[s][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + r * D + 64 * c));
     }
+    ksn = kid < 0 ? 1.f : p.c.k_scale[(int64_t)kid * p.c.H_kv + h];
+    vsn = vid < 0 ? 1.f : p.c.v_scale[(int64_t)vid * p.c.H_kv + h];
   };
-  auto load_v = [&](int t) __attribute__((always_inline)) {
-    vid = page_at(t, g16);
-    const uint8_t* base = p.c.v + page_rows(p.c, max(vid, 0), h) * D + (D / 16) * j16;
-    const int r0 = (t * kRows + 16 * g16) & pmask;
+  auto load_v = [&](int t, int id) __attribute__((always_inline)) {
+    const uint8_t* base = p.c.v + page_rows(p.c, max(id, 0), h) * D + (D / 16) * j16;
+    const uint32_t r0 = (t * kR + kG * g16) & pmask;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      vc[e] = __builtin_nontemporal_load(reinterpret_cast<const vword*>(base + (int64_t)(r0 + e) * D));
+    for (int e = 0; e < kG; ++e)
+      vc[e] = __builtin_nontemporal_load(reinterpret_cast<const vword*>(base + (r0 + e) * D));
+  };
+  auto ids = [&](int t) __attribute__((always_inline)) {
+    kid = page_at(t, j16 >> 2);
+    vid = page_at(t, g16);
   };
 
   int t = tb + wave;
   if (t < te) {
+    ids(t);
     load_k(t);
-    load_v(t);
+    load_v(t, vid);
+    cur = vid;
+    ids(t + kDecWaves);
   }
 #pragma unroll 1
   for (; t < te; t += kDecWaves) {
+    const int64_t vrow = page_rows(p.c, max(cur, 0), h) + ((t * kR + kG * g16) & pmask);
+    const bool bad = cur < 0;
+    ks = ksn;
+    vs = vsn;
     // S^T = K Q^T, the K codes times their page's scale
-    const float ks = kid < 0 ? 1.f : p.c.k_scale[(int64_t)kid * p.c.H_kv + h];
-    const float vs = vid < 0 ? 1.f : p.c.v_scale[(int64_t)vid * p.c.H_kv + h];
-    const int64_t vrow = page_rows(p.c, max(vid, 0), h) + ((t * kRows + 16 * g16) & pmask);
-    const bool bad = vid < 0;
-    f32x4 s[4];
+    f32x4 s[kTS];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < kTS; ++x) {
       s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < kP; ++c) {
@@ -164,21 +220,25 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
       }
     }
     const bool more = t + kDecWaves < te;
-    if (more) load_k(t + kDecWaves);            // in flight over the softmax and the second product
-    const int r0 = t * kRows + 16 * g16;        // first of this lane's 16 rows
+    const int nid = vid;                        // V page of the next tile
+    if (more) {                                 // in flight over the softmax and the second product
+      load_k(t + kDecWaves);
+      ids(t + 2 * kDecWaves);
+    }
+    const int r0 = t * kR + kG * g16;           // first of this lane's rows
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < kTS; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[x][e] = p.softcap > 0.f ? capped(s[x][e], c1, c2) : s[x][e] * c1;
-    const bool partial = t * kRows < rg.lo || t * kRows + kRows > rg.hi || __any(bad);
+    const bool partial = t * kR < rg.lo || t * kR + kR > rg.hi || __any(bad);
     unsigned hidden = 0;                        // bit 4 x + e: that row is not seen
     if (partial) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) hidden |= (bad || r0 + i < rg.lo || r0 + i >= rg.hi ? 1u : 0u) << i;
+      for (int i = 0; i < kG; ++i) hidden |= (bad || r0 + i < rg.lo || r0 + i >= rg.hi ? 1u : 0u) << i;
     }
     if (by_pos) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < kTS; ++x) {
         const int4 kp = *reinterpret_cast<const int4*>(p.c.pos + vrow + 4 * x);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -189,11 +249,11 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
       }
     } else if (p.slopes) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] -= slope * (float)abs(qpos - (r0 + i));
+      for (int i = 0; i < kG; ++i) s[i >> 2][i & 3] -= slope * (float)abs(qpos - (r0 + i));
     }
     if (__any(hidden != 0)) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kG; ++i) {
         const bool off = hidden >> i & 1;
         s[i >> 2][i & 3] = off ? -INFINITY : s[i >> 2][i & 3];
         if (off) {                              // what the row holds must not meet a weight of 0
@@ -204,13 +264,14 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
     if (p.accumulate && live) {
       float* at = p.scores + ((int64_t)n * p.H + hq) * p.score_cap + r0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) *reinterpret_cast<f32x4*>(at + 4 * x) = s[x];
+      for (int x = 0; x < kTS; ++x) *reinterpret_cast<f32x4*>(at + 4 * x) = s[x];
     }
     float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
 #pragma unroll
-    for (int x = 1; x < 4; ++x) mx = fmaxf(mx, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
-    mx = fmaxf(m, max_over_groups(mx));
-    if (__any(mx > m)) {
+    for (int x = 1; x < kTS; ++x) mx = fmaxf(mx, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
+    mx = max_over_groups(mx);
+    if (__any(mx > m + 8.f)) {                  // (the maximum in use may lag the true one by 2^8)
+      mx = fmaxf(m, mx);
       const float f = __builtin_amdgcn_exp2f(m == mx ? 0.f : m - mx);
       m = mx;
       l *= f;
@@ -219,19 +280,21 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
     }
     const float base = m == -INFINITY ? 0.f : m;   // a column that has seen nothing yet
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < kTS; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         s[x][e] = __builtin_amdgcn_exp2f(s[x][e] - base);
         l += s[x][e];
       }
-    const bf16x8 p0 = pair_to_op(s[0], s[1]), p1 = pair_to_op(s[2], s[3]);
+    bf16x8 pb[kTS / 2];
+#pragma unroll
+    for (int x = 0; x < kTS / 2; ++x) pb[x] = pair_to_op(s[2 * x], s[2 * x + 1]);
     // O^T += V^T P^T
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      uint32_t tr[4][4];                        // [rows 4 i ..][column]: four rows of one column
+      uint32_t tr[kTS][4];                      // [rows 4 i ..][column]: four rows of one column
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kTS; ++i) {
         const uint32_t a0 = word_of<kW>(vc[4 * i], w), a1 = word_of<kW>(vc[4 * i + 1], w);
         const uint32_t a2 = word_of<kW>(vc[4 * i + 2], w), a3 = word_of<kW>(vc[4 * i + 3], w);
         const uint32_t lo01 = __builtin_amdgcn_perm(a1, a0, 0x05010400), hi01 = __builtin_amdgcn_perm(a1, a0, 0x07030602);
@@ -242,12 +305,13 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
         tr[i][3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302);
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        o[4 * w + c] = mfma1632(f8x8_to_op(tr[0][c], tr[1][c], vs), p0, o[4 * w + c]);
-        o[4 * w + c] = mfma1632(f8x8_to_op(tr[2][c], tr[3][c], vs), p1, o[4 * w + c]);
-      }
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int x = 0; x < kTS / 2; ++x)
+          o[4 * w + c] = mfma1632(f8x8_to_op(tr[2 * x][c], tr[2 * x + 1][c], vs), pb[x], o[4 * w + c]);
     }
-    if (more) load_v(t + kDecWaves);
+    if (more) load_v(t + kDecWaves, nid);
+    cur = nid;
   }
 
   // Join the waves: waves 2, 3 hand theirs to waves 0, 1, then wave 1 to wave 0.
@@ -280,7 +344,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
     __syncthreads();
   }
   if (wave != 0 || !live) return;
-  const bool alone = rg.t1 - rg.t0 <= rg.per;   // no other split holds tiles
+  const bool alone = rg.t1 - rg.t0 <= rg.per;   // no other split holds chunks
   if (alone) {
     const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // (a NaN sum stays NaN)
     u16* at = p.out + n * p.out_stride + (int64_t)hq * D;
@@ -308,40 +372,48 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const AttnDecodeLau
 // Join: blockIdx.x = 0 .. H - 1: the partial outputs of one query head; the blocks behind
 // (accumulate): 1024 rows of one kv head, four per thread.
 constexpr int kAccRows = 4 * kDecThreads;
+constexpr int kMaxSplits = kDecThreads;
 
 template <int D>
 __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDecodeLaunch p) {
-  __shared__ float sM[64], sInv[64];
-  __shared__ float sPart[kDecThreads];
+  __shared__ float sM[64], sInv[64], sPart[8];
   const int tid = threadIdx.x, n = blockIdx.y;
   int qpos;
   const DecRange rg = dec_range(p, n, qpos);
   if (p.kv_len[n] < 0) return;
-  const int tiles = rg.t1 - rg.t0, used = (tiles + rg.per - 1) / rg.per;   // splits that hold tiles
+  const int used = (rg.t1 - rg.t0 + rg.per - 1) / rg.per;   // splits that hold chunks
   if ((int)blockIdx.x < p.H) {
     if (used <= 1) return;                      // written by the first launch
+    __shared__ float sF[kMaxSplits];
+    __shared__ f32x4 sAcc[kDecThreads];
     const int64_t row = ((int64_t)n * p.H + blockIdx.x) * p.splits;
-    const float* ml = p.part_ml + row * 2;
-    float m = -INFINITY;
-    for (int s = 0; s < used; ++s) m = fmaxf(m, ml[2 * s]);
+    // factors of the partial sums: a thread per split (kMaxSplits = kDecThreads)
+    const f32x2 ml = tid < used ? *reinterpret_cast<const f32x2*>(p.part_ml + (row + tid) * 2) : f32x2{-INFINITY, 0.f};
+    float m = ml.x;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+    if ((tid & 63) == 0) sPart[tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sPart[0], sPart[1]), fmaxf(sPart[2], sPart[3]));
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+    sF[tid] = f;
+    float l = ml.y * f;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, kWave);
+    if ((tid & 63) == 0) sPart[4 + (tid >> 6)] = l;
+    __syncthreads();
+    l = sPart[4] + sPart[5] + sPart[6] + sPart[7];
     constexpr int kC = D / 4;                   // four columns per thread, kDecThreads / kC splits at a time
     const int c = tid % kC, part = tid / kC;
-    float l = 0.f;
+    const float* src = p.part_o + row * D + 4 * c;
     f32x4 o{0.f, 0.f, 0.f, 0.f};
-    for (int s = part; s < used; s += kDecThreads / kC) {
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[2 * s] - m);
-      l += ml[2 * s + 1] * f;
-      o += *reinterpret_cast<const f32x4*>(p.part_o + (row + s) * D + 4 * c) * f;
-    }
-    __shared__ f32x4 sAcc[kDecThreads];
+#pragma unroll 4
+    for (int s = part; s < used; s += kDecThreads / kC) o += *reinterpret_cast<const f32x4*>(src + (int64_t)s * D) * sF[s];
     sAcc[tid] = o;
-    sPart[tid] = l;
     __syncthreads();
     if (part == 0) {
-      for (int i = 1; i < kDecThreads / kC; ++i) {
-        o += sAcc[tid + i * kC];
-        l += sPart[tid + i * kC];
-      }
+#pragma unroll
+      for (int i = 1; i < kDecThreads / kC; ++i) o += sAcc[tid + i * kC];
       const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
       *reinterpret_cast<uint2*>(p.out + n * p.out_stride + (int64_t)blockIdx.x * D + 4 * c) =
           make_uint2(cvt2(o[0] * inv, o[1] * inv), cvt2(o[2] * inv, o[3] * inv));
@@ -351,7 +423,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDeco
   // accumulated weights
   const int G = p.H / p.c.H_kv;
   const int blk = blockIdx.x - p.H, h = blk % p.c.H_kv;
-  const int64_t first = (int64_t)(blk / p.c.H_kv) * kAccRows + (int64_t)rg.t0 * kRows;
+  const int64_t first = (int64_t)(blk / p.c.H_kv) * kAccRows + (int64_t)rg.t0 * kChunk;
   if (first >= rg.hi || used == 0) return;
   const int r = (int)first + 4 * tid;
   f32x4 w{0.f, 0.f, 0.f, 0.f};
@@ -391,22 +463,27 @@ hipError_t launch_d(const AttnDecodeLaunch& p, int64_t max_rows, hipStream_t s) 
   decode_kernel<D><<<dim3((unsigned)blocks), kDecThreads, 0, s>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.splits == 1 && !p.accumulate)) return e;
-  // (a range of max_rows rows can begin inside a tile)
-  const int64_t acc = p.accumulate ? (max_rows + kRows + kAccRows - 1) / kAccRows * p.c.H_kv : 0;
+  // (a range of max_rows rows can begin inside a chunk)
+  const int64_t acc = p.accumulate ? (max_rows + kChunk + kAccRows - 1) / kAccRows * p.c.H_kv : 0;
   decode_join_kernel<D><<<dim3((unsigned)(p.H + acc), (unsigned)p.N), kDecThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Splits per (sequence, kv head, 16 query heads): enough workgroups for four on each CU,
-// none with less than two tiles per wave.
-int attn_decode_splits(int64_t N, int H, int H_kv, int64_t max_rows, int cus) {
-  const int64_t base = N * H_kv * ((H / H_kv + 15) / 16);
-  const int64_t want = (4 * (int64_t)cus + base - 1) / base;
-  const int64_t most = (max_rows + 2 * kDecWaves * kRows - 1) / (2 * kDecWaves * kRows);
-  int64_t s = want < most ? want : most;
-  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+// How a call is cut: splits per (sequence, kv head, 16 query heads), the fewest chunks that
+// one takes, and whether the longest sequences come first.  Two workgroups fit a CU.  A few
+// sequences are cut into one round of workgroups (2 x 131000 rows, d = 256: 59 us, in two
+// rounds 70); more of them may differ in length, and two rounds (32 sequences of 2000 to
+// 8192 rows: 92 us, in four 106) with the longest first even that out.
+void plan_attn_decode(AttnDecodeLaunch& p, int64_t max_rows, int cus) {
+  const int64_t base = (int64_t)p.N * p.c.H_kv * ((p.H / p.c.H_kv + 15) / 16), chunks = (max_rows + kChunk - 1) / kChunk;
+  p.min_chunks = 2 * (p.c.d == 256 ? 2 : 4);    // two tiles per wave
+  const int64_t want = ((p.N >= 8 ? 4 : 2) * (int64_t)cus + base - 1) / base;
+  const int64_t most = (chunks + p.min_chunks - 1) / p.min_chunks;
+  const int64_t s = want < most ? want : most;
+  p.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+  p.ranked = p.N > 1 && p.N <= kRanked && base * p.splits > 2 * cus;
 }
 
 hipError_t launch_attn_decode(const AttnDecodeLaunch& p, hipStream_t s) {

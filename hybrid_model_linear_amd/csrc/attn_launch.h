@@ -81,6 +81,8 @@ struct AttnDecodeLaunch {
   float scale;
   float softcap;
   int accumulate;
+  int min_chunks;           // fewest 64-row chunks of a split
+  int ranked;               // workgroups in order of the sequences' lengths
   int splits;               // workgroups per (sequence, kv head, group of 16 query heads)
   float* part_o;            // [N, H, splits, d] partial sums (splits > 1)
   float* part_ml;           // [N, H, splits, 2] running maximum and sum (splits > 1 or accumulate)
@@ -103,7 +105,7 @@ struct EvictLaunch {
 
 hipError_t launch_kv_store(const StoreLaunch& p, hipStream_t stream);
 hipError_t launch_attn_extend(const AttnExtendLaunch& p, hipStream_t stream);
-int attn_decode_splits(int64_t N, int H, int H_kv, int64_t max_rows, int cus);
+void plan_attn_decode(AttnDecodeLaunch& p, int64_t max_rows, int cus);   // splits, min_chunks, ranked
 hipError_t launch_attn_decode(const AttnDecodeLaunch& p, hipStream_t stream);
 hipError_t launch_kv_evict(const EvictLaunch& p, hipStream_t stream);
 
