@@ -116,6 +116,7 @@ int plan_evict(const gdn_kv_evict_args* a, gdn::EvictLaunch& p, int64_t& need) {
   const int st = check_cache(a->cache, a->block_table, a->table_stride, a->table_width, true, p.c);
   if (st != GDN_OK) return st;
   if (a->N > 0 && (!a->kv_len || !a->new_len)) return GDN_E_NULL;
+  if (a->cache.num_pages > INT32_MAX / a->cache.page) return GDN_E_UNSUPPORTED;   // rows of the cache: 32-bit in the kernel
   p.N = a->N;
   // (a budget past the table's rows keeps them all)
   const int64_t rows = (int64_t)a->table_width * a->cache.page;
@@ -160,7 +161,7 @@ int gdn_kv_store(const gdn_kv_store_args* a, void* stream) {
   if (a->N > 0 && !a->cache_len) return GDN_E_NULL;
   if (!rows_ok(a->k, a->k_stride, p.c.H_kv, p.c.d) || !rows_ok(a->v, a->v_stride, p.c.H_kv, p.c.d)) return GDN_E_SHAPE;
   if (a->N == 0 || a->T == 0) return GDN_OK;
-  if ((a->T >> p.c.page_log2) + 2 * (int64_t)a->N > kMaxGrid) return GDN_E_UNSUPPORTED;
+  if (((a->T >> p.c.page_log2) + 2 * (int64_t)a->N) * p.c.H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.T = a->T;
   p.k = static_cast<const gdn::u16*>(a->k);

@@ -50,6 +50,19 @@ __device__ __forceinline__ int64_t page_rows(const CacheRef& c, int page, int h)
   return ((int64_t)page * c.H_kv + h) << c.page_log2;
 }
 
+// Largest n in [0, N) with le(n), for le true at 0 and then false from some n on: 64 probes
+// at a time, the same in every lane of a wave (which all take part).
+template <typename F> __device__ __forceinline__ int find_last(int N, int lane, F le) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + kWave - 1) / kWave, i = lo + lane * step;
+    const int n = __builtin_popcountll(__ballot(i < hi && (lane == 0 || le(i))));
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // Raw score q.k -> score in units of log2, after scale and cap: with f1 = scale / cap and
 // f2 = cap log2 e:  f2 tanh(f1 x), tanh(y) = 1 - 2 / (1 + e^2y).  Near 0 that form is
 // off by a few 2^-24 absolutely, i.e. by cap 2^-22 in the score: below the error of the

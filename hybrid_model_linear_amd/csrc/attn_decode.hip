@@ -182,7 +182,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
     ksn = kid < 0 ? 1.f : p.c.k_scale[(int64_t)kid * p.c.H_kv + h];
     vsn = vid < 0 ? 1.f : p.c.v_scale[(int64_t)vid * p.c.H_kv + h];
   };
+  int4 pc[kTS];                                 // positions of the rows
   auto load_v = [&](int t, int id) __attribute__((always_inline)) {
+    if (by_pos) {
+      const int32_t* at = p.c.pos + page_rows(p.c, max(id, 0), h) + ((t * kR + kG * g16) & pmask);
+#pragma unroll
+      for (int x = 0; x < kTS; ++x) pc[x] = *reinterpret_cast<const int4*>(at + 4 * x);
+    }
     const uint8_t* base = p.c.v + page_rows(p.c, max(id, 0), h) * D + (D / 16) * j16;
     const uint32_t r0 = (t * kR + kG * g16) & pmask;
 #pragma unroll
@@ -204,7 +210,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
   }
 #pragma unroll 1
   for (; t < te; t += kDecWaves) {
-    const int64_t vrow = page_rows(p.c, max(cur, 0), h) + ((t * kR + kG * g16) & pmask);
     const bool bad = cur < 0;
     ks = ksn;
     vs = vsn;
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
     if (by_pos) {
 #pragma unroll
       for (int x = 0; x < kTS; ++x) {
-        const int4 kp = *reinterpret_cast<const int4*>(p.c.pos + vrow + 4 * x);
+        const int4 kp = pc[x];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int dist = abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w));
@@ -430,22 +435,38 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDeco
   for (int g0 = 0; g0 < G; g0 += 64) {
     const int gn = min(64, G - g0);
     __syncthreads();
-    if (tid < gn) {
-      const float* ml = p.part_ml + ((int64_t)n * p.H + h * G + g0 + tid) * p.splits * 2;
+    for (int g = tid >> 6; g < gn; g += kDecWaves) {   // a wave per head, a lane per split
+      const f32x2* ml = reinterpret_cast<const f32x2*>(p.part_ml) + ((int64_t)n * p.H + h * G + g0 + g) * p.splits;
+      f32x2 v[kMaxSplits / kWave];
       float m = -INFINITY, l = 0.f;
-      for (int s = 0; s < used; ++s) m = fmaxf(m, ml[2 * s]);
-      if (m > -INFINITY)
-        for (int s = 0; s < used; ++s) l += ml[2 * s + 1] * __builtin_amdgcn_exp2f(ml[2 * s] - m);
-      sM[tid] = m > -INFINITY ? m : 0.f;
-      sInv[tid] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+      for (int i = 0; i < kMaxSplits / kWave; ++i) {
+        const int s = i * kWave + (tid & 63);
+        v[i] = f32x2{-INFINITY, 0.f};
+        if (s < used) v[i] = ml[s];
+        m = fmaxf(m, v[i].x);
+      }
+#pragma unroll
+      for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+      const float base = m > -INFINITY ? m : 0.f;
+#pragma unroll
+      for (int i = 0; i < kMaxSplits / kWave; ++i) l += v[i].y * __builtin_amdgcn_exp2f(v[i].x - base);
+#pragma unroll
+      for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, kWave);
+      if ((tid & 63) == 0) {
+        sM[g] = base;
+        sInv[g] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+      }
     }
     __syncthreads();
-    if (r < rg.hi)
+    if (r < rg.hi) {
+#pragma unroll 4
       for (int g = 0; g < gn; ++g) {
         const f32x4 s = *reinterpret_cast<const f32x4*>(p.scores + ((int64_t)n * p.H + h * G + g0 + g) * p.score_cap + r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(s[e] - sM[g]) * sInv[g];
       }
+    }
   }
   if (r >= rg.hi) return;
   const int id = page_of(p.c, n, r);

@@ -101,12 +101,8 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const int h = blockIdx.x % p.H_kv;
   const int w = (int)(gridDim.x / p.H_kv) - 1 - (int)(blockIdx.x / p.H_kv);
   // slot w -> (sequence n, tile): sequence n's tiles begin at floor(cu[n] G / 128) + n
-  int lo = 0, hi = p.N;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu[mid] * G / kBM + mid <= w) lo = mid; else hi = mid;
-  }
-  const int n = lo, t0 = p.cu[n], L = p.cu[n + 1] - t0;
+  const int n = find_last(p.N, threadIdx.x & 63, [&](int i) { return p.cu[i] * G / kBM + i <= w; });
+  const int t0 = p.cu[n], L = p.cu[n + 1] - t0;
   const int rows = L * G, f0 = (w - (t0 * G / kBM + n)) * kBM;   // (T G stays below 2^31)
   if (f0 < 0 || f0 >= rows) return;
   int P = CACHED ? p.cache_len[n] : 0;                  // cached rows

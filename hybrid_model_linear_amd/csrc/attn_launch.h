@@ -98,7 +98,7 @@ struct EvictLaunch {
   const int32_t* kv_len;
   int32_t* new_len;
   int32_t* holes;           // [N, H_kv, budget] rows to fill, ascending
-  int32_t* movers;          // [N, H_kv, budget] rows that fill them
+  int32_t* movers;          // [N, H_kv, budget] rows that fill them (rows of the whole cache, one head's)
   float* scales;            // [N, H_kv, budget, 2] k and v scale of the movers' pages
   int32_t* first;           // [N, H_kv, pages + 1] first entry of `holes` in each page before budget
 };

@@ -19,6 +19,63 @@ namespace gdn {
 namespace {
 
 constexpr int kStoreThreads = 256;
+constexpr int kFewTokens = 8;     // per sequence on average: a wave per page and head, else a workgroup
+
+// The page of a store slot: rows [r0, r1) of it are new, its row 0 is (or would be) token
+// tok0.  Sequence n has the slots floor(cu[n] / page) + 2 n + j for its j-th touched page: it
+// touches at most floor(L / page) + 2, so slots of different sequences never meet and no
+// prefix pass is needed.  False: nothing to do.
+struct StoreSlot {
+  int n, id, r0, r1, old;
+  int64_t first, tok0;
+};
+__device__ __forceinline__ bool store_slot(const StoreLaunch& p, int w, int lane, StoreSlot& s) {
+  const int lg = p.c.page_log2, page = 1 << lg;
+  int j = 0, t0 = w, len = 1;
+  s.n = w;
+  if (p.cu) {
+    s.n = find_last(p.N, lane, [&](int i) { return (p.cu[i] >> lg) + 2 * i <= w; });
+    t0 = p.cu[s.n];
+    len = p.cu[s.n + 1] - t0;
+    j = w - ((t0 >> lg) + 2 * s.n);
+  }
+  s.old = p.cache_len[s.n];
+  if (s.old < 0 || len <= 0 || j < 0) return false;
+  s.first = ((int64_t)(s.old >> lg) + j) << lg;                    // the page's first row
+  const int64_t end = (int64_t)s.old + len;
+  if (s.first >= end || s.first > INT32_MAX - page) return false;
+  s.r0 = s.old > s.first ? (int)(s.old - s.first) : 0;
+  s.r1 = end - s.first < page ? (int)(end - s.first) : page;
+  s.id = page_of(p.c, s.n, (int)s.first);
+  s.tok0 = (int64_t)t0 + (s.first - s.old);
+  return s.id >= 0;
+}
+// largest finite magnitude bits of eight bf16, NaN and infinities left out
+__device__ __forceinline__ unsigned top_of(const u32x4& x, unsigned top) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const unsigned a = x[e] & 0x7fff, b = x[e] >> 16 & 0x7fff;
+    top = max(top, max(a < 0x7f80 ? a : 0u, b < 0x7f80 ? b : 0u));
+  }
+  return top;
+}
+// eight bf16 as codes; NaN and infinities become NaN
+__device__ __forceinline__ uint2 codes_of(const u32x4& x, float inv) {
+  float f[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = bf_lo(x[q]);
+    f[2 * q + 1] = bf_hi(x[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    f[q] = (__float_as_uint(f[q]) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : f[q] * inv;
+  return make_uint2(to_f8x4(f[0], f[1], f[2], f[3]), to_f8x4(f[4], f[5], f[6], f[7]));
+}
+__device__ __forceinline__ void store_track(const StoreLaunch& p, const StoreSlot& s, int64_t row0, int r) {
+  if (p.c.pos) p.c.pos[row0 + r] = (p.start ? p.start[s.n] : s.old) + (int)(s.first + r - s.old);
+  if (p.c.weight) p.c.weight[row0 + r] = 0.f;
+}
 
 // NP: passes of 256 threads over a page's 16-byte (8 element) pieces, page * d / 8 / 256.
 template <int D, int NP>
@@ -26,38 +83,11 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreLaun
   constexpr int kPer = D / 8;                       // pieces of a row
   __shared__ unsigned sTop[kStoreThreads / kWave];
   const int tid = threadIdx.x, h = blockIdx.y, isv = blockIdx.z;
-  const int lg = p.c.page_log2, page = 1 << lg;
-  // block -> (sequence n, its j-th touched page).  Sequence n has the slots
-  // floor(cu[n] / page) + 2 n + j: it touches at most floor(L / page) + 2 pages, so slots
-  // of different sequences never meet and no prefix pass is needed.
-  int n, j = 0, t0, len;
-  if (p.cu == nullptr) {
-    n = blockIdx.x;
-    t0 = n;
-    len = 1;
-  } else {
-    const int w = blockIdx.x;
-    int lo = 0, hi = p.N;                           // largest n with slot0(n) <= w
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((p.cu[mid] >> lg) + 2 * mid <= w) lo = mid; else hi = mid;
-    }
-    n = lo;
-    t0 = p.cu[n];
-    len = p.cu[n + 1] - t0;
-    j = w - ((t0 >> lg) + 2 * n);
-  }
-  const int old = p.cache_len[n];
-  if (old < 0 || len <= 0 || j < 0) return;
-  const int64_t first = ((int64_t)(old >> lg) + j) << lg;          // the page's first row
-  const int64_t end = (int64_t)old + len;
-  if (first >= end || first > INT32_MAX - page) return;
-  const int r0 = old > first ? (int)(old - first) : 0;             // new rows [r0, r1) of the page
-  const int r1 = end - first < page ? (int)(end - first) : page;
-  const int id = page_of(p.c, n, (int)first);
-  if (id < 0) return;
+  StoreSlot st;
+  if (!store_slot(p, blockIdx.x, tid & 63, st)) return;
+  const int r0 = st.r0, r1 = st.r1, id = st.id;
+  const int64_t tok0 = st.tok0;
   const int64_t row0 = page_rows(p.c, id, h);
-  const int64_t tok0 = (int64_t)t0 + (first - old);                // token of the page's row 0
   const u16* src = isv ? p.v : p.k;
   const int64_t stride = isv ? p.v_stride : p.k_stride;
   uint8_t* codes = (isv ? p.c.v : p.c.k) + row0 * D;
@@ -73,12 +103,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreLaun
       x[s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + (tok0 + r) * stride + (int64_t)h * D + c * 8));
   }
 #pragma unroll
-  for (int s = 0; s < NP; ++s)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned a = x[s][e] & 0x7fff, b = x[s][e] >> 16 & 0x7fff;
-      top = max(top, max(a < 0x7f80 ? a : 0u, b < 0x7f80 ? b : 0u));
-    }
+  for (int s = 0; s < NP; ++s) top = top_of(x[s], top);
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, o, kWave));
   if ((tid & 63) == 0) sTop[tid >> 6] = top;
@@ -107,24 +132,59 @@ __global__ void __launch_bounds__(kStoreThreads) kv_store_kernel(const StoreLaun
 #pragma unroll
   for (int s = 0; s < NP; ++s) {
     const int i = tid + s * kStoreThreads, r = i / kPer, c = i % kPer;
-    if (r >= r0 && r < r1) {
-      float f[8];
+    if (r >= r0 && r < r1) *reinterpret_cast<uint2*>(codes + (int64_t)r * D + c * 8) = codes_of(x[s], inv);
+  }
+  if (!isv && tid >= r0 && tid < r1) store_track(p, st, row0, tid);
+}
+
+// The same for a few tokens per sequence (decode steps, verify batches): a wave per (page, kv
+// head, K or V), four to a workgroup; the new rows' first 64 pieces stay in registers, more
+// are read twice.  256 sequences, 1 token each, 8 heads of 128: 15.3 us with the kernel above.
+template <int D>
+__global__ void __launch_bounds__(kStoreThreads) kv_store_few_kernel(const StoreLaunch p, int64_t items) {
+  constexpr int kPer = D / 8;
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * (kStoreThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (item >= items) return;
+  const int isv = item & 1, h = (int)((item >> 1) % p.c.H_kv);
+  StoreSlot st;
+  if (!store_slot(p, (int)((item >> 1) / p.c.H_kv), lane, st)) return;
+  const int64_t row0 = page_rows(p.c, st.id, h);
+  const int64_t stride = isv ? p.v_stride : p.k_stride;
+  const u16* src = (isv ? p.v : p.k) + (st.tok0 + st.r0) * stride + (int64_t)h * D;
+  uint8_t* codes = (isv ? p.c.v : p.c.k) + row0 * D;
+  float* scale_at = (isv ? p.c.v_scale : p.c.k_scale) + (int64_t)st.id * p.c.H_kv + h;
+  const float was = st.r0 ? *scale_at : 0.f;
+  const int count = (st.r1 - st.r0) * kPer;
+  auto piece = [&](int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(src + (i / kPer) * stride + (i % kPer) * 8);
+  };
+  u32x4 x{0, 0, 0, 0};
+  if (lane < count) x = piece(lane);
+  unsigned top = top_of(x, 0);
+  for (int i = lane + kWave; i < count; i += kWave) top = top_of(piece(i), top);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[2 * q] = bf_lo(x[s][q]);
-        f[2 * q + 1] = bf_hi(x[s][q]);
+  for (int o = 32; o; o >>= 1) top = max(top, (unsigned)__shfl_xor((int)top, o, kWave));
+  int e = scale_exp_of(top);
+  if (st.r0) {
+    const int eo = min(exp_of(was), 120);
+    if (e > eo) {                                   // the scale grows: round the earlier rows to it
+      const float shrink = ldexpf(1.0f, eo - e);
+      for (int i = lane; i < st.r0 * kPer; i += kWave) {
+        uint2* at = reinterpret_cast<uint2*>(codes) + i;
+        const uint2 w = *at;
+        *at = make_uint2(f8x4_rescale(w.x, shrink), f8x4_rescale(w.y, shrink));
       }
-#pragma unroll
-      for (int q = 0; q < 8; ++q)                   // NaN and infinities become NaN
-        f[q] = (__float_as_uint(f[q]) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : f[q] * inv;
-      *reinterpret_cast<uint2*>(codes + (int64_t)r * D + c * 8) =
-          make_uint2(to_f8x4(f[0], f[1], f[2], f[3]), to_f8x4(f[4], f[5], f[6], f[7]));
     }
+    e = max(e, eo);
   }
-  if (!isv && tid < page && tid >= r0 && tid < r1) {
-    if (p.c.pos) p.c.pos[row0 + tid] = (p.start ? p.start[n] : old) + (int)(first + tid - old);
-    if (p.c.weight) p.c.weight[row0 + tid] = 0.f;
-  }
+  if (lane == 0) *scale_at = exp2_int(e);           // (read by every lane above)
+  const float inv = exp2_int(-e);
+  uint2* to = reinterpret_cast<uint2*>(codes + (int64_t)st.r0 * D);
+  if (lane < count) to[lane] = codes_of(x, inv);
+  for (int i = lane + kWave; i < count; i += kWave) to[i] = codes_of(piece(i), inv);
+  if (!isv)
+    for (int r = st.r0 + lane; r < st.r1; r += kWave) store_track(p, st, row0, r);
 }
 
 template <int D>
@@ -144,6 +204,7 @@ hipError_t store_by_page(const StoreLaunch& p, dim3 grid, hipStream_t s) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / kWave;
 constexpr int kBins = 2048;
+constexpr int kCopies = 4;
 
 // Weight -> unsigned key of the same order: NaN below every number, -0 equal to +0, and
 // 0xffffffff left for the newest rows.
@@ -162,8 +223,11 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
   return v;
 }
 
+// KG: groups of four rows that a thread holds in registers (the whole sequence: 4096 KG
+// rows); 0: any length, rows are read again for every pass.
+template <int KG>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLaunch p) {
-  __shared__ int sHist[kBins];
+  __shared__ int sHist[kCopies][kBins];
   __shared__ int sWave[3][kSelWaves];
   __shared__ int sPick[2];
   const int tid = threadIdx.x, wave = tid >> 6, h = blockIdx.x, n = blockIdx.y;
@@ -173,70 +237,105 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
   const int64_t slot = (int64_t)n * p.c.H_kv + h;
   const int pages = (p.budget + (1 << lg) - 1) >> lg;
   int* first = p.first + slot * (pages + 1);
-  // pages all in range? (a sequence with a bad page is left as it is)
-  bool ok = len > p.budget;
-  if (ok)
-    for (int j = tid; j << lg < len; j += kSelThreads) ok = ok && page_of(p.c, n, j << lg) >= 0;
-  if (!__syncthreads_and(ok)) {
-    if (tid == 0) first[pages] = len > p.budget ? -1 : 0;   // -1: left alone, 0: nothing to move
+  if (len <= p.budget) {
+    if (tid == 0) first[pages] = 0;                 // nothing to move
     return;
   }
-  // Four rows (r0 .. r0 + 3, one page) at a time: their keys given the newest position.
-  auto load = [&](int r0, int4& pos, f32x4& w, int64_t& row) __attribute__((always_inline)) {
-    const int id = page_of(p.c, n, r0);
-    row = page_rows(p.c, id, h) + (r0 & ((1 << lg) - 1));
-    pos = *reinterpret_cast<const int4*>(p.c.pos + row);
-    w = *reinterpret_cast<const f32x4*>(p.c.weight + row);
-  };
-  int last = INT32_MIN;
-  for (int r0 = 4 * tid; r0 < len; r0 += 4 * kSelThreads) {
+  // Four rows (r0 .. r0 + 3, one page) at a time; a row's place is its row over the whole
+  // cache (page id and row in it; -1: a bad page).
+  struct Rows {
     int4 pos;
     f32x4 w;
-    int64_t row;
-    load(r0, pos, w, row);
-    last = max(last, pos.x);
-    if (r0 + 1 < len) last = max(last, pos.y);
-    if (r0 + 2 < len) last = max(last, pos.z);
-    if (r0 + 3 < len) last = max(last, pos.w);
+    int at;
+  };
+  auto load = [&](int r0) __attribute__((always_inline)) {
+    Rows x;
+    const int id = r0 < len ? page_of(p.c, n, r0) : -1, r = r0 & ((1 << lg) - 1);
+    x.at = id < 0 ? -1 : (id << lg) + r;
+    const int64_t row = page_rows(p.c, max(id, 0), h) + r;
+    x.pos = *reinterpret_cast<const int4*>(p.c.pos + row);
+    x.w = *reinterpret_cast<const f32x4*>(p.c.weight + row);
+    return x;
+  };
+  Rows held[KG ? KG : 1];
+  const int steps = KG ? KG : (len + 4 * kSelThreads - 1) / (4 * kSelThreads);
+  auto row_of = [&](int s) __attribute__((always_inline)) { return 4 * (s * kSelThreads + tid); };
+  int last = INT32_MIN;
+  bool ok = true;                                   // a sequence with a bad page is left as it is
+  auto look = [&](const Rows& x, int r0) __attribute__((always_inline)) {
+    ok = ok && (x.at >= 0 || r0 >= len);
+    if (r0 < len) last = max(last, x.pos.x);
+    if (r0 + 1 < len) last = max(last, x.pos.y);
+    if (r0 + 2 < len) last = max(last, x.pos.z);
+    if (r0 + 3 < len) last = max(last, x.pos.w);
+  };
+  if constexpr (KG > 0) {
+#pragma unroll
+    for (int s = 0; s < KG; ++s) held[s] = load(row_of(s));
+#pragma unroll
+    for (int s = 0; s < KG; ++s) look(held[s], row_of(s));
+  } else {
+    for (int s = 0; s < steps; ++s) look(load(row_of(s)), row_of(s));
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) last = max(last, __shfl_xor(last, o, kWave));
   if ((tid & 63) == 0) sWave[0][wave] = last;
-  __syncthreads();
+  if (!__syncthreads_and(ok)) {
+    if (tid == 0) first[pages] = -1;                // left alone
+    return;
+  }
   for (int i = 0; i < kSelWaves; ++i) last = max(last, sWave[0][i]);
   const int64_t newest = (int64_t)last - p.recent;
-  auto keys = [&](int r0, unsigned (&k)[4]) __attribute__((always_inline)) {
-    int4 pos;
-    f32x4 w;
-    int64_t row;
-    load(r0, pos, w, row);
-    k[0] = pos.x > newest ? 0xffffffffu : weight_key(w[0]);
-    k[1] = pos.y > newest ? 0xffffffffu : weight_key(w[1]);
-    k[2] = pos.z > newest ? 0xffffffffu : weight_key(w[2]);
-    k[3] = pos.w > newest ? 0xffffffffu : weight_key(w[3]);
+  auto keys_of = [&](const Rows& x, unsigned (&k)[4]) __attribute__((always_inline)) {
+    k[0] = x.pos.x > newest ? 0xffffffffu : weight_key(x.w[0]);
+    k[1] = x.pos.y > newest ? 0xffffffffu : weight_key(x.w[1]);
+    k[2] = x.pos.z > newest ? 0xffffffffu : weight_key(x.w[2]);
+    k[3] = x.pos.w > newest ? 0xffffffffu : weight_key(x.w[3]);
   };
+  unsigned kept_keys[KG ? KG : 1][4];
+  if constexpr (KG > 0) {
+#pragma unroll
+    for (int s = 0; s < KG; ++s) keys_of(held[s], kept_keys[s]);
+  }
 
   // Radix selection of the budget-th largest key: digits of 11, 11 and 10 bits.  `want` of
-  // the keys that share the digits found so far are still to be kept.
+  // the keys that share the digits found so far are still to be kept.  (Weights crowd into a
+  // few bins, and lanes that count into one wait for each other: neighbours use copies.)
   unsigned found = 0, mask = 0;
   int want = p.budget;
 #pragma unroll 1
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : kBins;
     __syncthreads();
-    for (int i = tid; i < kBins; i += kSelThreads) sHist[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies * kBins / kSelThreads; ++i) (&sHist[0][0])[tid + i * kSelThreads] = 0;
     __syncthreads();
-    for (int r0 = 4 * tid; r0 < len; r0 += 4 * kSelThreads) {
-      unsigned k[4];
-      keys(r0, k);
+    auto count = [&](const unsigned (&k)[4], int r0) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (r0 + e < len && (k[e] & mask) == found) atomicAdd(&sHist[k[e] >> shift & (bins - 1)], 1);
+        if (r0 + e < len && (k[e] & mask) == found) atomicAdd(&sHist[tid & (kCopies - 1)][k[e] >> shift & (bins - 1)], 1);
+    };
+    if constexpr (KG > 0) {
+#pragma unroll
+      for (int s = 0; s < KG; ++s) count(kept_keys[s], row_of(s));
+    } else {
+      for (int s = 0; s < steps; ++s)
+        if (row_of(s) < len) {
+          unsigned k[4];
+          keys_of(load(row_of(s)), k);
+          count(k, row_of(s));
+        }
     }
     __syncthreads();
     // suffix sums: thread t owns bins 2047 - 2 t and 2046 - 2 t, so a prefix scan over the
     // threads counts from the largest key down
-    const int b1 = kBins - 1 - 2 * tid, c1 = sHist[b1], c0 = sHist[b1 - 1];
+    const int b1 = kBins - 1 - 2 * tid;
+    int c1 = 0, c0 = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      c1 += sHist[i][b1];
+      c0 += sHist[i][b1 - 1];
+    }
     const int inc = wave_scan(c1 + c0);
     if ((tid & 63) == 63) sWave[0][wave] = inc;
     __syncthreads();
@@ -261,11 +360,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
   int* movers = p.movers + slot * p.budget;
   f32x2* scales = reinterpret_cast<f32x2*>(p.scales) + slot * p.budget;
   int equal0 = 0, hole0 = 0, mover0 = 0;
-  for (int base = 0; base < len; base += 4 * kSelThreads) {
-    const int r0 = base + 4 * tid;
-    unsigned k[4] = {0, 0, 0, 0};
+  auto list = [&](const unsigned (&k)[4], int r0, int at) __attribute__((always_inline)) {
     int eq = 0;
-    if (r0 < len) keys(r0, k);
 #pragma unroll
     for (int e = 0; e < 4; ++e) eq += r0 + e < len && k[e] == found;
     const int eqi = wave_scan(eq);
@@ -307,18 +403,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
     if (r0 < p.budget && (r0 & ((1 << lg) - 1)) == 0) first[r0 >> lg] = hb;
     f32x2 sc{0.f, 0.f};
     if (nm) {
-      const int64_t at = (int64_t)page_of(p.c, n, r0) * p.c.H_kv + h;
-      sc = f32x2{p.c.k_scale[at], p.c.v_scale[at]};
+      const int64_t pg = (int64_t)(at >> lg) * p.c.H_kv + h;
+      sc = f32x2{p.c.k_scale[pg], p.c.v_scale[pg]};
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (hole[e]) holes[hb++] = r0 + e;
       if (mover[e]) {
-        movers[mb] = r0 + e;
+        movers[mb] = at + e;
         scales[mb++] = sc;
       }
     }
     __syncthreads();                                // sWave is written again by the next rows
+  };
+  if constexpr (KG > 0) {
+#pragma unroll
+    for (int s = 0; s < KG; ++s)
+      if (4 * s * kSelThreads < len) list(kept_keys[s], row_of(s), held[s].at);
+  } else {
+    for (int s = 0; s < steps; ++s) {
+      unsigned k[4];
+      const Rows x = load(row_of(s));
+      keys_of(x, k);
+      list(k, row_of(s), x.at);
+    }
   }
   if (tid == 0) first[pages] = hole0;               // = mover0: budget rows are kept in all
 }
@@ -326,6 +434,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
 template <int D>
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictLaunch p) {
   __shared__ int sE[2][4];
+  __shared__ unsigned sHole[4];                     // the page's rows that are filled
   const int tid = threadIdx.x, j = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
   const int lg = p.c.page_log2, page = 1 << lg, pages = (p.budget + page - 1) >> lg;
   const int64_t slot = (int64_t)n * p.c.H_kv + h;
@@ -338,17 +447,43 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictLaunch p) {
   if (total <= 0) return;
   const int a = first[j], b = j + 1 < pages ? first[j + 1] : total;
   if (a >= b) return;
+  constexpr int kPer = D / 16;                      // 16-byte pieces of a row
+  constexpr int kRows = 256 / kPer;                 // rows that the threads take at a time
   const int64_t to = page_of(p.c, n, j << lg) * (int64_t)p.c.H_kv + h;   // (the first launch checked the pages)
   const int* holes = p.holes + slot * p.budget;
   const int* movers = p.movers + slot * p.budget;
   const f32x2* scales = reinterpret_cast<const f32x2*>(p.scales) + slot * p.budget;
+  const int c = tid % kPer;
+  // This thread's piece of moved row m: all of a row's loads at once.
+  struct Piece {
+    uint4 k, v;
+    int64_t from, dst;
+    f32x2 s;
+  };
+  const int64_t row0 = to << lg;
+  auto get = [&](int m) __attribute__((always_inline)) {
+    Piece x;
+    const int src = movers[m];
+    x.s = scales[m];
+    x.dst = row0 + (holes[m] & (page - 1));
+    x.from = page_rows(p.c, src >> lg, h) + (src & (page - 1));
+    x.k = *(reinterpret_cast<const uint4*>(p.c.k + x.from * D) + c);
+    x.v = *(reinterpret_cast<const uint4*>(p.c.v + x.from * D) + c);
+    return x;
+  };
+  Piece x;
+  if (a + tid / kPer < b) x = get(a + tid / kPer);  // in flight while the scales are compared
   // the page's new scales
   const int ko = exp_of(p.c.k_scale[to]), vo = exp_of(p.c.v_scale[to]);
   int ke = ko, ve = vo;
+  if (tid < 4) sHole[tid] = 0;
+  __syncthreads();
   for (int i = a + tid; i < b; i += 256) {
     const f32x2 s = scales[i];
     ke = max(ke, exp_of(s.x));
     ve = max(ve, exp_of(s.y));
+    const int r = holes[i] & (page - 1);
+    atomicOr(&sHole[r >> 5], 1u << (r & 31));
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
@@ -366,48 +501,31 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictLaunch p) {
     p.c.k_scale[to] = exp2_int(ke);
     p.c.v_scale[to] = exp2_int(ve);
   }
-  const int64_t row0 = to << lg;
-  const int alive = min(page, p.budget - (j << lg));   // rows of the page before budget
-  constexpr int kPer = D / 16;                      // 16-byte pieces of a row
-  if (ke > ko || ve > vo) {
+  auto rescale = [](uint4 w, float f) __attribute__((always_inline)) {
+    return make_uint4(f8x4_rescale(w.x, f), f8x4_rescale(w.y, f), f8x4_rescale(w.z, f), f8x4_rescale(w.w, f));
+  };
+  if (ke > ko || ve > vo) {                         // round the rows that stay to the new scales
+    const int alive = min(page, p.budget - (j << lg));   // rows of the page before budget
     const float ks = ldexpf(1.0f, ko - ke), vs = ldexpf(1.0f, vo - ve);
-    for (int i = tid; i < alive * kPer; i += 256) {
-      if (ke > ko) {
-        uint4* at = reinterpret_cast<uint4*>(p.c.k + row0 * D) + i;
-        const uint4 w = *at;
-        *at = make_uint4(f8x4_rescale(w.x, ks), f8x4_rescale(w.y, ks), f8x4_rescale(w.z, ks), f8x4_rescale(w.w, ks));
-      }
-      if (ve > vo) {
-        uint4* at = reinterpret_cast<uint4*>(p.c.v + row0 * D) + i;
-        const uint4 w = *at;
-        *at = make_uint4(f8x4_rescale(w.x, vs), f8x4_rescale(w.y, vs), f8x4_rescale(w.z, vs), f8x4_rescale(w.w, vs));
-      }
+    for (int r = tid / kPer; r < alive; r += kRows) {
+      if (sHole[r >> 5] >> (r & 31) & 1) continue;
+      uint4* kp = reinterpret_cast<uint4*>(p.c.k + (row0 + r) * D) + c;
+      uint4* vp = reinterpret_cast<uint4*>(p.c.v + (row0 + r) * D) + c;
+      if (ke > ko) *kp = rescale(*kp, ks);
+      if (ve > vo) *vp = rescale(*vp, vs);
     }
-    __syncthreads();                                // the holes' old codes are written before the rows that fill them
   }
-  for (int i = tid; i < (b - a) * kPer; i += 256) {
-    const int m = a + i / kPer, c = i % kPer;
-    const int src = movers[m];
-    const int64_t from = page_rows(p.c, page_of(p.c, n, src), h) + (src & (page - 1));
-    const int64_t dst = row0 + (holes[m] & (page - 1));
-    const f32x2 s = scales[m];
-    uint4 k = *(reinterpret_cast<const uint4*>(p.c.k + from * D) + c);
-    uint4 v = *(reinterpret_cast<const uint4*>(p.c.v + from * D) + c);
-    const int dk = exp_of(s.x) - ke, dv = exp_of(s.y) - ve;   // <= 0
-    if (dk) {
-      const float f = ldexpf(1.0f, dk);
-      k = make_uint4(f8x4_rescale(k.x, f), f8x4_rescale(k.y, f), f8x4_rescale(k.z, f), f8x4_rescale(k.w, f));
-    }
-    if (dv) {
-      const float f = ldexpf(1.0f, dv);
-      v = make_uint4(f8x4_rescale(v.x, f), f8x4_rescale(v.y, f), f8x4_rescale(v.z, f), f8x4_rescale(v.w, f));
-    }
-    *(reinterpret_cast<uint4*>(p.c.k + dst * D) + c) = k;
-    *(reinterpret_cast<uint4*>(p.c.v + dst * D) + c) = v;
+  for (int m = a + tid / kPer; m < b; m += kRows) {
+    const int dk = exp_of(x.s.x) - ke, dv = exp_of(x.s.y) - ve;   // <= 0
+    if (dk) x.k = rescale(x.k, ldexpf(1.0f, dk));
+    if (dv) x.v = rescale(x.v, ldexpf(1.0f, dv));
+    *(reinterpret_cast<uint4*>(p.c.k + x.dst * D) + c) = x.k;
+    *(reinterpret_cast<uint4*>(p.c.v + x.dst * D) + c) = x.v;
     if (c == 0) {
-      p.c.pos[dst] = p.c.pos[from];
-      p.c.weight[dst] = p.c.weight[from];
+      p.c.pos[x.dst] = p.c.pos[x.from];
+      p.c.weight[x.dst] = p.c.weight[x.from];
     }
+    if (m + kRows < b) x = get(m + kRows);
   }
 }
 
@@ -415,6 +533,16 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictLaunch p) {
 
 hipError_t launch_kv_store(const StoreLaunch& p, hipStream_t stream) {
   const int64_t slots = p.cu ? (p.T >> p.c.page_log2) + 2 * (int64_t)p.N : p.N;
+  if (p.T <= kFewTokens * (int64_t)p.N) {
+    const int64_t items = slots * p.c.H_kv * 2;
+    const dim3 grid((unsigned)((items + kStoreThreads / kWave - 1) / (kStoreThreads / kWave)));
+    switch (p.c.d) {
+      case 64: kv_store_few_kernel<64><<<grid, kStoreThreads, 0, stream>>>(p, items); break;
+      case 128: kv_store_few_kernel<128><<<grid, kStoreThreads, 0, stream>>>(p, items); break;
+      default: kv_store_few_kernel<256><<<grid, kStoreThreads, 0, stream>>>(p, items); break;
+    }
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)slots, (unsigned)p.c.H_kv, 2);
   switch (p.c.d) {
     case 64: return store_by_page<64>(p, grid, stream);
@@ -424,7 +552,12 @@ hipError_t launch_kv_store(const StoreLaunch& p, hipStream_t stream) {
 }
 
 hipError_t launch_kv_evict(const EvictLaunch& p, hipStream_t stream) {
-  evict_select_kernel<<<dim3((unsigned)p.c.H_kv, (unsigned)p.N), kSelThreads, 0, stream>>>(p);
+  const dim3 heads((unsigned)p.c.H_kv, (unsigned)p.N);
+  const int64_t rows = (int64_t)p.c.table_width << p.c.page_log2;   // the longest sequence
+  if (rows <= 4 * kSelThreads) evict_select_kernel<1><<<heads, kSelThreads, 0, stream>>>(p);
+  else if (rows <= 8 * kSelThreads) evict_select_kernel<2><<<heads, kSelThreads, 0, stream>>>(p);
+  else if (rows <= 16 * kSelThreads) evict_select_kernel<4><<<heads, kSelThreads, 0, stream>>>(p);
+  else evict_select_kernel<0><<<heads, kSelThreads, 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const unsigned pages = (unsigned)(((int64_t)p.budget + (1 << p.c.page_log2) - 1) >> p.c.page_log2);
