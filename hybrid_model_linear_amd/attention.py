@@ -22,6 +22,8 @@ from ._lib import GDN_BF16
 
 _PAGES = (16, 32, 64, 128)
 _NO_CACHE = _lib.KVCacheArgs()
+_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
 
 
 # ------------------------------------------------------------------ helpers
@@ -43,21 +45,23 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _vec(t, name: str, n: int, dtype=torch.int32):
+def _vec(t, name: str, n: int, dtype=_I32):
     """Address of a contiguous vector of n elements, None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _heads(t, name: str, n: int, heads: int, d: int) -> int:
     """Token stride of a bf16 [n, heads, d] view whose heads are contiguous."""
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _BF16:
         raise ValueError(f"{name} must be bf16, got {t.dtype}")
     if t.shape != (n, heads, d):
         raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return heads * d
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name} must have contiguous heads (strides {st})")
@@ -66,27 +70,36 @@ def _heads(t, name: str, n: int, heads: int, d: int) -> int:
 
 def _table(t, n: int) -> tuple[int, int]:
     """(row stride, width) of a block table."""
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be int32 [{n}, width] with unit column stride, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-    w = t.shape[1]
-    return (t.stride(0) if n > 1 else w), w
+    if t.dtype is _I32 and t.dim() == 2:
+        rows, w = t.shape
+        if rows == n:
+            if t.is_contiguous():
+                return w, w
+            if w == 1 or t.stride(1) == 1:
+                return (t.stride(0) if n > 1 else w), w
+    raise ValueError(f"block_table must be int32 [{n}, width] with unit column stride, got "
+                     f"{t.dtype} {tuple(t.shape)} / {t.stride()}")
+
+
+def _like(q):
+    """A contiguous output of q's shape and type."""
+    return torch.empty_like(q) if q.is_contiguous() else torch.empty_like(q, memory_format=torch.contiguous_format)
 
 
 def _run(name: str, fn, args, i: int) -> None:
     """The call on device i's current stream."""
-    if torch.cuda.current_device() == i:
-        st = fn(ct.byref(args), torch._C._cuda_getCurrentRawStream(i))
+    if _current_device() == i:
+        st = fn(ct.byref(args), _raw_stream(i))
     else:
         with torch.cuda.device(i):
-            st = fn(ct.byref(args), torch._C._cuda_getCurrentRawStream(i))
+            st = fn(ct.byref(args), _raw_stream(i))
     if st:
         _lib.check(name, st)
 
 
 def _need(name: str, fn, args, i: int) -> int:
     """A workspace query on device i."""
-    if torch.cuda.current_device() == i:
+    if _current_device() == i:
         need = fn(ct.byref(args))
     else:
         with torch.cuda.device(i):
@@ -102,8 +115,8 @@ def _attach(name: str, fn, args, i: int, workspace):
         need = _need(name, fn, args, i)
         if need == 0:
             return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", i))
-    elif workspace.dtype is not torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
+        workspace = torch.empty(need, dtype=_U8, device=torch.device("cuda", i))
+    elif workspace.dtype is not _U8 or workspace.dim() != 1 or not workspace.is_contiguous() \
             or workspace.get_device() != i:
         raise ValueError("workspace must be a contiguous uint8 vector on the call's device")
     args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
@@ -121,15 +134,15 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale, pos=None, weight=None):
         shape = k.shape
-        if len(shape) != 4 or k.dtype is not torch.float8_e4m3fn or not k.is_contiguous():
+        if len(shape) != 4 or k.dtype is not _F8 or not k.is_contiguous():
             raise ValueError("cache.k must be contiguous float8_e4m3fn [num_pages, H_kv, page, d]")
         pages, H_kv, page, d = shape
-        if v.shape != shape or v.dtype is not torch.float8_e4m3fn or not v.is_contiguous():
+        if v.shape != shape or v.dtype is not _F8 or not v.is_contiguous():
             raise ValueError("cache.v must be like cache.k")
         for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t.dtype is not torch.float32 or t.shape != (pages, H_kv) or not t.is_contiguous():
+            if t.dtype is not _F32 or t.shape != (pages, H_kv) or not t.is_contiguous():
                 raise ValueError(f"cache.{nm} must be contiguous fp32 [{pages}, {H_kv}]")
-        for t, nm, dt in ((pos, "pos", torch.int32), (weight, "weight", torch.float32)):
+        for t, nm, dt in ((pos, "pos", _I32), (weight, "weight", _F32)):
             if t is not None and (t.dtype is not dt or t.shape != (pages, H_kv, page) or not t.is_contiguous()):
                 raise ValueError(f"cache.{nm} must be contiguous {dt} [{pages}, {H_kv}, {page}]")
         self._device = _place(k, v, k_scale, v_scale, pos, weight)
@@ -209,13 +222,13 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
         ca, ts, tw = _NO_CACHE, 0, 0
         i = _place(q, k, v, cu_seqlens, slopes, doc, visible, start, out)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _like(q)
     args = _lib.AttnExtendArgs(
         ca, GDN_BF16, GDN_BF16, N, H, H_kv, d, T, q.data_ptr(), _heads(q, "q", T, H, d), k.data_ptr(),
         _heads(k, "k", T, H_kv, d), v.data_ptr(), _heads(v, "v", T, H_kv, d), out.data_ptr(),
         _heads(out, "out", T, H, d), _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(cache_len, "cache_len", N),
         _vec(start, "start", N), _at(block_table), ts, tw, 1 if causal else 0, _vec(visible, "visible", N),
-        _vec(doc, "doc", T), _vec(slopes, "slopes", H, torch.float32), window, d ** -0.5 if scale is None else scale,
+        _vec(doc, "doc", T), _vec(slopes, "slopes", H, _F32), window, d ** -0.5 if scale is None else scale,
         softcap)
     _run("gdn_attn_extend", lib.gdn_attn_extend, args, i)
     return out
@@ -234,7 +247,7 @@ def _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, 
     o, os = (256, H * d) if out is None else (out.data_ptr(), _heads(out, "out", N, H, d))
     return _lib.AttnDecodeArgs(
         ca, GDN_BF16, GDN_BF16, N, H, q.data_ptr(), _heads(q, "q", N, H, d), o, os, _vec(kv_len, "kv_len", N),
-        _vec(q_pos, "q_pos", N), block_table.data_ptr(), ts, tw, max_kvlen, _vec(slopes, "slopes", H, torch.float32),
+        _vec(q_pos, "q_pos", N), block_table.data_ptr(), ts, tw, max_kvlen, _vec(slopes, "slopes", H, _F32),
         window, d ** -0.5 if scale is None else scale, softcap, 1 if accumulate else 0, None, 0), i
 
 
@@ -250,7 +263,7 @@ def attn_decode(q, cache: KVCache, block_table, kv_len, *, scale=None, softcap: 
     tensor of attn_decode_workspace_size bytes (else one is allocated)."""
     lib = _lib.load()
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _like(q)
     args, i = _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate,
                            max_kvlen, out)
     ws = _attach("gdn_attn_decode", lib.gdn_attn_decode_workspace_size, args, i, workspace)

@@ -131,13 +131,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
   const int h = b % p.c.H_kv;
   int n = b / p.c.H_kv;
   if (p.ranked) n = nth_longest(p.kv_len, p.N, n, lane);
-  int qpos;
-  const DecRange rg = dec_range(p, n, qpos);
-  if (p.kv_len[n] < 0) return;                  // a padding row
-  // this split's tiles of kR rows
-  const int c0 = rg.t0 + split * rg.per;
-  const int tb = c0 * (kChunk / kR), te = min((int)min((int64_t)c0 + rg.per, (int64_t)rg.t1) * (kChunk / kR), (rg.hi + kR - 1) / kR);
-  if (tb >= te && split > 0) return;            // (the join counts the splits that hold chunks)
   const int hq = h * G + gt * 16 + j16;         // this lane's query head
   const bool live = gt * 16 + j16 < G;
   const int lg = p.c.page_log2, pmask = (1 << lg) - 1;
@@ -159,11 +152,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
 #pragma unroll
   for (int t = 0; t < kT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // The page of the rows kG g .. of tile t, clamped into the sequence so that every address is
-  // a held row's (-1: out of range).
-  auto page_at = [&](int t, int g) __attribute__((always_inline)) {
-    return page_of(p.c, n, min(t * kR + kG * g, rg.hi - 1));
-  };
+  // The page of the rows kG g .. of tile t (-1: out of range, or past the table).
+  auto page_at = [&](int t, int g) __attribute__((always_inline)) { return page_of(p.c, n, t * kR + kG * g); };
   u32x4 kc[kTS][kP];
   vword vc[kG];
   int kid = -1, vid = -1;                       // pages of this lane's K rows and V rows: the next tile's to load
@@ -200,14 +190,25 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
     vid = page_at(t, g16);
   };
 
-  int t = tb + wave;
-  if (t < te) {
+  auto start = [&](int t) __attribute__((always_inline)) {
     ids(t);
     load_k(t);
     load_v(t, vid);
     cur = vid;
     ids(t + kDecWaves);
-  }
+  };
+  // Where the first tile does not depend on the length, its loads do not wait for it.
+  const bool early = p.splits == 1 && !(p.window > 0 && !p.c.pos);
+  if (early) start(wave);
+  int qpos;
+  const DecRange rg = dec_range(p, n, qpos);
+  if (p.kv_len[n] < 0) return;                  // a padding row
+  // this split's tiles of kR rows
+  const int c0 = rg.t0 + split * rg.per;
+  const int tb = c0 * (kChunk / kR), te = min((int)min((int64_t)c0 + rg.per, (int64_t)rg.t1) * (kChunk / kR), (rg.hi + kR - 1) / kR);
+  if (tb >= te && split > 0) return;            // (the join counts the splits that hold chunks)
+  int t = tb + wave;
+  if (!early && t < te) start(t);
 #pragma unroll 1
   for (; t < te; t += kDecWaves) {
     const bool bad = cur < 0;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
     if (partial) {
 #pragma unroll
       for (int i = 0; i < kG; ++i) hidden |= (bad || r0 + i < rg.lo || r0 + i >= rg.hi ? 1u : 0u) << i;
+      if (r0 >= rg.hi) vs = 1.f;                // (a page behind the last row may hold any scale)
     }
     if (by_pos) {
 #pragma unroll
@@ -432,6 +434,18 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDeco
   if (first >= rg.hi || used == 0) return;
   const int r = (int)first + 4 * tid;
   f32x4 w{0.f, 0.f, 0.f, 0.f};
+  // the row's weights and its first heads' scores, in flight while the statistics are joined
+  constexpr int kPre = 4;
+  const int id = r < rg.hi ? page_of(p.c, n, r) : -1;
+  float* const at = p.c.weight + page_rows(p.c, max(id, 0), h) + (r & ((1 << p.c.page_log2) - 1));
+  const float* const sc = p.scores + ((int64_t)n * p.H + h * G) * p.score_cap + r;
+  f32x4 old{0.f, 0.f, 0.f, 0.f}, pre[kPre];
+  if (id >= 0) {
+    old = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll
+    for (int g = 0; g < kPre; ++g)
+      if (g < G) pre[g] = *reinterpret_cast<const f32x4*>(sc + g * p.score_cap);
+  }
   for (int g0 = 0; g0 < G; g0 += 64) {
     const int gn = min(64, G - g0);
     __syncthreads();
@@ -459,22 +473,25 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDeco
       }
     }
     __syncthreads();
-    if (r < rg.hi) {
-#pragma unroll 4
-      for (int g = 0; g < gn; ++g) {
-        const f32x4 s = *reinterpret_cast<const f32x4*>(p.scores + ((int64_t)n * p.H + h * G + g0 + g) * p.score_cap + r);
+    auto add = [&](const f32x4& s, int g) __attribute__((always_inline)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(s[e] - sM[g]) * sInv[g];
+      for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(s[e] - sM[g]) * sInv[g];
+    };
+    if (id >= 0) {
+      int g = 0;
+      if (g0 == 0) {
+#pragma unroll
+        for (; g < kPre; ++g)
+          if (g < gn) add(pre[g], g);
       }
+#pragma unroll 4
+      for (; g < gn; ++g) add(*reinterpret_cast<const f32x4*>(sc + (g0 + g) * p.score_cap), g);
     }
   }
-  if (r >= rg.hi) return;
-  const int id = page_of(p.c, n, r);
   if (id < 0) return;
-  float* at = p.c.weight + page_rows(p.c, id, h) + (r & ((1 << p.c.page_log2) - 1));
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (r + e >= rg.lo && r + e < rg.hi) at[e] += w[e];
+    if (r + e >= rg.lo && r + e < rg.hi) at[e] = old[e] + w[e];
 }
 
 template <int D>

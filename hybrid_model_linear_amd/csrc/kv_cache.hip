@@ -201,8 +201,6 @@ hipError_t store_by_page(const StoreLaunch& p, dim3 grid, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ evict
-constexpr int kSelThreads = 1024;
-constexpr int kSelWaves = kSelThreads / kWave;
 constexpr int kBins = 2048;
 constexpr int kCopies = 4;
 
@@ -223,12 +221,35 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
   return v;
 }
 
-// KG: groups of four rows that a thread holds in registers (the whole sequence: 4096 KG
-// rows); 0: any length, rows are read again for every pass.
-template <int KG>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLaunch p) {
+// Exclusive sums over a workgroup of W waves of up to three counts per thread, and their
+// totals; buf: [3][W].  Two barriers.
+template <int W, int K>
+__device__ __forceinline__ void group_scan(int (&v)[K], int (&total)[K], int (*buf)[W]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int inc[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    inc[k] = wave_scan(v[k]);
+    if (lane == 63) buf[k][wave] = inc[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int s = wave_scan(lane < W ? buf[k][lane] : 0);       // every wave scans the waves' sums
+    total[k] = __builtin_amdgcn_readlane(s, W - 1);
+    const int before = __shfl(s, wave, kWave) - buf[k][wave];
+    v[k] = before + inc[k] - v[k];
+  }
+  __syncthreads();
+}
+
+// A workgroup of T threads.  KG: groups of four rows that a thread holds in registers (the
+// whole sequence: 4 T KG rows); 0: any length, rows are read again for every pass.
+template <int T, int KG>
+__global__ void __launch_bounds__(T) evict_select_kernel(const EvictLaunch p) {
+  constexpr int kSelThreads = T, kSelWaves = T / kWave;
   __shared__ int sHist[kCopies][kBins];
-  __shared__ int sWave[3][kSelWaves];
+  __shared__ int sWave[2][kSelWaves];
   __shared__ int sPick[2];
   const int tid = threadIdx.x, wave = tid >> 6, h = blockIdx.x, n = blockIdx.y;
   const int lg = p.c.page_log2;
@@ -327,26 +348,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
         }
     }
     __syncthreads();
-    // suffix sums: thread t owns bins 2047 - 2 t and 2046 - 2 t, so a prefix scan over the
-    // threads counts from the largest key down
-    const int b1 = kBins - 1 - 2 * tid;
-    int c1 = 0, c0 = 0;
+    // suffix sums: thread t owns the bins from kBins - 1 - kOwn t down, so a prefix scan over
+    // the threads counts from the largest key down
+    constexpr int kOwn = kBins / T;
+    const int b1 = kBins - 1 - kOwn * tid;
+    int c[kOwn], sum[1] = {0}, all[1];
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      c1 += sHist[i][b1];
-      c0 += sHist[i][b1 - 1];
+    for (int b = 0; b < kOwn; ++b) {
+      c[b] = 0;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) c[b] += sHist[i][b1 - b];
+      sum[0] += c[b];
     }
-    const int inc = wave_scan(c1 + c0);
-    if ((tid & 63) == 63) sWave[0][wave] = inc;
-    __syncthreads();
-    int before = inc - c1 - c0;
-    for (int i = 0; i < wave; ++i) before += sWave[0][i];
-    if (before < want && want <= before + c1) {
-      sPick[0] = b1;
-      sPick[1] = want - before;
-    } else if (before + c1 < want && want <= before + c1 + c0) {
-      sPick[0] = b1 - 1;
-      sPick[1] = want - before - c1;
+    group_scan<kSelWaves, 1>(sum, all, sWave);
+    int before = sum[0];
+#pragma unroll
+    for (int b = 0; b < kOwn; ++b) {
+      if (before < want && want <= before + c[b]) {
+        sPick[0] = b1 - b;
+        sPick[1] = want - before;
+      }
+      before += c[b];
     }
     __syncthreads();
     found |= (unsigned)sPick[0] << shift;
@@ -364,14 +386,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
     int eq = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) eq += r0 + e < len && k[e] == found;
-    const int eqi = wave_scan(eq);
-    if ((tid & 63) == 63) sWave[0][wave] = eqi;
-    __syncthreads();
-    int rank = equal0 + eqi - eq;
-    for (int i = 0; i < kSelWaves; ++i) {
-      if (i < wave) rank += sWave[0][i];
-      equal0 += sWave[0][i];
-    }
+    int rk[1] = {eq}, eqs[1];
+    group_scan<kSelWaves, 1>(rk, eqs, sWave);
+    int rank = equal0 + rk[0];
+    equal0 += eqs[0];
     bool hole[4], mover[4];
     int nh = 0, nm = 0;
 #pragma unroll
@@ -385,21 +403,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
       nh += hole[e];
       nm += mover[e];
     }
-    const int hi = wave_scan(nh), mi = wave_scan(nm);
-    if ((tid & 63) == 63) {
-      sWave[1][wave] = hi;
-      sWave[2][wave] = mi;
-    }
-    __syncthreads();
-    int hb = hole0 + hi - nh, mb = mover0 + mi - nm;
-    for (int i = 0; i < kSelWaves; ++i) {
-      if (i < wave) {
-        hb += sWave[1][i];
-        mb += sWave[2][i];
-      }
-      hole0 += sWave[1][i];
-      mover0 += sWave[2][i];
-    }
+    int at2[2] = {nh, nm}, sums[2];
+    group_scan<kSelWaves, 2>(at2, sums, sWave);
+    int hb = hole0 + at2[0], mb = mover0 + at2[1];
+    hole0 += sums[0];
+    mover0 += sums[1];
     if (r0 < p.budget && (r0 & ((1 << lg) - 1)) == 0) first[r0 >> lg] = hb;
     f32x2 sc{0.f, 0.f};
     if (nm) {
@@ -414,7 +422,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictLa
         scales[mb++] = sc;
       }
     }
-    __syncthreads();                                // sWave is written again by the next rows
   };
   if constexpr (KG > 0) {
 #pragma unroll
@@ -554,10 +561,12 @@ hipError_t launch_kv_store(const StoreLaunch& p, hipStream_t stream) {
 hipError_t launch_kv_evict(const EvictLaunch& p, hipStream_t stream) {
   const dim3 heads((unsigned)p.c.H_kv, (unsigned)p.N);
   const int64_t rows = (int64_t)p.c.table_width << p.c.page_log2;   // the longest sequence
-  if (rows <= 4 * kSelThreads) evict_select_kernel<1><<<heads, kSelThreads, 0, stream>>>(p);
-  else if (rows <= 8 * kSelThreads) evict_select_kernel<2><<<heads, kSelThreads, 0, stream>>>(p);
-  else if (rows <= 16 * kSelThreads) evict_select_kernel<4><<<heads, kSelThreads, 0, stream>>>(p);
-  else evict_select_kernel<0><<<heads, kSelThreads, 0, stream>>>(p);
+  // (a small workgroup for few rows: its barriers cost less)
+  if (rows <= 1024) evict_select_kernel<256, 1><<<heads, 256, 0, stream>>>(p);
+  else if (rows <= 2048) evict_select_kernel<256, 2><<<heads, 256, 0, stream>>>(p);
+  else if (rows <= 8192) evict_select_kernel<1024, 2><<<heads, 1024, 0, stream>>>(p);
+  else if (rows <= 16384) evict_select_kernel<1024, 4><<<heads, 1024, 0, stream>>>(p);
+  else evict_select_kernel<1024, 0><<<heads, 1024, 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const unsigned pages = (unsigned)(((int64_t)p.budget + (1 << p.c.page_log2) - 1) >> p.c.page_log2);
