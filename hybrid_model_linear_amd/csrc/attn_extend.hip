@@ -191,17 +191,23 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Score i of this lane -> weight, its part of the sum, and every eighth an operand.
+  // Scores [a, b) of this lane -> weights; then (a step later, since an exponential's result
+  // takes a few cycles) their part of the sum, and every eighth an operand.
   float ls[2];
-  auto weight = [&](int i, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
-    const float x = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -base));
-    s[i >> 4][i & 15] = x;
-    ls[i & 1] = i < 2 ? x : ls[i & 1] + x;
-    if ((i & 7) == 7) pb[i >> 3] = acc_to_op(s[i >> 4], i >> 3 & 1);
+  auto weigh = [&](int a, int b, f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = a; i < b; ++i) s[i >> 4][i & 15] = __builtin_amdgcn_exp2f(fmaf(s[i >> 4][i & 15], cs, -base));
+  };
+  auto gather = [&](int a, int b, const f32x16 (&s)[kN2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = a; i < b; ++i) {
+      ls[i & 1] = i < 2 ? s[0][i] : ls[i & 1] + s[i >> 4][i & 15];
+      if ((i & 7) == 7) pb[i >> 3] = acc_to_op(s[i >> 4], i >> 3 & 1);
+    }
   };
   auto weights = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kS; ++i) weight(i, s);
+    weigh(0, kS, s);
+    gather(0, kS, s);
     l += ls[0] + ls[1];
   };
   // O^T += V^T P^T with the V tile `voff` bytes behind the first.
@@ -242,11 +248,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
     }
   };
-  // One step: weights of the tile in s under the scores of the next (s2), then this tile's
-  // product under the next one's maximum.  load(0), load(1) start the loads of later tiles;
-  // finish(s2) brings the new scores to their final form (cap, bias, mask).  The order is fixed here, an MFMA and its share of vector work at a time
-  // with operands kRing MFMAs ahead: left alone, the compiler waits for each read before
-  // its MFMA and puts the vector work behind them all.
+  // One step: half of the weights of the tile in s under the scores of the next (s2), the
+  // other half under the first half of this tile's product, the next one's maximum under the
+  // second.  load(0), load(1) start the loads of later tiles; finish(s2) brings the new scores
+  // to their final form (cap, bias, mask).  The order is fixed here, an MFMA and its share of
+  // vector work at a time with operands kRing MFMAs ahead: left alone, the compiler waits
+  // for each read before its MFMA and puts the vector work behind them all.
   auto step = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t koff, uint32_t voff, auto load,
                   auto finish) __attribute__((always_inline)) {
     bf16x8 a[kRing];
@@ -256,30 +263,38 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 #pragma unroll
     for (int i = 0; i < kNS; ++i) {
       score(i, koff, s2, a);
-#pragma unroll
-      for (int e = i * kS / kNS; e < (i + 1) * kS / kNS; ++e) weight(e, s);
+      weigh(i * (kS / 2) / kNS, (i + 1) * (kS / 2) / kNS, s);
+      if (i > 0) gather((i - 1) * (kS / 2) / kNS, i * (kS / 2) / kNS, s);
       if (i < 2) load(i);
       __builtin_amdgcn_sched_barrier(0);
     }
-    l += ls[0] + ls[1];
+    gather((kNS - 1) * (kS / 2) / kNS, kS / 2, s);
     // (formed here: the compiler would sink them behind the branches of finish)
 #pragma unroll
-    for (int i = 0; i < 2 * kN2; ++i) asm volatile("" : "+v"(pb[i]));
-    asm volatile("" : "+v"(l));
+    for (int i = 0; i < kN2; ++i) asm volatile("" : "+v"(pb[i]));
+    asm volatile("" : "+v"(ls[0]), "+v"(ls[1]));
     finish(s2);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kRing; ++i) a[i] = v_op(i, voff);
     __builtin_amdgcn_sched_barrier(0);
     float mx = s2[0][0];
+    constexpr int kH = kNP / 2;
 #pragma unroll
     for (int i = 0; i < kNP; ++i) {
       o[i % kDT] = mfma32(a[i % kRing], pb[i / kDT], o[i % kDT]);
       if (i + kRing < kNP) a[i % kRing] = v_op(i + kRing, voff);
+      // (the second half's operands are whole a step before the products that take them)
+      constexpr int kQ = kH - 1;
+      if (i < kQ) weigh(kS / 2 + i * (kS / 2) / kQ, kS / 2 + (i + 1) * (kS / 2) / kQ, s);
+      if (i > 0 && i < kH) gather(kS / 2 + (i - 1) * (kS / 2) / kQ, kS / 2 + i * (kS / 2) / kQ, s);
+      if (i >= kH) {
 #pragma unroll
-      for (int e = i * kS / kNP; e < (i + 1) * kS / kNP; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
+        for (int e = (i - kH) * kS / kH; e < (i + 1 - kH) * kS / kH; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
+    l += ls[0] + ls[1];
     raise(mx);
   };
   auto to_log2 = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
