@@ -18,13 +18,13 @@ constexpr int64_t kMaxGrid = INT32_MAX;
 int page_log2(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
 
 // The cache and block table of a call; `track`: pos and weight are required.
-int check_cache(const gdn_kv_cache& c, const int32_t* table, int64_t table_stride, int32_t table_width, bool track,
-                gdn::CacheRef& r) {
+int check_cache(const gdn_kv_cache& c, int32_t N, const int32_t* table, int64_t table_stride, int32_t table_width,
+                bool track, gdn::CacheRef& r) {
   if (c.d != 64 && c.d != 128 && c.d != 256) return GDN_E_UNSUPPORTED;
   if (page_log2(c.page) < 0) return GDN_E_UNSUPPORTED;
   if (c.H_kv <= 0 || c.H_kv > 65535 || c.num_pages <= 0) return GDN_E_SHAPE;
   if (table_width <= 0 || table_stride < table_width || (int64_t)table_width * c.page > INT32_MAX - 4096) return GDN_E_SHAPE;
-  if (!c.k || !c.v || !c.k_scale || !c.v_scale || !table || (track && (!c.pos || !c.weight))) return GDN_E_NULL;
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale || (N > 0 && !table) || (track && (!c.pos || !c.weight))) return GDN_E_NULL;
   if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.pos, 16) || !aligned(c.weight, 16) || !aligned(c.k_scale, 4) ||
       !aligned(c.v_scale, 4) || !aligned(table, 4))
     return GDN_E_SHAPE;
@@ -66,7 +66,7 @@ int plan_decode(const gdn_attn_decode_args* a, gdn::AttnDecodeLaunch& p, int64_t
   if (!a) return GDN_E_NULL;
   if (a->in_dtype != GDN_BF16 || a->out_dtype != GDN_BF16) return GDN_E_DTYPE;
   if (a->N < 0 || a->N > 65535 || a->H <= 0 || a->max_kvlen < 0) return GDN_E_SHAPE;
-  int st = check_cache(a->cache, a->block_table, a->table_stride, a->table_width, false, p.c);
+  int st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, false, p.c);
   if (st != GDN_OK) return st;
   if (a->H % p.c.H_kv != 0) return GDN_E_SHAPE;
   st = check_scores(a->scale, a->softcap, a->window);
@@ -113,7 +113,7 @@ int plan_evict(const gdn_kv_evict_args* a, gdn::EvictLaunch& p, int64_t& need) {
   need = 0;
   if (!a) return GDN_E_NULL;
   if (a->N < 0 || a->N > 65535 || a->budget < 1 || a->recent < 0 || a->recent > a->budget) return GDN_E_SHAPE;
-  const int st = check_cache(a->cache, a->block_table, a->table_stride, a->table_width, true, p.c);
+  const int st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, true, p.c);
   if (st != GDN_OK) return st;
   if (a->N > 0 && (!a->kv_len || !a->new_len)) return GDN_E_NULL;
   if (a->cache.num_pages > INT32_MAX / a->cache.page) return GDN_E_UNSUPPORTED;   // rows of the cache: 32-bit in the kernel
@@ -154,7 +154,7 @@ int gdn_kv_store(const gdn_kv_store_args* a, void* stream) {
   if (a->in_dtype != GDN_BF16) return GDN_E_DTYPE;
   if (a->N < 0 || a->T < 0 || a->T > INT32_MAX) return GDN_E_SHAPE;
   gdn::StoreLaunch p{};
-  const int st = check_cache(a->cache, a->block_table, a->table_stride, a->table_width, false, p.c);
+  const int st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, false, p.c);
   if (st != GDN_OK) return st;
   if (!a->cu_seqlens && a->T != a->N) return GDN_E_SHAPE;
   if (a->T > 0 && (!a->k || !a->v)) return GDN_E_NULL;
@@ -183,7 +183,7 @@ int gdn_attn_extend(const gdn_attn_extend_args* a, void* stream) {
   if (st != GDN_OK) return st;
   gdn::AttnExtendLaunch p{};
   if (a->cache.k) {
-    st = check_cache(a->cache, a->block_table, a->table_stride, a->table_width, false, p.c);
+    st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, false, p.c);
     if (st != GDN_OK) return st;
     if (p.c.d != a->d || p.c.H_kv != a->H_kv) return GDN_E_SHAPE;
     if (a->doc) return GDN_E_UNSUPPORTED;

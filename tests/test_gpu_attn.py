@@ -289,3 +289,45 @@ def test_evict_leaves_a_sequence_with_a_bad_page(gdn_lib):
     g = upload_cache(gdn_lib, c)
     assert gdn_lib.kv_evict(g, i32(table), i32([100, 90]), 40, recent=4).tolist() == [100, 40]
     assert_same_cache(host_cache(g), ref, "evict")
+
+
+@pytest.mark.parametrize("pos", [False, True])
+def test_extend_over_cache_hidden_values_do_not_leak(gdn_lib, pos):
+    """NaN codes in cached rows that a window hides from some of the new tokens."""
+    print(f"[case] extend over cache, hidden NaN, pos={pos}", flush=True)
+    rng = np.random.default_rng(21)
+    lens, old, H, H_kv, d, page = [70, 33], [200, 131], 4, 2, 128, 32
+    c = make_cache(rng, 14, H_kv, page, d, track=pos)
+    table = make_table(rng, old, page, 14)
+    start = [x + 1 for x in spread_positions(rng, c, table, old)] if pos else None
+    c["v"][table[0, 4], 0, 7, 3], c["v"][table[0, 5], 1, 9], c["k"][table[0, 5], 0, 11, 0] = 0x7f, 0xff, 0x7f
+    c["v"][table[1, 3], :, 30, 100] = 0x7f
+    q, k, v = _qkv(rng, sum(lens), H, H_kv, d)
+    window = 110 if pos else 60
+    with np.errstate(invalid="ignore"):
+        ref, mag = oa.attn_extend(q, k, v, _cu(lens), 0.1, cache=c, table=table, cache_len=old, start=start, window=window)
+    got = gdn_lib.attn_extend(up(q, torch.bfloat16), up(k, torch.bfloat16), up(v, torch.bfloat16), i32(_cu(lens)), scale=0.1,
+                              cache=upload_cache(gdn_lib, c), block_table=i32(table), cache_len=i32(old), start=i32(start),
+                              window=window).float().cpu().numpy()
+    nan = np.isnan(ref)
+    assert nan.any() and not nan.all() and np.array_equal(np.isnan(got), nan)
+    tol = (BF * (np.abs(ref) + mag) + 1e-3 * mag) * 1.01
+    assert (np.abs(got[~nan] - ref[~nan]) <= tol[~nan]).all()
+
+
+@pytest.mark.parametrize("pos", [False, True])
+def test_decode_hidden_values_do_not_leak(gdn_lib, pos):
+    """NaN codes in rows outside of the window leave the output as it is."""
+    print(f"[case] decode, hidden NaN, pos={pos}", flush=True)
+    rng = np.random.default_rng(22)
+    c = make_cache(rng, 20, 2, 32, 64, track=pos)
+    table = make_table(rng, [300, 64], 32, 20)
+    q_pos = spread_positions(rng, c, table, [300, 64]) if pos else None
+    for a in ("k", "v"):
+        c[a][table[0, 0], :, 5], c[a][table[0, 6], 1, 0, 7] = 0x7f, 0xff
+    q = bf16(rng.normal(size=(2, 4, 64)))
+    ref, mag, _ = oa.attn_decode(q, c, table, [300, 64], 0.1, window=100, q_pos=q_pos)
+    got = gdn_lib.attn_decode(up(q, torch.bfloat16), upload_cache(gdn_lib, c), i32(table), i32([300, 64]), scale=0.1, window=100,
+                              q_pos=i32(q_pos)).float().cpu().numpy()
+    assert np.isfinite(ref).all()
+    assert_out(got, ref, mag, score_error(q, cache_norm(c), 0.1), "decode")
