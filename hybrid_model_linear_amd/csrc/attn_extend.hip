@@ -75,7 +75,16 @@ template <int D> __device__ __forceinline__ int row_swz(int r) {
   return D >= 128 ? ((r & 3) << 2 | (r >> 2 & 3)) : ((r >> 1 & 1) << 2 | (r >> 2 & 3));
 }
 
-template <int D, bool CACHED>
+// What happens to a score between the two products (a kernel per way: the vector work is laid
+// out by hand under the matrix instructions).
+enum Shape {
+  kRaw = 0,       // nothing but a positive scale, which is left to the exponent
+  kBias = 1,      // scale and distance bias (slopes may be null: a scale that is not positive)
+  kCap = 2,       // tanh cap
+  kCapBias = 3,
+};
+
+template <int D, bool CACHED, int SHAPE>
 __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(const AttnExtendLaunch p) {
   constexpr int kBN = 64;                  // keys of a tile
   constexpr int kN2 = kBN / 32;
@@ -129,13 +138,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     if (live) x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(t0 + ti) * p.q_stride + (int64_t)hq * D + 16 * u + 8 * hh);
     q[u] = as_bf16x8(x);
   }
-  // Scores stay raw (q.k) until the exponent where nothing but a positive scale applies;
-  // otherwise they are brought to units of log2 first.
-  const bool raw = p.softcap == 0.f && !p.slopes && p.scale > 0.f;
-  const float c1 = p.softcap > 0.f ? p.scale / p.softcap * 2.0f * kLog2e : p.scale * kLog2e;
+  // kRaw: scores stay q.k until the exponent; otherwise they are brought to units of log2 first.
+  constexpr bool kHasBias = SHAPE & kBias, kHasCap = SHAPE & kCap;
+  const float c1 = kHasCap ? p.scale / p.softcap * 2.0f * kLog2e : p.scale * kLog2e;
   const float c2 = p.softcap * kLog2e;
-  const float cs = raw ? c1 : 1.f;
-  const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
+  const float cs = SHAPE == kRaw ? c1 : 1.f;
+  const float slope = kHasBias && p.slopes ? p.slopes[hq] * kLog2e : 0.f;
   const float slack = 8.f / cs;            // the maximum in use may lag the true one by 2^8
 
   // operand addresses in the first K and V tile (kTile bytes each: K, V, K, V)
@@ -242,69 +250,79 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       for (int t = 0; t < kDT; ++t) o[t] *= fct;
     }
   };
-  auto hide = [&](f32x16 (&s)[kN2], unsigned hidden) __attribute__((always_inline)) {
+  auto hide = [&](f32x16 (&s)[kN2], unsigned hidden, float& mx) __attribute__((always_inline)) {
     if (__any(hidden != 0)) {
 #pragma unroll
       for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = hidden >> i & 1 ? -INFINITY : s[i >> 4][i & 15];
+      mx = tile_max(s);
     }
   };
-  // One step: half of the weights of the tile in s under the scores of the next (s2), the
-  // other half under the first half of this tile's product, the next one's maximum under the
-  // second.  load(0), load(1) start the loads of later tiles; finish(s2) brings the new scores
-  // to their final form (cap, bias, mask).  The order is fixed here, an MFMA and its share of
-  // vector work at a time with operands kRing MFMAs ahead: left alone, the compiler waits
-  // for each read before its MFMA and puts the vector work behind them all.
-  auto step = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t koff, uint32_t voff, auto load,
-                  auto finish) __attribute__((always_inline)) {
+  // Score i to its final form but for the mask; dq: this row's position minus that of the tile's
+  // first key of this lane, sl the slope.
+  auto shape = [&](int i, f32x16 (&s)[kN2], float dq, float sl) __attribute__((always_inline)) {
+    float x = s[i >> 4][i & 15];
+    if (kHasCap) x = capped(x, c1, c2); else if (kHasBias) x *= c1;
+    if (kHasBias) x -= sl * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
+    s[i >> 4][i & 15] = x;
+  };
+  // One step: weights of the tile in s under the scores of the next (s2), then this tile's
+  // product, under which the new scores are shaped and their maximum is found; kRaw leaves
+  // half of the weights to the first half of the product.  load(j) starts one of
+  // the loads of later tiles; mask(s2, mx) hides scores of a tile that is seen in part.  The order is fixed here, an MFMA and
+  // its share of vector work at a time with operands kRing MFMAs ahead: left alone, the
+  // compiler waits for each read before its MFMA and puts the vector work behind them all.
+  auto step = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t koff, uint32_t voff, float dq, float sl, auto loads,
+                  auto load, auto mask) __attribute__((always_inline)) {
+    constexpr int kW = SHAPE == kRaw && D < 256 ? kS / 2 : kS;   // weights formed under the scores
+    constexpr int kFirst = kW / 8;                      // of them, while the first operands are on their way
+    constexpr int kH = kNP / 2, kQ = kH - 1, kLoads = decltype(loads)::value;
+    auto part = [](int i, int n, int of, int from) { return from + i * of / n; };
     bf16x8 a[kRing];
 #pragma unroll
     for (int i = 0; i < kRing; ++i) a[i] = k_op(i, koff);
+    weigh(0, kFirst, s);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kNS; ++i) {
       score(i, koff, s2, a);
-      weigh(i * (kS / 2) / kNS, (i + 1) * (kS / 2) / kNS, s);
-      if (i > 0) gather((i - 1) * (kS / 2) / kNS, i * (kS / 2) / kNS, s);
-      if (i < 2) load(i);
+      if (i + kRing >= kNS) a[i % kRing] = v_op(i + kRing - kNS, voff);
+      weigh(part(i, kNS, kW - kFirst, kFirst), part(i + 1, kNS, kW - kFirst, kFirst), s);
+      gather(i ? part(i - 1, kNS, kW - kFirst, kFirst) : 0, part(i, kNS, kW - kFirst, kFirst), s);
+      if (i % (kNS / kLoads) == 0) load(i / (kNS / kLoads));
       __builtin_amdgcn_sched_barrier(0);
     }
-    gather((kNS - 1) * (kS / 2) / kNS, kS / 2, s);
-    // (formed here: the compiler would sink them behind the branches of finish)
-#pragma unroll
-    for (int i = 0; i < kN2; ++i) asm volatile("" : "+v"(pb[i]));
-    asm volatile("" : "+v"(ls[0]), "+v"(ls[1]));
-    finish(s2);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < kRing; ++i) a[i] = v_op(i, voff);
-    __builtin_amdgcn_sched_barrier(0);
-    float mx = s2[0][0];
-    constexpr int kH = kNP / 2;
+    gather(part(kNS - 1, kNS, kW - kFirst, kFirst), kW, s);
+    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kNP; ++i) {
       o[i % kDT] = mfma32(a[i % kRing], pb[i / kDT], o[i % kDT]);
       if (i + kRing < kNP) a[i % kRing] = v_op(i + kRing, voff);
-      // (the second half's operands are whole a step before the products that take them)
-      constexpr int kQ = kH - 1;
-      if (i < kQ) weigh(kS / 2 + i * (kS / 2) / kQ, kS / 2 + (i + 1) * (kS / 2) / kQ, s);
-      if (i > 0 && i < kH) gather(kS / 2 + (i - 1) * (kS / 2) / kQ, kS / 2 + i * (kS / 2) / kQ, s);
-      if (i >= kH) {
+      if (kW < kS) {                                    // (the second half's operands are whole a step before they are used)
+        if (i < kQ) weigh(part(i, kQ, kS - kW, kW), part(i + 1, kQ, kS - kW, kW), s);
+        if (i > 0 && i < kH) gather(part(i - 1, kQ, kS - kW, kW), part(i, kQ, kS - kW, kW), s);
+      }
+      const int n0 = kW < kS ? kH : 2, nn = kNP - n0;   // (the last scores are not there at once)
+      if (i >= n0) {
+        const int e0 = part(i - n0, nn, kS, 0), e1 = part(i + 1 - n0, nn, kS, 0);
 #pragma unroll
-        for (int e = (i - kH) * kS / kH; e < (i + 1 - kH) * kS / kH; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
+        for (int e = e0; e < e1; ++e) shape(e, s2, dq, sl);
+        const int m0 = SHAPE == kRaw ? e0 : i > n0 ? part(i - 1 - n0, nn, kS, 0) : 0, m1 = SHAPE == kRaw ? e1 : e0;
+#pragma unroll
+        for (int e = m0; e < m1; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    l += ls[0] + ls[1];
-    raise(mx);
-  };
-  auto to_log2 = [&](f32x16 (&s)[kN2]) __attribute__((always_inline)) {
-    if (p.softcap > 0.f) {
+    if (SHAPE != kRaw) {
 #pragma unroll
-      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] = capped(s[i >> 4][i & 15], c1, c2);
-    } else if (!raw) {
-#pragma unroll
-      for (int i = 0; i < kS; ++i) s[i >> 4][i & 15] *= c1;
+      for (int e = kS - (kS + kNP - 3) / (kNP - 2); e < kS; ++e) mx = fmaxf(mx, s2[e >> 4][e & 15]);
     }
+    l += ls[0] + ls[1];
+    // (formed here: the compiler would sink the vector work behind the branches of mask)
+#pragma unroll
+    for (int i = 0; i < kN2; ++i) asm volatile("" : "+v"(s2[i]));
+    asm volatile("" : "+v"(l), "+v"(mx));
+    mask(s2, mx);
+    raise(mx);
   };
   // A copy of v that the compiler cannot see through: what the paths below compute from it
   // is computed there, and not kept in registers over the whole loop.
@@ -327,11 +345,15 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     }
     return bits;
   };
-  auto bias = [&](f32x16 (&s)[kN2], int qrel) __attribute__((always_inline)) {   // qrel: query minus the tile's first key
-    const float dq = (float)(qrel - 4 * (opaque(lane) >> 5));
+  auto dist0 = [&](int qrel) __attribute__((always_inline)) {   // shape()'s dq; qrel: query minus the tile's first key
+    return kHasBias ? (float)(qrel - 4 * (opaque(lane) >> 5)) : 0.f;
+  };
+  // The scores of the first tile, whole.
+  auto first_scores = [&](f32x16 (&s)[kN2], float dq, float sl) __attribute__((always_inline)) {
+    scores(0, s);
 #pragma unroll
-    for (int i = 0; i < kS; ++i)
-      s[i >> 4][i & 15] -= slope * fabsf(dq - (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)));
+    for (int i = 0; i < kS; ++i) shape(i, s, dq, sl);
+    return tile_max(s);
   };
   typedef u16 u16x2 __attribute__((ext_vector_type(2)));
   // A masked weight is 0, and 0 times NaN or infinity would reach rows that do not see the
@@ -473,18 +495,17 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const uint32_t ldsw = uni(lds_at(sT) + wave * 1024);
   const int fr = wave * kRpi + lane / kPc;              // row of the wave's first load; the next ones 4 kRpi further
   const uint32_t fc = (uint32_t)((lane % kPc) ^ row_swz<D>(fr)) << 4;
-  auto fetch = [&](const char* src, uint32_t st, uint32_t row0, int t, uint32_t to) __attribute__((always_inline)) {
+  auto fetch = [&](const char* src, uint32_t st, uint32_t row0, int t, uint32_t to, int s) __attribute__((always_inline)) {
     const int left = t >= d0 ? min(kBN, L - t * kBN) : 0;   // (behind the last tile nothing: zeros)
     const u32x4 rs = buffer_of(src + (int64_t)(t * kBN) * st, left > 0 ? (left - 1) * st + 2 * D : 0);
-#pragma unroll
-    for (int s = 0; s < kLd; ++s)                       // (8 rows on, the swizzle's bit 1 flips)
-      to_lds(rs, row0 + s * (4 * kRpi * st) + (4 * kRpi * s & 8 ? fc ^ 32 : fc), ldsw + to + s * 4096);
+    // (8 rows on, the swizzle's bit 1 flips)
+    to_lds(rs, row0 + s * (4 * kRpi * st) + (4 * kRpi * s & 8 ? fc ^ 32 : fc), ldsw + to + s * 4096);
   };
   const uint32_t rowk = fr * kst, rowv = fr * vst;
   const char* const ksrc = (const char*)(p.k + (int64_t)t0 * p.k_stride + (int64_t)h * D);
   const char* const vsrc = (const char*)(p.v + (int64_t)t0 * p.v_stride + (int64_t)h * D);
-  auto fetch_k = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(ksrc, kst, rowk, t, to); };
-  auto fetch_v = [&](int t, uint32_t to) __attribute__((always_inline)) { fetch(vsrc, vst, rowv, t, to + kTile); };
+  auto fetch_k = [&](int t, uint32_t to, int s) __attribute__((always_inline)) { fetch(ksrc, kst, rowk, t, to, s); };
+  auto fetch_v = [&](int t, uint32_t to, int s) __attribute__((always_inline)) { fetch(vsrc, vst, rowv, t, to + kTile, s); };
   // Tiles [wf, wl) are seen whole by all rows of the wave, [gf, gl) by the workgroup's
   // (documents aside): seen keys are a range, below the row's own or the prefix, inside the
   // window.
@@ -500,10 +521,8 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   int wf, wl, gf, gl;
   whole(wa, wz, wf, wl);
   whole(ta, tz, gf, gl);
-  auto finish = [&](f32x16 (&s)[kN2], int t, bool all) __attribute__((always_inline)) -> unsigned {
+  auto mask = [&](f32x16 (&s)[kN2], int t, bool all, float& mx) __attribute__((always_inline)) -> unsigned {
     const int j0 = t * kBN;
-    to_log2(s);
-    if (p.slopes) bias(s, ti - j0);
     unsigned hidden = 0;
     if (t < wf || t >= wl || !all) {
       int lo = 0, hi = min(max(ti + 1, vis), L) - j0;
@@ -526,7 +545,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         }
         lds_order();
       }
-      hide(s, hidden);
+      hide(s, hidden, mx);
     }
     return hidden;
   };
@@ -534,15 +553,18 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   int t = next(d1 - 1, all_t);
   if (t >= d0) {
     int nx = next(t - 1, all_x), n2 = next(nx - 1, all_2);    // the tiles after t
-    fetch_k(t, 0);
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) fetch_k(t, 0, i);
     vm_wait();
     lds_sync();
-    fetch_v(t, 0);
-    fetch_k(nx, 2 * kTile);
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) fetch_v(t, 0, i);
+#pragma unroll
+    for (int i = 0; i < kLd; ++i) fetch_k(nx, 2 * kTile, i);
     f32x16 s0[kN2], s1[kN2];
-    scores(0, s0);
-    unsigned hidden = finish(s0, t, all_t);
-    raise(tile_max(s0));
+    float mx = first_scores(s0, dist0(ti - t * kBN), slope);
+    unsigned hidden = mask(s0, t, all_t, mx);
+    raise(mx);
     // Tile t (scores in s, V `kV` bytes behind the first), the next one's K in the other pair.
     auto top = [&](uint32_t kV) __attribute__((always_inline)) -> unsigned long long {
       vm_wait();                                        // this wave's share has landed
@@ -555,14 +577,15 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
       });
     };
-    auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], auto par) __attribute__((always_inline)) {
-      constexpr int kV = decltype(par)::value * 2 * kTile, kK = 2 * kTile - kV;
+    auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t kV) __attribute__((always_inline)) {
+      const uint32_t kK = 2 * kTile - kV;
       const unsigned long long bad = top(kV);
       unsigned hid2 = 0;
       const auto load = [&](int i) __attribute__((always_inline)) {
-        if (i == 0) fetch_k(n2, kV); else fetch_v(nx, kK);
+        if (i < kLd) fetch_k(n2, kV, i); else fetch_v(nx, kK, i - kLd);
       };
-      step(s, s2, kK, kV, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, nx, all_x); });
+      step(s, s2, kK, kV, dist0(ti - nx * kBN), slope, Par<2 * kLd>{}, load,
+           [&](f32x16 (&f)[kN2], float& mx) __attribute__((always_inline)) { hid2 = mask(f, nx, all_x, mx); });
       if (bad) dirty(bad);
       hidden = hid2;
       t = nx;
@@ -572,16 +595,28 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       n2 = next(n2 - 1, all_2);
     };
     uint32_t off = 0;
-#pragma unroll 1
-    while (nx >= d0) {
-      one(s0, s1, Par<0>{});
-      if (nx < d0) {
-        off = 2 * kTile;
+    auto turn = [&]() __attribute__((always_inline)) {
+      off ^= 2 * kTile;
 #pragma unroll
-        for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
-        break;
+      for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
+    };
+    if constexpr (CACHED) {
+      // (one copy of the step: with two, and the cached rows' loop behind them, registers spill)
+#pragma unroll 1
+      while (nx >= d0) {
+        one(s0, s1, off);
+        turn();
       }
-      one(s1, s0, Par<1>{});
+    } else {
+#pragma unroll 1
+      while (nx >= d0) {
+        one(s0, s1, 0);
+        if (nx < d0) {
+          turn();
+          break;
+        }
+        one(s1, s0, 2 * kTile);
+      }
     }
     const unsigned long long bad = top(off);
     weights(s0);
@@ -602,122 +637,104 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       x0 = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
     }
     // A load brings 4, 8 or 16 rows of one page, so page addresses and scales are the same in
-    // every lane of a wave.  Lane l holds those of page pb + l of the sequence (byte offset of
-    // the page's rows, -1: not there), 64 pages at a time; a tile's are read out of the lanes,
-    // once where a page holds whole tiles.
+    // every lane of a wave.  Lane l holds those of page pb + l of the sequence (its place in
+    // units of 16 rows, -1: not there), 64 pages at a time; a load's are read out of the lanes.
     const bool big = lg >= 6;
-    int pb = 0;
-    int64_t poff = -1;
+    int pb = 0, punit = -1;
     float pks = 0.f, pvs = 0.f;
     auto pages = [&](int first) __attribute__((always_inline)) {
       pb = first;
       const int j = first + lane, id = j < ((P + pmask) >> lg) ? page_of(p.c, n, j << lg) : -1;
       const int64_t at = (int64_t)max(id, 0) * p.H_kv + h;
-      poff = id < 0 ? -1 : (at << lg) * D;
+      punit = id < 0 ? -1 : (int)(at << (lg - 4));
       pks = p.c.k_scale[at];
       pvs = p.c.v_scale[at];
     };
     auto lane_of = [&](int row) __attribute__((always_inline)) { return (row >> lg) - pb; };
-    auto off_of = [&](int pl) __attribute__((always_inline)) -> int64_t {   // (-1: not there)
-      return (int64_t)((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(poff >> 32), pl & 63) << 32 |
-                       (unsigned)__builtin_amdgcn_readlane((int)poff, pl & 63));
-    };
+    auto unit_of = [&](int pl) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(punit, pl & 63); };   // (-1: not there)
     const uint32_t rlane = (uint32_t)(lane / kCp) * D + 16 * (lane % kCp);   // this lane's piece of a load
     const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K and V, kTile / 2 bytes each, behind the first tiles
-    auto fetch = [&](const uint8_t* src, uint32_t to, int x) __attribute__((always_inline)) {
-      if (big) {
-        const int64_t off = max(off_of(lane_of(x * kBN)), (int64_t)0);
-        const u32x4 rs = buffer_of(src + off + ((x * kBN) & pmask) * D, kBN * D);
+    auto fetch = [&](const uint8_t* src, uint32_t to, int x, int s) __attribute__((always_inline)) {
+      const int r = x * kBN + (wave + 4 * s) * kCr, unit = max(unit_of(lane_of(r)), 0) + ((r & pmask) >> 4);
+      to_lds(buffer_of(src + (int64_t)unit * (16 * D) + (r & 15) * D, kCr * D), rlane, to + s * 4096);
+    };
+    auto fetch_all = [&](const uint8_t* src, uint32_t to, int x) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < kCt; ++s) to_lds(rs, rlane + (wave + 4 * s) * (kCr * D), to + s * 4096);
-      } else {
-#pragma unroll
-        for (int s = 0; s < kCt; ++s) {
-          const int r = x * kBN + (wave + 4 * s) * kCr;
-          const int64_t off = max(off_of(lane_of(r)), (int64_t)0);
-          to_lds(buffer_of(src + off + (r & pmask) * D, kCr * D), rlane, to + s * 4096);
-        }
-      }
+      for (int s = 0; s < kCt; ++s) fetch(src, to, x, s);
     };
     auto lane_f = [&](float v, int pl) __attribute__((always_inline)) {
       return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), pl & 63));
     };
     // Codes of tile x -> bf16 (rows that are not held -> zeros).
-    auto put = [&](const u32x4& w, float sc, uint32_t to, int r, int c) __attribute__((always_inline)) {
+    auto put = [&](const u32x4& w, float sc, uint32_t at) __attribute__((always_inline)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint2 a = f8x4_to_bf16(w[2 * e], sc), b = f8x4_to_bf16(w[2 * e + 1], sc);
-        *(lds_u32x4w*)(uintptr_t)(lds_at(sT) + to + r * 2 * D + (((2 * c + e) ^ row_swz<D>(r)) << 4)) =
-            u32x4{a.x, a.y, b.x, b.y};
+        *(lds_u32x4w*)(uintptr_t)(at ^ 16 * e) = u32x4{a.x, a.y, b.x, b.y};
       }
     };
     auto convert = [&](uint32_t from, uint32_t to, float lane_scale, int x) __attribute__((always_inline)) {
-      const int c = lane % kCp, pl = lane_of(x * kBN);
+      // (the rows of a lane's loads lie a multiple of 16 apart: one swizzle)
+      const int ol = opaque(lane), pl = lane_of(x * kBN), r = wave * kCr + ol / kCp;
+      const uint32_t at = lds_at(sT) + to + r * 2 * D + ((2 * (ol % kCp) ^ row_swz<D>(r)) << 4);
       u32x4 w[kCt];
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) w[s] = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + lane * 16);
-      if (big && x * kBN + kBN <= P && off_of(pl) >= 0) {
+      for (int s = 0; s < kCt; ++s) w[s] = *(lds_u32x4*)(uintptr_t)(from + s * 4096 + ol * 16);
+      if (big && x * kBN + kBN <= P && unit_of(pl) >= 0) {
         const float sc = lane_f(lane_scale, pl);
 #pragma unroll
-        for (int s = 0; s < kCt; ++s) put(w[s], sc, to, (wave + 4 * s) * kCr + lane / kCp, c);
+        for (int s = 0; s < kCt; ++s) put(w[s], sc, at + s * (8 * kCr * D));
       } else {
 #pragma unroll
         for (int s = 0; s < kCt; ++s) {
-          const int r0 = (wave + 4 * s) * kCr, r = r0 + lane / kCp, l0 = lane_of(x * kBN + r0);
-          if (off_of(l0) < 0 || x * kBN + r >= P) w[s] = u32x4{0, 0, 0, 0};
-          put(w[s], lane_f(lane_scale, l0), to, r, c);
+          const int r0 = 4 * s * kCr, l0 = lane_of(x * kBN + wave * kCr + r0);
+          if (unit_of(l0) < 0 || x * kBN + r + r0 >= P) w[s] = u32x4{0, 0, 0, 0};
+          put(w[s], lane_f(lane_scale, l0), at + s * (8 * kCr * D));
         }
       }
     };
     // Bit r: row x kBN + r is held.
     auto held = [&](int x) __attribute__((always_inline)) -> unsigned long long {
-      if (big && x * kBN + kBN <= P && off_of(lane_of(x * kBN)) >= 0) return ~0ull;
+      if (big && x * kBN + kBN <= P && unit_of(lane_of(x * kBN)) >= 0) return ~0ull;
       unsigned long long bits = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {                     // 16 rows lie on one page
         const int left = P - x * kBN - 16 * i;
-        if (left > 0 && off_of(lane_of(x * kBN + 16 * i)) >= 0)
+        if (left > 0 && unit_of(lane_of(x * kBN + 16 * i)) >= 0)
           bits |= (left >= 16 ? 0xffffull : (1ull << left) - 1) << 16 * i;
       }
       return bits;
     };
-    // Cap, bias and mask of tile x's scores; returns the hidden keys.
-    auto finish = [&](f32x16 (&s)[kN2], int x, unsigned long long now) __attribute__((always_inline)) -> unsigned {
+    // Mask of tile x's scores (and the bias, where rows hold positions of their own); returns
+    // the hidden keys.
+    auto mask = [&](f32x16 (&s)[kN2], int x, unsigned long long now, float& mx) __attribute__((always_inline)) -> unsigned {
       unsigned hidden = 0;
       const int j0 = x * kBN, oh = opaque(lane) >> 5;
-      if (p.slopes && p.softcap == 0.f && !p.c.pos && start + ta >= j0 + kBN) {
-        // the tile lies before every row: one line, -slope (q - k)
-        const float b0 = -slope * (float)(start + ti - j0 - 4 * oh);
-#pragma unroll
-        for (int i = 0; i < kS; ++i)
-          s[i >> 4][i & 15] = fmaf(s[i >> 4][i & 15], c1, fmaf(slope, (float)(32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3)), b0));
-      } else {
-        to_log2(s);
-        if (p.slopes && !p.c.pos) bias(s, start + ti - j0);
-      }
       if (now != ~0ull) {
 #pragma unroll
         for (int i = 0; i < kS; i += 4) hidden |= ((unsigned)(~now >> key(i, oh)) & 15u) << i;
       }
-      if (p.c.pos && (p.slopes || p.window > 0)) {
+      if (p.c.pos && (kHasBias || p.window > 0)) {
         const int qpos = start + ti;
 #pragma unroll
         for (int i = 0; i < kS; i += 4) {
+          asm volatile("" ::: "memory");                // (one at a time: registers)
           const int r = j0 + key(i, oh), pg = r < P ? page_of(p.c, n, r) : -1;
           int4 kp = make_int4(qpos, qpos, qpos, qpos);
           if (pg >= 0) kp = *reinterpret_cast<const int4*>(p.c.pos + page_rows(p.c, pg, h) + (r & pmask));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int dist = abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w));
-            s[i >> 4][(i & 15) + e] -= slope * (float)dist;
+            if (kHasBias) s[i >> 4][(i & 15) + e] -= slope * (float)dist;
             if (p.window > 0 && dist >= p.window) hidden |= 1u << (i + e);
           }
         }
+        mx = tile_max(s);
       } else if (p.window > 0 && start + wz - j0 >= p.window) {
         const int qrel = start + ti - j0;
         hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
       }
-      hide(s, hidden);
+      hide(s, hidden, mx);
       return hidden;
     };
     if (x >= x0) {
@@ -727,16 +744,17 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         if (lane_of(max(x - 2, x0) * kBN) < 0) block(x);
       };
       block(x);
-      fetch(p.c.k, raws, x);
+      fetch_all(p.c.k, raws, x);
       vm_wait();
       convert(raws, 0, pks, x);
       lds_sync();
-      fetch(p.c.v, raws + kTile / 2, x);
-      fetch(p.c.k, raws, max(x - 1, x0));
+      fetch_all(p.c.v, raws + kTile / 2, x);
+      fetch_all(p.c.k, raws, max(x - 1, x0));
       f32x16 s0[kN2], s1[kN2];
-      scores(0, s0);
-      unsigned hidden = finish(s0, x, held(x));
-      raise(tile_max(s0));
+      const float sl = p.c.pos ? 0.f : slope;           // (positions of their own: mask() subtracts the bias)
+      float mx = first_scores(s0, dist0(start + ti - x * kBN), sl);
+      unsigned hidden = mask(s0, x, held(x), mx);
+      raise(mx);
       auto top = [&](bool more) __attribute__((always_inline)) -> unsigned long long {
         vm_wait();                                      // this wave's codes have landed
         lds_sync();                                     // nobody reads the last tiles any more
@@ -763,9 +781,10 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         unsigned hid2 = 0;
         ahead(x);
         const auto load = [&](int i) __attribute__((always_inline)) {
-          if (i == 0) fetch(p.c.v, raws + kTile / 2, x - 1); else fetch(p.c.k, raws, max(x - 2, x0));
+          if (i < kCt) fetch(p.c.v, raws + kTile / 2, x - 1, i); else fetch(p.c.k, raws, max(x - 2, x0), i - kCt);
         };
-        step(s, s2, 0, 0, load, [&](f32x16 (&f)[kN2]) __attribute__((always_inline)) { hid2 = finish(f, x - 1, held(x - 1)); });
+        step(s, s2, 0, 0, dist0(start + ti - (x - 1) * kBN), sl, Par<2 * kCt>{}, load,
+             [&](f32x16 (&f)[kN2], float& mx) __attribute__((always_inline)) { hid2 = mask(f, x - 1, held(x - 1), mx); });
         if (bad) dirty(bad);
         hidden = hid2;
         --x;
@@ -773,12 +792,8 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 #pragma unroll 1
       while (x > x0) {
         one(s0, s1);
-        if (x <= x0) {
 #pragma unroll
-          for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
-          break;
-        }
-        one(s1, s0);
+        for (int i = 0; i < kN2; ++i) s0[i] = s1[i];
       }
       const unsigned long long bad = top(false);
       weights(s0);
@@ -807,15 +822,21 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
           make_uint2(cvt2(o[d][4 * r4] * inv, o[d][4 * r4 + 1] * inv), cvt2(o[d][4 * r4 + 2] * inv, o[d][4 * r4 + 3] * inv));
 }
 
-template <int D>
-hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
+template <int D, int SHAPE>
+hipError_t launch_shape(const AttnExtendLaunch& p, hipStream_t s) {
   const int64_t slots = p.T * (p.H / p.H_kv) / kBM + p.N;
   const dim3 grid((unsigned)(slots * p.H_kv));
   if (p.c.k)
-    extend_kernel<D, true><<<grid, kExtThreads, 0, s>>>(p);
+    extend_kernel<D, true, SHAPE><<<grid, kExtThreads, 0, s>>>(p);
   else
-    extend_kernel<D, false><<<grid, kExtThreads, 0, s>>>(p);
+    extend_kernel<D, false, SHAPE><<<grid, kExtThreads, 0, s>>>(p);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
+  if (p.softcap > 0.f) return p.slopes ? launch_shape<D, kCapBias>(p, s) : launch_shape<D, kCap>(p, s);
+  return p.slopes || !(p.scale > 0.f) ? launch_shape<D, kBias>(p, s) : launch_shape<D, kRaw>(p, s);
 }
 
 }  // namespace
