@@ -38,7 +38,7 @@ from ._lib import GDN_BF16, GDN_F32, GDN_MODE_GDN, GDN_MODE_SSD, GDNError
 __all__ = ["load", "gate", "ssd_gate", "extend", "extend_noalloc", "extend_kernel",
            "extend_workspace_size", "decode", "conv1d", "conv1d_update", "validate_slots", "forward_gdn",
            "ssd_combined_fwd", "GDNError", "split_mixed_qkv", "probe_copy", "probe_mfma",
-           "KVCache", "kv_cache", "kv_store", "attn_extend", "attn_decode", "attn_decode_workspace_size",
+           "KVCache", "kv_cache", "kv_store", "attn_extend", "attn_extend_workspace_size", "attn_decode", "attn_decode_workspace_size",
            "kv_evict", "kv_evict_workspace_size", "forward_attn"]
 
 
@@ -709,5 +709,5 @@ def ssd_combined_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=F
     return o.view(batch, L, H, P), (pool if return_final_states else None)
 
 
-from .attention import (KVCache, attn_decode, attn_decode_workspace_size, attn_extend, forward_attn,  # noqa: E402
-                        kv_cache, kv_evict, kv_evict_workspace_size, kv_store)
+from .attention import (KVCache, attn_decode, attn_decode_workspace_size, attn_extend,  # noqa: E402
+                        attn_extend_workspace_size, forward_attn, kv_cache, kv_evict, kv_evict_workspace_size, kv_store)

@@ -16,7 +16,7 @@ EXPORTED = ["gdn_gate", "gdn_extend", "gdn_decode", "gdn_extend_gated", "gdn_dec
             "gdn_conv1d", "gdn_conv1d_update", "gdn_validate_slots", "gdn_status_str",
             "gdn_last_hip_error", "gdn_abi_version", "gdn_extend_workspace_size", "gdn_extend_kernel",
             "gdn_extend_noalloc", "gdn_probe_copy", "gdn_probe_mfma",
-            "gdn_kv_store", "gdn_attn_extend", "gdn_attn_decode", "gdn_attn_decode_workspace_size",
+            "gdn_kv_store", "gdn_attn_extend", "gdn_attn_extend_workspace_size", "gdn_attn_decode", "gdn_attn_decode_workspace_size",
             "gdn_kv_evict", "gdn_kv_evict_workspace_size"]
 
 # gdn_extend_kernel results and reason bits (include/gdn.h)
@@ -97,7 +97,8 @@ class AttnExtendArgs(C.Structure):
                 ("cu_seqlens", C.c_void_p), ("cache_len", C.c_void_p), ("start", C.c_void_p),
                 ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32),
                 ("causal", C.c_int32), ("visible", C.c_void_p), ("doc", C.c_void_p), ("slopes", C.c_void_p),
-                ("window", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float), ("_pad0", C.c_int32)]
+                ("window", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float), ("_pad0", C.c_int32),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
 
 
 class AttnDecodeArgs(C.Structure):
@@ -156,7 +157,8 @@ def load(path: str | None = None) -> C.CDLL:
                      ("gdn_attn_decode", AttnDecodeArgs), ("gdn_kv_evict", KVEvictArgs)):
         getattr(lib, fn).argtypes = [C.POINTER(args), C.c_void_p]
         getattr(lib, fn).restype = C.c_int
-    for fn, args in (("gdn_attn_decode_workspace_size", AttnDecodeArgs), ("gdn_kv_evict_workspace_size", KVEvictArgs)):
+    for fn, args in (("gdn_attn_extend_workspace_size", AttnExtendArgs),
+                     ("gdn_attn_decode_workspace_size", AttnDecodeArgs), ("gdn_kv_evict_workspace_size", KVEvictArgs)):
         getattr(lib, fn).argtypes = [C.POINTER(args)]
         getattr(lib, fn).restype = C.c_int64
     lib.gdn_status_str.argtypes = [C.c_int]

@@ -193,21 +193,8 @@ def kv_store(k, v, cu_seqlens, cache: KVCache, block_table, cache_len, *, start=
 
 
 # ------------------------------------------------------------------ attention
-def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0, slopes=None,
-                window: int = 0, doc=None, visible=None, cache: KVCache | None = None, block_table=None,
-                cache_len=None, start=None, out=None):
-    """Attention of packed new tokens over their own keys and values and, with `cache`, the
-    cache_len[n] rows that each sequence holds already.  q [T, H, d], k, v [T, H_kv, d]
-    bf16; cu_seqlens int32 [N+1].
-    softcap: scores become softcap * tanh(score / softcap) (0: none).  slopes fp32 [H]: a
-    bias of -slope * |distance|.  window: only keys closer than this (0: all).  visible
-    int32 [N]: the first visible[n] tokens are seen by every token of the sequence (prefix
-    mask); causal=False lets every token see every other.  doc int32 [T]: a token sees only
-    tokens with its own id; a negative id sees nothing and is not seen (output 0).
-    start int32 [N]: position of each first token (default: behind the cached rows).
-    Returns out [T, H, d] bf16 (rows behind the last sequence, and those of sequences with
-    cache_len[n] < 0, are not written)."""
-    lib = _lib.load()
+def _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache, block_table,
+                 cache_len, start, out):
     T, H, d = q.shape
     H_kv, N = k.shape[1], cu_seqlens.shape[0] - 1
     if cache is not None:
@@ -221,17 +208,56 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
             raise ValueError("block_table and cache_len need a cache")
         ca, ts, tw = _NO_CACHE, 0, 0
         i = _place(q, k, v, cu_seqlens, slopes, doc, visible, start, out)
-    if out is None:
-        out = _like(q)
-    args = _lib.AttnExtendArgs(
+    # (a query of the workspace reads no buffer: an aligned stand-in for the output)
+    o, os = (256, H * d) if out is None else (out.data_ptr(), _heads(out, "out", T, H, d))
+    return _lib.AttnExtendArgs(
         ca, GDN_BF16, GDN_BF16, N, H, H_kv, d, T, q.data_ptr(), _heads(q, "q", T, H, d), k.data_ptr(),
-        _heads(k, "k", T, H_kv, d), v.data_ptr(), _heads(v, "v", T, H_kv, d), out.data_ptr(),
-        _heads(out, "out", T, H, d), _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(cache_len, "cache_len", N),
+        _heads(k, "k", T, H_kv, d), v.data_ptr(), _heads(v, "v", T, H_kv, d), o, os,
+        _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(cache_len, "cache_len", N),
         _vec(start, "start", N), _at(block_table), ts, tw, 1 if causal else 0, _vec(visible, "visible", N),
         _vec(doc, "doc", T), _vec(slopes, "slopes", H, _F32), window, d ** -0.5 if scale is None else scale,
-        softcap)
+        softcap), i
+
+
+def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0, slopes=None,
+                window: int = 0, doc=None, visible=None, cache: KVCache | None = None, block_table=None,
+                cache_len=None, start=None, out=None, workspace: torch.Tensor | None = None):
+    """Attention of packed new tokens over their own keys and values and, with `cache`, the
+    cache_len[n] rows that each sequence holds already.  q [T, H, d], k, v [T, H_kv, d]
+    bf16; cu_seqlens int32 [N+1].
+    softcap: scores become softcap * tanh(score / softcap) (0: none).  slopes fp32 [H]: a
+    bias of -slope * |distance|.  window: only keys closer than this (0: all).  visible
+    int32 [N]: the first visible[n] tokens are seen by every token of the sequence (prefix
+    mask); causal=False lets every token see every other.  doc int32 [T]: a token sees only
+    tokens with its own id; a negative id sees nothing and is not seen (output 0).
+    start int32 [N]: position of each first token (default: behind the cached rows).
+    workspace: uint8 device tensor of attn_extend_workspace_size bytes (else one is
+    allocated where the keys of few rows are split).
+    Returns out [T, H, d] bf16 (rows behind the last sequence, and those of sequences with
+    cache_len[n] < 0, are not written)."""
+    lib = _lib.load()
+    if out is None:
+        out = _like(q)
+    args, i = _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache,
+                           block_table, cache_len, start, out)
+    # (fewer than 512 keys are not split: no query, which short calls would feel)
+    ws = None
+    if workspace is not None or cache is not None or q.shape[0] >= 512:
+        ws = _attach("gdn_attn_extend", lib.gdn_attn_extend_workspace_size, args, i, workspace)
     _run("gdn_attn_extend", lib.gdn_attn_extend, args, i)
+    del ws
     return out
+
+
+def attn_extend_workspace_size(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0,
+                               slopes=None, window: int = 0, doc=None, visible=None, cache: KVCache | None = None,
+                               block_table=None, cache_len=None, start=None) -> int:
+    """Bytes of workspace with which attn_extend splits the keys of these arguments (0: no
+    split)."""
+    lib = _lib.load()
+    args, i = _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache,
+                           block_table, cache_len, start, None)
+    return _need("gdn_attn_extend_workspace_size", lib.gdn_attn_extend_workspace_size, args, i)
 
 
 def _decode_args(q, cache, block_table, kv_len, scale, softcap, slopes, window, q_pos, accumulate, max_kvlen, out):

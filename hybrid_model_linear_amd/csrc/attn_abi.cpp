@@ -109,6 +109,74 @@ int plan_decode(const gdn_attn_decode_args* a, gdn::AttnDecodeLaunch& p, int64_t
   return GDN_OK;
 }
 
+// Descriptor of an extend call; need receives the workspace bytes with which its keys are split.
+int plan_extend(const gdn_attn_extend_args* a, gdn::AttnExtendLaunch& p, int64_t& need) {
+  need = 0;
+  if (!a) return GDN_E_NULL;
+  if (a->in_dtype != GDN_BF16 || a->out_dtype != GDN_BF16) return GDN_E_DTYPE;
+  if (a->d != 64 && a->d != 128 && a->d != 256) return GDN_E_UNSUPPORTED;
+  if (a->N < 0 || a->T < 0 || a->T > INT32_MAX || a->H_kv <= 0 || a->H <= 0 || a->H % a->H_kv != 0) return GDN_E_SHAPE;
+  int st = check_scores(a->scale, a->softcap, a->window);
+  if (st != GDN_OK) return st;
+  if (a->cache.k) {
+    st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, false, p.c);
+    if (st != GDN_OK) return st;
+    if (p.c.d != a->d || p.c.H_kv != a->H_kv) return GDN_E_SHAPE;
+    if (a->doc) return GDN_E_UNSUPPORTED;
+    if (a->N > 0 && !a->cache_len) return GDN_E_NULL;
+  } else if (a->cache_len || a->block_table) {
+    return GDN_E_NULL;
+  }
+  if (a->T > 0 && (!a->q || !a->k || !a->v || !a->out)) return GDN_E_NULL;
+  if (a->N > 0 && !a->cu_seqlens) return GDN_E_NULL;
+  if (!rows_ok(a->q, a->q_stride, a->H, a->d) || !rows_ok(a->k, a->k_stride, a->H_kv, a->d) ||
+      !rows_ok(a->v, a->v_stride, a->H_kv, a->d) || !rows_ok(a->out, a->out_stride, a->H, a->d))
+    return GDN_E_SHAPE;
+  const int64_t out_bytes = rows_bytes(a->T, a->out_stride, (int64_t)a->H * a->d);
+  if (overlap(a->out, out_bytes, a->q, rows_bytes(a->T, a->q_stride, (int64_t)a->H * a->d)) ||
+      overlap(a->out, out_bytes, a->k, rows_bytes(a->T, a->k_stride, (int64_t)a->H_kv * a->d)) ||
+      overlap(a->out, out_bytes, a->v, rows_bytes(a->T, a->v_stride, (int64_t)a->H_kv * a->d)))
+    return GDN_E_SHAPE;
+  if (a->N == 0 || a->T == 0) return GDN_OK;
+  const int64_t rows = a->T * (a->H / a->H_kv);          // (token, head of a group) rows: 32-bit in the kernel
+  if (rows > INT32_MAX - 1024 || (rows / 128 + a->N) * a->H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
+  p.N = a->N;
+  p.T = a->T;
+  p.H = a->H;
+  p.H_kv = a->H_kv;
+  p.d = a->d;
+  p.q = static_cast<const gdn::u16*>(a->q);
+  p.q_stride = a->q_stride;
+  p.k = static_cast<const gdn::u16*>(a->k);
+  p.k_stride = a->k_stride;
+  p.v = static_cast<const gdn::u16*>(a->v);
+  p.v_stride = a->v_stride;
+  p.out = static_cast<gdn::u16*>(a->out);
+  p.out_stride = a->out_stride;
+  p.cu = a->cu_seqlens;
+  p.cache_len = a->cache_len;
+  p.start = a->start;
+  p.causal = a->causal != 0;
+  p.visible = a->visible;
+  p.doc = a->doc;
+  p.slopes = a->slopes;
+  p.window = a->window;
+  p.scale = a->scale;
+  p.softcap = a->softcap;
+  const int64_t group = a->H / a->H_kv;
+  int64_t keys = (a->T + a->N - 1) / a->N;               // (a table has room for the new tokens as a rule)
+  if (p.c.k && (int64_t)a->table_width * a->cache.page > keys) keys = (int64_t)a->table_width * a->cache.page;
+  if (a->window > 0 && !(p.c.k && a->cache.pos) && keys > a->window + 128 / group + 64) keys = a->window + 128 / group + 64;
+  gdn::plan_attn_extend(p, keys, gdn::current_device_cus());
+  if (p.splits > 1) {
+    const int64_t at = reinterpret_cast<uintptr_t>(a->workspace), heads = p.splits * a->T * a->H;
+    p.part_o = reinterpret_cast<float*>(at);
+    p.part_ml = reinterpret_cast<float*>(at + heads * a->d * 4);
+    need = (heads * (a->d + 2) * 4 + 255) / 256 * 256;
+  }
+  return GDN_OK;
+}
+
 int plan_evict(const gdn_kv_evict_args* a, gdn::EvictLaunch& p, int64_t& need) {
   need = 0;
   if (!a) return GDN_E_NULL;
@@ -174,59 +242,24 @@ int gdn_kv_store(const gdn_kv_store_args* a, void* stream) {
   return gdn::status_of_hip(gdn::launch_kv_store(p, (hipStream_t)stream));
 }
 
-int gdn_attn_extend(const gdn_attn_extend_args* a, void* stream) {
-  if (!a) return GDN_E_NULL;
-  if (a->in_dtype != GDN_BF16 || a->out_dtype != GDN_BF16) return GDN_E_DTYPE;
-  if (a->d != 64 && a->d != 128 && a->d != 256) return GDN_E_UNSUPPORTED;
-  if (a->N < 0 || a->T < 0 || a->T > INT32_MAX || a->H_kv <= 0 || a->H <= 0 || a->H % a->H_kv != 0) return GDN_E_SHAPE;
-  int st = check_scores(a->scale, a->softcap, a->window);
-  if (st != GDN_OK) return st;
+int64_t gdn_attn_extend_workspace_size(const gdn_attn_extend_args* a) {
   gdn::AttnExtendLaunch p{};
-  if (a->cache.k) {
-    st = check_cache(a->cache, a->N, a->block_table, a->table_stride, a->table_width, false, p.c);
+  int64_t need = 0;
+  const int st = plan_extend(a, p, need);
+  return st == GDN_OK ? need : -(int64_t)st;
+}
+
+int gdn_attn_extend(const gdn_attn_extend_args* a, void* stream) {
+  gdn::AttnExtendLaunch p{};
+  int64_t need = 0;
+  int st = plan_extend(a, p, need);
+  if (st != GDN_OK || a->N == 0 || a->T == 0) return st;
+  if (!a->workspace) {
+    p.splits = 1;
+  } else {
+    st = check_workspace(a->workspace, a->workspace_bytes, need);
     if (st != GDN_OK) return st;
-    if (p.c.d != a->d || p.c.H_kv != a->H_kv) return GDN_E_SHAPE;
-    if (a->doc) return GDN_E_UNSUPPORTED;
-    if (a->N > 0 && !a->cache_len) return GDN_E_NULL;
-  } else if (a->cache_len || a->block_table) {
-    return GDN_E_NULL;
   }
-  if (a->T > 0 && (!a->q || !a->k || !a->v || !a->out)) return GDN_E_NULL;
-  if (a->N > 0 && !a->cu_seqlens) return GDN_E_NULL;
-  if (!rows_ok(a->q, a->q_stride, a->H, a->d) || !rows_ok(a->k, a->k_stride, a->H_kv, a->d) ||
-      !rows_ok(a->v, a->v_stride, a->H_kv, a->d) || !rows_ok(a->out, a->out_stride, a->H, a->d))
-    return GDN_E_SHAPE;
-  const int64_t out_bytes = rows_bytes(a->T, a->out_stride, (int64_t)a->H * a->d);
-  if (overlap(a->out, out_bytes, a->q, rows_bytes(a->T, a->q_stride, (int64_t)a->H * a->d)) ||
-      overlap(a->out, out_bytes, a->k, rows_bytes(a->T, a->k_stride, (int64_t)a->H_kv * a->d)) ||
-      overlap(a->out, out_bytes, a->v, rows_bytes(a->T, a->v_stride, (int64_t)a->H_kv * a->d)))
-    return GDN_E_SHAPE;
-  if (a->N == 0 || a->T == 0) return GDN_OK;
-  const int64_t rows = a->T * (a->H / a->H_kv);          // (token, head of a group) rows: 32-bit in the kernel
-  if (rows > INT32_MAX - 1024 || (rows / 128 + a->N) * a->H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
-  p.N = a->N;
-  p.T = a->T;
-  p.H = a->H;
-  p.H_kv = a->H_kv;
-  p.d = a->d;
-  p.q = static_cast<const gdn::u16*>(a->q);
-  p.q_stride = a->q_stride;
-  p.k = static_cast<const gdn::u16*>(a->k);
-  p.k_stride = a->k_stride;
-  p.v = static_cast<const gdn::u16*>(a->v);
-  p.v_stride = a->v_stride;
-  p.out = static_cast<gdn::u16*>(a->out);
-  p.out_stride = a->out_stride;
-  p.cu = a->cu_seqlens;
-  p.cache_len = a->cache_len;
-  p.start = a->start;
-  p.causal = a->causal != 0;
-  p.visible = a->visible;
-  p.doc = a->doc;
-  p.slopes = a->slopes;
-  p.window = a->window;
-  p.scale = a->scale;
-  p.softcap = a->softcap;
   return gdn::status_of_hip(gdn::launch_attn_extend(p, (hipStream_t)stream));
 }
 

@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kExtThreads = 256;
 constexpr int kBM = 128;      // rows of a workgroup
+constexpr int kMaxSplits = 16;
 constexpr int kFlags = 4096;  // document mask: key tiles whose overlap is looked up ahead
 
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
@@ -429,7 +430,19 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     first = (int)max((int64_t)0, (int64_t)ta - p.window + 1);
     last = (int)min((int64_t)last, (int64_t)tz + p.window);
   }
-  const int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;
+  int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;    // tiles [d0, d1), from the last
+  // Cached tiles x, x - 1, ... x0, without those that a window leaves out for every row
+  int x0 = 0, x = CACHED ? (P + kBN - 1) / kBN - 1 : -1;
+  if (CACHED && p.window > 0 && !p.c.pos)
+    x0 = (int)min((int64_t)(x + 1), max((int64_t)0, (int64_t)start + ta - p.window + 1) / kBN);
+  if (p.splits > 1) {                                   // this workgroup's part of both
+    const int nd = max(d1 - d0, 0), nt = nd + x + 1 - x0;
+    const int a = (int)((int64_t)nt * blockIdx.y / p.splits), b = (int)((int64_t)nt * (blockIdx.y + 1) / p.splits);
+    d0 = d1 - min(b, nd);
+    d1 -= min(a, nd);
+    x0 = x + 1 - max(b - nd, 0);
+    x -= max(a - nd, 0);
+  }
   // Document mask: which key tiles hold a document of this workgroup's rows, a wave per
   // tile.  (Rows with a negative id see nothing: they take part as they come and give
   // zeros in the end.)
@@ -630,12 +643,6 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     constexpr int kCp = D / 16;                         // 16-code pieces of a row
     constexpr int kCr = kWave / kCp;                    // rows that one wave's load brings
     constexpr int kCt = kBN / kCr / 4;                  // loads per wave and tile
-    const int tiles = (P + kBN - 1) / kBN;
-    int x0 = 0, x = tiles - 1;                          // tiles x, x - 1, ... x0
-    if (p.window > 0 && !p.c.pos) {                     // rows that a window leaves out for every row
-      const int64_t first = (int64_t)start + ta - p.window + 1;
-      x0 = (int)min((int64_t)tiles, max((int64_t)0, first) / kBN);
-    }
     // A load brings 4, 8 or 16 rows of one page, so page addresses and scales are the same in
     // every lane of a wave.  Lane l holds those of page pb + l of the sequence (its place in
     // units of 16 rows, -1: not there), 64 pages at a time; a load's are read out of the lanes.
@@ -805,6 +812,20 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
 
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
+  if (p.splits > 1) {                                   // sums and outputs as they are, for extend_join_kernel
+    const int64_t row = ((int64_t)blockIdx.y * p.T + t0 + ti) * p.H + hq;
+    const bool none = doc && di < 0;
+    if (hh == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * row) = none ? make_float2(-INFINITY, 0.f) : make_float2(m == -INFINITY ? m : base, l);
+    float* at = p.part_o + row * D;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4)
+        *reinterpret_cast<float4*>(at + 32 * d + 8 * r4 + 4 * hh) =
+            none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(o[d][4 * r4], o[d][4 * r4 + 1], o[d][4 * r4 + 2], o[d][4 * r4 + 3]);
+    return;
+  }
   float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);   // nothing seen: zeros; a NaN sum stays NaN
   if (doc && di < 0) {                                  // a row outside of all documents
     inv = 0.f;
@@ -822,14 +843,47 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
           make_uint2(cvt2(o[d][4 * r4] * inv, o[d][4 * r4 + 1] * inv), cvt2(o[d][4 * r4 + 2] * inv, o[d][4 * r4 + 3] * inv));
 }
 
+// Joins the parts of a row: o = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M), M the largest m_s.
+// D / 4 lanes per (token, head), the heads of a token side by side.
+template <int D> __global__ void __launch_bounds__(kExtThreads) extend_join_kernel(const AttnExtendLaunch p) {
+  constexpr int kLanes = D / 4;
+  const int t = blockIdx.x, hq = blockIdx.y * (kExtThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes * 4;
+  if (t < p.cu[0] || t >= p.cu[p.N]) return;            // (in every lane; rows that no sequence holds)
+  const int n = find_last(p.N, threadIdx.x & 63, [&](int i) { return p.cu[i] <= t; });
+  if (hq >= p.H || (p.cache_len && p.cache_len[n] < 0)) return;
+  const int64_t step = p.T * p.H, row = (int64_t)t * p.H + hq;
+  float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_ml[2 * (row + s * step)]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (row + s * step));
+    const float4 x = *reinterpret_cast<const float4*>(p.part_o + (row + s * step) * D + c);
+    const float f = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - M);   // (0 times a NaN sum stays NaN)
+    l += ml.y * f;
+    o.x += x.x * f;
+    o.y += x.y * f;
+    o.z += x.z * f;
+    o.w += x.w * f;
+  }
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.out_stride + (int64_t)hq * D + c) =
+      make_uint2(cvt2(o.x * inv, o.y * inv), cvt2(o.z * inv, o.w * inv));
+}
+
 template <int D, int SHAPE>
 hipError_t launch_shape(const AttnExtendLaunch& p, hipStream_t s) {
   const int64_t slots = p.T * (p.H / p.H_kv) / kBM + p.N;
-  const dim3 grid((unsigned)(slots * p.H_kv));
+  const dim3 grid((unsigned)(slots * p.H_kv), (unsigned)p.splits);
   if (p.c.k)
     extend_kernel<D, true, SHAPE><<<grid, kExtThreads, 0, s>>>(p);
   else
     extend_kernel<D, false, SHAPE><<<grid, kExtThreads, 0, s>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (p.splits == 1 || e != hipSuccess) return e;
+  constexpr int kRows = kExtThreads / (D / 4);
+  extend_join_kernel<D><<<dim3((unsigned)p.T, (p.H + kRows - 1) / kRows), kExtThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -840,6 +894,23 @@ hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
 }
 
 }  // namespace
+
+// Parts of every row's keys.  A workgroup walks its keys one tile after the other (about 1.25
+// us a tile, 2.5 at d = 256), so with few rows most of the chip waits for a few long walks:
+// 16 tokens over 8000 cached rows, 32 / 8 heads, d = 128: 196 us whole, 25 in 16 parts; 512
+// over 8000 222 and 106; 64 over 16000, 16 / 2, d = 256: 667 and 62.  Parts cost a launch and
+// their way through memory, about 5 us and 15 with all places taken, and pay where the walk
+// is shortened by more: 1024 new tokens 23 us whole, 36 in two parts; 8 over 600 22 and 18.
+// All parts have a place at once (two workgroups per CU, one at d = 256; twice as many for the
+// sake of uneven sequences: 2 x 256 over 7000, d = 256, 111 -> 128) and four tiles or more.
+void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus) {
+  const int64_t wgs = (p.T * (p.H / p.H_kv) + kBM - 1) / kBM * p.H_kv, places = (int64_t)cus * (p.d <= 128 ? 2 : 1);
+  const int64_t fit = places / wgs, most = keys / (4 * 64);
+  int64_t s = fit < most ? fit : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  const double tiles = (double)keys / 64, step = p.d == 256 ? 2.5 : 1.25;
+  p.splits = s > 1 && tiles * step * (double)(s - 1) / (double)s > 5 + 15.0 * (double)(s * wgs) / (double)places ? (int)s : 1;
+}
 
 hipError_t launch_attn_extend(const AttnExtendLaunch& p, hipStream_t s) {
   switch (p.d) {

@@ -478,7 +478,11 @@ int gdn_kv_store(const gdn_kv_store_args* args, void* stream);
  *   q, out : bf16 [T, H, d]; k, v : bf16 [T, H_kv, d]; heads contiguous, 16-byte aligned
  *   rows (strides multiples of 8, at most 2^22).
  * cu_seqlens follows gdn_extend: cu_seqlens[N] <= T, rows behind the last sequence are
- * not written.  out must not overlap an input.  The new tokens are not stored (gdn_kv_store).  One launch. */
+ * not written.  out must not overlap an input.  The new tokens are not stored (gdn_kv_store).
+ * T * (H / H_kv) must stay below 2^31 - 1024 (GDN_E_UNSUPPORTED).
+ * With few rows the keys are split over workgroups, whose parts stand in a workspace of
+ * gdn_attn_extend_workspace_size bytes (0: none), 256-byte aligned; without one (NULL) they
+ * are not split.  One launch, two with a split. */
 typedef struct gdn_attn_extend_args {
   gdn_kv_cache cache;
   int32_t in_dtype;            /* GDN_BF16                         */
@@ -508,8 +512,13 @@ typedef struct gdn_attn_extend_args {
   float scale;
   float softcap;               /* 0 = none                         */
   int32_t _pad0;
+  void* workspace;             /* or NULL                          */
+  int64_t workspace_bytes;
 } gdn_attn_extend_args;
 int gdn_attn_extend(const gdn_attn_extend_args* args, void* stream);
+/* Workspace bytes with which a gdn_attn_extend call with these arguments splits its keys,
+ * or minus the gdn_status of a call that would be refused. */
+int64_t gdn_attn_extend_workspace_size(const gdn_attn_extend_args* args);
 
 /* gdn_attn_decode: one token per sequence over the rows 0 .. kv_len[n] - 1 of the cache
  * (its own row among them: gdn_kv_store first).  kv_len[n] = 0 writes zeros, kv_len[n] < 0

@@ -173,6 +173,22 @@ def test_workspaces():
         lib.gdn_kv_evict_workspace_size(ct.byref(_evict(budget=256)))
 
 
+def test_extend_workspace():
+    lib = gdn.load()
+    size = lambda *a, **kw: lib.gdn_attn_extend_workspace_size(ct.byref(_extend(*a, **kw)))  # noqa: E731
+    wide = dict(table_width=4096, table_stride=4096)
+    assert size() == 0 and size(_cache()) == 0                                # too few keys
+    need = size(_cache(), **wide)
+    assert need > 0 and need % 256 == 0
+    assert size(_cache(pos=None), window=100, **wide) == 0                    # a window leaves too few
+    assert size(_cache(), window=100, **wide) == need                         # (not where rows hold positions of their own)
+    assert size(T=40000, N=1) == 0                                            # rows enough
+    assert size(T=2000, N=1) > 0 and size(T=2000, N=40) == 0
+    assert size(H=0) == -SHAPE and size(d=96) == -UNSUP
+    for ws, nbytes in ((P, need - 1), (P + 64, need)):
+        assert lib.gdn_attn_extend(ct.byref(_extend(_cache(), workspace=ws, workspace_bytes=nbytes, **wide)), None) == SHAPE
+
+
 # ------------------------------------------------------------------ binding
 def _tensors(**kw):
     z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)  # noqa: E731
