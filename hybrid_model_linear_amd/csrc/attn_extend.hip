@@ -20,11 +20,12 @@
 // is on the global side.  Cached rows arrive as codes the same way; the lane that asked
 // for a piece turns it into bf16 times its page's power-of-two scale (exact).
 // The loop is a tile deep: while the matrix units form the scores of the next tile, the
-// vector units turn this tile's into weights; then, under the second product, they look
-// for the next tile's maximum.  (One after the other, both kept the SIMDs busy 44% of the
-// time each with hardly any overlap, even with two workgroups on a CU: 944 TFLOP/s at
-// 8 x 4096 tokens, 32 / 8 heads, d = 128.)  Up to d = 128 two workgroups fit a CU; at d =
-// 256 one does (its output alone takes 128 registers).
+// vector units turn this tile's into weights; then, under the second product, they cap and
+// bias the next tile's scores and look for their maximum.  (One after the other, both kept
+// the SIMDs busy 44% of the time each with hardly any overlap, even with two workgroups on
+// a CU: 944 TFLOP/s at 8 x 4096 tokens, 32 / 8 heads, d = 128; now 1030 - 1060, where a
+// library product of two matrices of 16384^2 normal values reaches 1390.)  Up to d = 128
+// two workgroups fit a CU; at d = 256 one does (its output alone takes 128 registers).
 // Keys are taken from the last to the first, the new tokens before the cached: with a
 // distance bias the nearest keys set the maximum at once and the sums are not rescaled again.
 // The weights are rounded to bf16 for the second product, their sum is not.
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   bf16x8 pb[2 * kN2];                      // the weights as operands, 16 keys each
 
   constexpr int kNS = kN2 * kU, kNP = 2 * kN2 * kDT;   // MFMAs of a tile's scores and of its product
-  constexpr int kRing = 4;                 // operands in flight
+  constexpr int kRing = 4;                 // operands in flight (3, 6 and 8 are no faster)
   auto k_op = [&](int i, uint32_t koff) __attribute__((always_inline)) {   // operand i of the K tile at koff
     const int t = i % kN2, u = i / kN2;
     return lds_op(ka[u & 7] + (koff + t * 32 * 2 * D + (u >> 3) * 256));
@@ -268,13 +269,15 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   };
   // One step: weights of the tile in s under the scores of the next (s2), then this tile's
   // product, under which the new scores are shaped and their maximum is found; kRaw leaves
-  // half of the weights to the first half of the product.  load(j) starts one of
-  // the loads of later tiles; mask(s2, mx) hides scores of a tile that is seen in part.  The order is fixed here, an MFMA and
-  // its share of vector work at a time with operands kRing MFMAs ahead: left alone, the
-  // compiler waits for each read before its MFMA and puts the vector work behind them all.
+  // half of the weights to the first half of the product.  load(j) starts one of the loads
+  // of later tiles; mask(s2, mx) hides scores of a tile that is seen in part.  The order is
+  // fixed here, an MFMA and its share of vector work at a time with operands kRing MFMAs
+  // ahead: left alone, the compiler waits for each read before its MFMA and puts the vector
+  // work behind them all.
   auto step = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t koff, uint32_t voff, float dq, float sl, auto loads,
                   auto load, auto mask) __attribute__((always_inline)) {
-    constexpr int kW = SHAPE == kRaw && D < 256 ? kS / 2 : kS;   // weights formed under the scores
+    // weights formed under the scores (half of them: 8 x 4096, d = 128 1.09 -> 1.06 ms; d = 256 no change)
+    constexpr int kW = SHAPE == kRaw && D < 256 ? kS / 2 : kS;
     constexpr int kFirst = kW / 8;                      // of them, while the first operands are on their way
     constexpr int kH = kNP / 2, kQ = kH - 1, kLoads = decltype(loads)::value;
     auto part = [](int i, int n, int of, int from) { return from + i * of / n; };

@@ -522,11 +522,11 @@ int64_t gdn_attn_extend_workspace_size(const gdn_attn_extend_args* args);
 
 /* gdn_attn_decode: one token per sequence over the rows 0 .. kv_len[n] - 1 of the cache
  * (its own row among them: gdn_kv_store first).  kv_len[n] = 0 writes zeros, kv_len[n] < 0
- * marks a padding row: nothing of it is read or written.  The query's position is q_pos[n]
+ * marks a padding row: its output row is left as it is.  The query's position is q_pos[n]
  * (NULL: kv_len[n] - 1); with a window only rows closer than it are seen.  accumulate != 0
  * adds to cache.weight of every row of the sequence the sum of the softmax weights that
  * the kv head's H / H_kv query heads give it; sequences of one call must then not share
- * pages.  max_kvlen is a host hint of the longest kv_len (0 = unknown): speed only.
+ * pages.  N is at most 65535.  max_kvlen is a host hint of the longest kv_len (0 = unknown): speed only.
  * The rows are split over workgroups, whose partial results a second launch joins; they
  * stand in a workspace of gdn_attn_decode_workspace_size bytes (0: none needed), 256-byte
  * aligned, with any contents; calls in flight at once need their own. */
@@ -571,7 +571,9 @@ int64_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
  * Rows at or past new_len mean nothing afterwards.  The cache needs pos and weight.
  * A sequence with an id out of range among its pages' first kv_len[n] rows is left as it
  * is, with new_len[n] = kv_len[n].  Sequences must not share pages.  0 <= recent <= budget,
- * budget >= 1 (a budget past the table's rows counts as those).  Two launches; workspace as for gdn_attn_decode. */
+ * budget >= 1 (a budget past the table's rows counts as those), N at most 65535, fewer
+ * than 2^31 rows (num_pages * page) in the cache (GDN_E_UNSUPPORTED).  Two launches;
+ * workspace as for gdn_attn_decode. */
 typedef struct gdn_kv_evict_args {
   gdn_kv_cache cache;
   int32_t N;
