@@ -14,6 +14,7 @@ bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t
 
 constexpr int64_t kMaxStride = 1 << 22;     // a 64-row tile's byte offsets stay in 32 bits
 constexpr int64_t kMaxGrid = INT32_MAX;
+constexpr int32_t kMaxWindow = 1 << 30;     // distances are shorter; a window added to one stays in 32 bits
 
 int page_log2(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
 
@@ -86,7 +87,7 @@ int plan_decode(const gdn_attn_decode_args* a, gdn::AttnDecodeLaunch& p, int64_t
   p.kv_len = a->kv_len;
   p.q_pos = a->q_pos;
   p.slopes = a->slopes;
-  p.window = a->window;
+  p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
   p.scale = a->scale;
   p.softcap = a->softcap;
   p.accumulate = a->accumulate != 0;
@@ -160,7 +161,7 @@ int plan_extend(const gdn_attn_extend_args* a, gdn::AttnExtendLaunch& p, int64_t
   p.visible = a->visible;
   p.doc = a->doc;
   p.slopes = a->slopes;
-  p.window = a->window;
+  p.window = a->window < kMaxWindow ? a->window : kMaxWindow;
   p.scale = a->scale;
   p.softcap = a->softcap;
   const int64_t group = a->H / a->H_kv;

@@ -408,7 +408,8 @@ int gdn_conv1d_update(const gdn_conv_args* args, void* stream);
  * and o_i = 0 for a query that sees nothing.  bf16 inputs and outputs, d in {64, 128,
  * 256}, fp32 scores, softmax statistics and sums; the softmax weights are rounded to
  * bf16 for the product with the values.  A value that a query does not see does not
- * reach it, whatever it holds (NaN and infinities too).
+ * reach it, whatever it holds (NaN and infinities too).  Positions, given or from lengths,
+ * lie in [0, 2^30).
  *
  * The cache.  Pages of `page` rows; row r of a sequence is row r % page of the page
  * block_table[n, r / page] (row stride table_stride, table_width entries per sequence).
@@ -481,8 +482,9 @@ int gdn_kv_store(const gdn_kv_store_args* args, void* stream);
  * not written.  out must not overlap an input.  The new tokens are not stored (gdn_kv_store).
  * T * (H / H_kv) must stay below 2^31 - 1024 (GDN_E_UNSUPPORTED).
  * With few rows the keys are split over workgroups, whose parts stand in a workspace of
- * gdn_attn_extend_workspace_size bytes (0: none), 256-byte aligned; without one (NULL) they
- * are not split.  One launch, two with a split. */
+ * gdn_attn_extend_workspace_size bytes (0: none), 256-byte aligned, with any contents (calls in
+ * flight at once need their own); without one (NULL) they are not split.  One launch, two
+ * with a split. */
 typedef struct gdn_attn_extend_args {
   gdn_kv_cache cache;
   int32_t in_dtype;            /* GDN_BF16                         */

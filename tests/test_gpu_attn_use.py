@@ -309,3 +309,22 @@ def test_empty_calls_launch_nothing(gdn_lib):
     gdn_lib.kv_store(kv, kv, i32([0, 0]), c, torch.zeros(1, 3, dtype=torch.int32, device="cuda"), i32([4]))
     torch.cuda.synchronize()
     assert c.k.view(torch.uint8).sum() == 0
+
+
+def test_the_widest_window_hides_nothing(gdn_lib):
+    print("[case] window 2^31 - 1", flush=True)
+    rng = np.random.default_rng(12)
+    lens, H, H_kv, d, page, w = [150, 9], 4, 2, 64, 16, 2 ** 31 - 1
+    x = [up(bf16(rng.normal(size=(sum(lens), h, d))), torch.bfloat16) for h in (H, H_kv, H_kv)]
+    cu, old = i32([0, 150, 159]), [200, 40]
+    c = make_cache(rng, 20, H_kv, page, d, track=True)
+    table = make_table(rng, old, page, 20)
+    c["pos"][:] = rng.integers(0, 1000, c["pos"].shape)
+    for causal in (True, False):
+        assert torch.equal(gdn_lib.attn_extend(*x, cu, causal=causal, window=w), gdn_lib.attn_extend(*x, cu, causal=causal))
+    for track in (True, False):
+        g = upload_cache(gdn_lib, dict(c, pos=c["pos"] if track else None))
+        kw = dict(cache=g, block_table=i32(table), cache_len=i32(old))
+        assert torch.equal(gdn_lib.attn_extend(*x, cu, window=w, **kw), gdn_lib.attn_extend(*x, cu, **kw))
+        q = x[0][:2]
+        assert torch.equal(gdn_lib.attn_decode(q, g, i32(table), i32(old), window=w), gdn_lib.attn_decode(q, g, i32(table), i32(old)))
