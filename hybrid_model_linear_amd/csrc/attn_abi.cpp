@@ -58,6 +58,9 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 
 
 int check_scores(float scale, float softcap, int32_t window) {
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return GDN_E_SHAPE;
+  // the tanh is off by softcap 2^-22 (2^-9 at most here, below the weights' rounding), and its
+  // argument's factor has to be a number
+  if (softcap > 8192.f || (softcap > 0.f && !std::isfinite(scale / softcap * 4.f))) return GDN_E_UNSUPPORTED;
   return GDN_OK;
 }
 

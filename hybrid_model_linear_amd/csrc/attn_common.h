@@ -66,7 +66,7 @@ template <typename F> __device__ __forceinline__ int find_last(int N, int lane, 
 // Raw score q.k -> score in units of log2, after scale and cap: with f1 = scale / cap and
 // f2 = cap log2 e:  f2 tanh(f1 x), tanh(y) = 1 - 2 / (1 + e^2y).  Near 0 that form is
 // off by a few 2^-24 absolutely, i.e. by cap 2^-22 in the score: below the error of the
-// bf16 output for every cap that caps (a few hundred at most).
+// bf16 output for every cap that a call may have (8192 at most).
 __device__ __forceinline__ float capped(float x, float f1x2log2e, float f2) {
   const float e = __builtin_amdgcn_exp2f(x * f1x2log2e);
   return fmaf(-2.0f * f2, __builtin_amdgcn_rcpf(1.0f + e), f2);

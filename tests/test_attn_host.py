@@ -173,6 +173,14 @@ def test_workspaces():
         lib.gdn_kv_evict_workspace_size(ct.byref(_evict(budget=256)))
 
 
+@pytest.mark.parametrize("softcap,scale,status", [(8192.0, 0.1, OK), (8193.0, 0.1, UNSUP), (1e30, 0.1, UNSUP),
+                                                  (1e-38, 10.0, UNSUP), (1e-30, 1.0, OK)])
+def test_caps_that_fp32_cannot_hold(softcap, scale, status):
+    lib, kw = gdn.load(), dict(softcap=softcap, scale=scale)
+    assert lib.gdn_attn_extend(ct.byref(_extend(T=0, **kw)), None) == status
+    assert lib.gdn_attn_decode(ct.byref(_decode(N=0, **kw)), None) == status
+
+
 def test_extend_workspace():
     lib = gdn.load()
     size = lambda *a, **kw: lib.gdn_attn_extend_workspace_size(ct.byref(_extend(*a, **kw)))  # noqa: E731
