@@ -108,9 +108,10 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const int tid = threadIdx.x, wave = (int)uni(threadIdx.x >> 6), lane = tid & 63, q32 = lane & 31, hh = lane >> 5;
   const int G = p.H / p.H_kv;
   // Heads fastest: consecutive workgroups go to the 8 XCDs in turn, so a head's tiles share
-  // an L2.  Late tiles of a causal sequence see the most keys: they are launched first.
-  const int h = blockIdx.x % p.H_kv;
-  const int w = (int)(gridDim.x / p.H_kv) - 1 - (int)(blockIdx.x / p.H_kv);
+  // an L2.  Late tiles of a causal sequence see the most keys: they are launched first, and
+  // from slot p.fold of the launch on the earliest.
+  const int h = blockIdx.x % p.H_kv, pos = blockIdx.x / p.H_kv;
+  const int w = pos < p.fold ? (int)(gridDim.x / p.H_kv) - 1 - pos : pos - p.fold;
   // slot w -> (sequence n, tile): sequence n's tiles begin at floor(cu[n] G / 128) + n
   const int n = find_last(p.N, threadIdx.x & 63, [&](int i) { return p.cu[i] * G / kBM + i <= w; });
   const int t0 = p.cu[n], L = p.cu[n + 1] - t0;
@@ -898,19 +899,26 @@ hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
 
 }  // namespace
 
-// Parts of every row's keys.  A workgroup walks its keys one tile after the other (about 1.25
-// us a tile, 2.5 at d = 256), so with few rows most of the chip waits for a few long walks:
-// 16 tokens over 8000 cached rows, 32 / 8 heads, d = 128: 196 us whole, 25 in 16 parts; 512
-// over 8000 222 and 106; 64 over 16000, 16 / 2, d = 256: 667 and 62.  Parts cost a launch and
-// their way through memory, about 5 us and 15 with all places taken, and pay where the walk
-// is shortened by more: 1024 new tokens 23 us whole, 36 in two parts; 8 over 600 22 and 18.
-// All parts have a place at once (two workgroups per CU, one at d = 256; twice as many for the
-// sake of uneven sequences: 2 x 256 over 7000, d = 256, 111 -> 128) and four tiles or more.
+// How a call is cut.  Parts of every row's keys: a workgroup walks its keys one tile after
+// the other (about 1.25 us a tile, 2.5 at d = 256), so with few rows most of the chip waits
+// for a few long walks: 16 tokens over 8000 cached rows, 32 / 8 heads, d = 128: 196 us
+// whole, 25 in 16 parts; 512 over 8000 222 and 106; 64 over 16000, 16 / 2, d = 256: 667 and
+// 62.  Parts cost a launch and their way through memory, about 5 us and 15 with all places
+// taken, and pay where the walk is shortened by more: 1024 new tokens 23 us whole, 36 in
+// two parts; 8 over 600 22 and 18. All parts have a place at once (two workgroups per CU,
+// one at d = 256; twice as many for the sake of uneven sequences: 2 x 256 over 7000, d =
+// 256, 111 -> 128) and four tiles or more.
 void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus) {
   const int64_t wgs = (p.T * (p.H / p.H_kv) + kBM - 1) / kBM * p.H_kv, places = (int64_t)cus * (p.d <= 128 ? 2 : 1);
   const int64_t fit = places / wgs, most = keys / (4 * 64);
   int64_t s = fit < most ? fit : most;
   if (s > kMaxSplits) s = kMaxSplits;
+  // Where every CU gets two workgroups (d <= 128) and there are few more, the second ones run
+  // from the shortest walk up, so that a long and a short one share a CU: 2 x 1024 tokens, 32 / 8
+  // heads, d = 128 34 -> 29 us, 4095, 16 / 4 83 -> 80.  With more of them it is better to go
+  // on from the longest (5000 tokens, 16 / 4: 110 us, 118 so).
+  const int64_t grid = (p.T * (p.H / p.H_kv) / kBM + p.N) * p.H_kv;
+  p.fold = p.d <= 128 && grid > cus && 4 * grid <= 9 * (int64_t)cus ? (cus + p.H_kv - 1) / p.H_kv : INT32_MAX;
   const double tiles = (double)keys / 64, step = p.d == 256 ? 2.5 : 1.25;
   p.splits = s > 1 && tiles * step * (double)(s - 1) / (double)s > 5 + 15.0 * (double)(s * wgs) / (double)places ? (int)s : 1;
 }

@@ -65,6 +65,7 @@ struct AttnExtendLaunch {
   float scale;
   float softcap;            // 0 = none
   int splits;               // parts of every row's keys
+  int fold;                 // slot of the launch from which the shortest walks come first
   float* part_o;            // [splits, T, H, d] unscaled outputs (splits > 1)
   float* part_ml;           // [splits, T, H, 2] running maximum and sum (splits > 1)
 };
@@ -107,7 +108,7 @@ struct EvictLaunch {
 };
 
 hipError_t launch_kv_store(const StoreLaunch& p, hipStream_t stream);
-void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus);   // splits
+void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus);   // splits, fold
 hipError_t launch_attn_extend(const AttnExtendLaunch& p, hipStream_t stream);
 void plan_attn_decode(AttnDecodeLaunch& p, int64_t max_rows, int cus);   // splits, min_chunks, ranked
 hipError_t launch_attn_decode(const AttnDecodeLaunch& p, hipStream_t stream);
