@@ -665,13 +665,27 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     auto unit_of = [&](int pl) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(punit, pl & 63); };   // (-1: not there)
     const uint32_t rlane = (uint32_t)(lane / kCp) * D + 16 * (lane % kCp);   // this lane's piece of a load
     const uint32_t raws = uni(lds_at(sT) + 2 * kTile + wave * 1024);   // codes: K and V, kTile / 2 bytes each, behind the first tiles
-    auto fetch = [&](const uint8_t* src, uint32_t to, int x, int s) __attribute__((always_inline)) {
-      const int r = x * kBN + (wave + 4 * s) * kCr, unit = max(unit_of(lane_of(r)), 0) + ((r & pmask) >> 4);
-      to_lds(buffer_of(src + (int64_t)unit * (16 * D) + (r & 15) * D, kCr * D), rlane, to + s * 4096);
+    auto fetch = [&](const uint8_t* src, uint32_t to, int unit, int s) __attribute__((always_inline)) {
+      to_lds(buffer_of(src + (int64_t)unit * (16 * D) + (wave * kCr & 15) * D, kCr * D), rlane, to + s * 4096);
+    };
+    auto units = [&](int x, int* u) __attribute__((always_inline)) {   // places of a tile's loads (whole pages: of one)
+      if (big) {
+        const int first = max(unit_of(lane_of(x * kBN)), 0) + ((x * kBN & pmask) >> 4);
+#pragma unroll
+        for (int s = 0; s < kCt; ++s) u[s] = first + ((wave + 4 * s) * kCr >> 4);
+      } else {
+#pragma unroll
+        for (int s = 0; s < kCt; ++s) {
+          const int r = x * kBN + (wave + 4 * s) * kCr;
+          u[s] = max(unit_of(lane_of(r)), 0) + ((r & pmask) >> 4);
+        }
+      }
     };
     auto fetch_all = [&](const uint8_t* src, uint32_t to, int x) __attribute__((always_inline)) {
+      int u[kCt];
+      units(x, u);
 #pragma unroll
-      for (int s = 0; s < kCt; ++s) fetch(src, to, x, s);
+      for (int s = 0; s < kCt; ++s) fetch(src, to, u[s], s);
     };
     auto lane_f = [&](float v, int pl) __attribute__((always_inline)) {
       return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), pl & 63));
@@ -791,8 +805,11 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         const unsigned long long bad = top(true);
         unsigned hid2 = 0;
         ahead(x);
+        int uv[kCt], uk[kCt];
+        units(x - 1, uv);
+        units(max(x - 2, x0), uk);
         const auto load = [&](int i) __attribute__((always_inline)) {
-          if (i < kCt) fetch(p.c.v, raws + kTile / 2, x - 1, i); else fetch(p.c.k, raws, max(x - 2, x0), i - kCt);
+          if (i < kCt) fetch(p.c.v, raws + kTile / 2, uv[i], i); else fetch(p.c.k, raws, uk[i - kCt], i - kCt);
         };
         step(s, s2, 0, 0, dist0(start + ti - (x - 1) * kBN), sl, Par<2 * kCt>{}, load,
              [&](f32x16 (&f)[kN2], float& mx) __attribute__((always_inline)) { hid2 = mask(f, x - 1, held(x - 1), mx); });
@@ -916,9 +933,10 @@ void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus) {
   // Where every CU gets two workgroups (d <= 128) and there are few more, the second ones run
   // from the shortest walk up, so that a long and a short one share a CU: 2 x 1024 tokens, 32 / 8
   // heads, d = 128 34 -> 29 us, 4095, 16 / 4 83 -> 80.  With more of them it is better to go
-  // on from the longest (5000 tokens, 16 / 4: 110 us, 118 so).
+  // on from the longest (5000 tokens, 16 / 4: 110 us, 118 so), and over a cache, where walks are
+  // alike, in the order of the batch (4 x 512 over 7000 rows, 32 / 8: 276 us, 390 so).
   const int64_t grid = (p.T * (p.H / p.H_kv) / kBM + p.N) * p.H_kv;
-  p.fold = p.d <= 128 && grid > cus && 4 * grid <= 9 * (int64_t)cus ? (cus + p.H_kv - 1) / p.H_kv : INT32_MAX;
+  p.fold = p.causal && !p.c.k && p.d <= 128 && grid > cus && 4 * grid <= 9 * (int64_t)cus ? (cus + p.H_kv - 1) / p.H_kv : INT32_MAX;
   const double tiles = (double)keys / 64, step = p.d == 256 ? 2.5 : 1.25;
   p.splits = s > 1 && tiles * step * (double)(s - 1) / (double)s > 5 + 15.0 * (double)(s * wgs) / (double)places ? (int)s : 1;
 }
