@@ -512,15 +512,18 @@ hipError_t launch_d(const AttnDecodeLaunch& p, int64_t max_rows, hipStream_t s) 
 }  // namespace
 
 // How a call is cut: splits per (sequence, kv head, 16 query heads), the fewest chunks that
-// one takes, and whether the longest sequences come first.  Two workgroups fit a CU.  A few
-// sequences are cut into one round of workgroups (2 x 131000 rows, d = 256: 59 us, in two
-// rounds 70); more of them may differ in length, and two rounds (32 sequences of 2000 to
-// 8192 rows: 92 us, in four 106) with the longest first even that out (256 of 512 to 4096:
-// 217 us in the order of the batch, 182; 256 of 2048 alike 196 and 208).
+// one takes, and whether the longest sequences come first.  Two workgroups fit a CU.  Up to
+// 16 sequences are cut into one round of workgroups (2 x 131000 rows, d = 256: 59 us, in two
+// rounds 70; 16 x 5000, 8 heads of 128 39 and 48; 16 of 500 to 10000 47 and 48); more of them
+// differ in length too much for one round, and two (32 of 100 to 8000 rows: 48 us, in one 66;
+// 32 of 2000 to 8192 with weights 92, in four 106) with the longest first even that out (256 of
+// 512 to 4096: 217 us in the order of the batch, 182; 256 of 2048 alike 196 and 208), at the
+// cost of batches of like lengths (32 x 5000 77 us, in one round 69).  Shares of the batch's
+// whole length, found on the device, were slower than the better of the two throughout.
 void plan_attn_decode(AttnDecodeLaunch& p, int64_t max_rows, int cus) {
   const int64_t base = (int64_t)p.N * p.c.H_kv * ((p.H / p.c.H_kv + 15) / 16), chunks = (max_rows + kChunk - 1) / kChunk;
   p.min_chunks = 2 * (p.c.d == 256 ? 2 : 4);    // two tiles per wave
-  const int64_t want = ((p.N >= 8 ? 4 : 2) * (int64_t)cus + base - 1) / base;
+  const int64_t want = ((p.N > 16 ? 4 : 2) * (int64_t)cus + base - 1) / base;
   const int64_t most = (chunks + p.min_chunks - 1) / p.min_chunks;
   const int64_t s = want < most ? want : most;
   p.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
