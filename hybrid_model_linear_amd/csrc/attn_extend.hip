@@ -23,7 +23,7 @@
 // vector units turn this tile's into weights; then, under the second product, they cap and
 // bias the next tile's scores and look for their maximum.  (One after the other, both kept
 // the SIMDs busy 44% of the time each with hardly any overlap, even with two workgroups on
-// a CU: 944 TFLOP/s at 8 x 4096 tokens, 32 / 8 heads, d = 128; now 1030 - 1060, where a
+// a CU: 944 TFLOP/s at 8 x 4096 tokens, 32 / 8 heads, d = 128; now 1020 - 1060, where a
 // library product of two matrices of 16384^2 normal values reaches 1390.)  Up to d = 128
 // two workgroups fit a CU; at d = 256 one does (its output alone takes 128 registers).
 // Keys are taken from the last to the first, the new tokens before the cached: with a
