@@ -437,8 +437,10 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   int d0 = first / kBN, d1 = (last + kBN - 1) / kBN;    // tiles [d0, d1), from the last
   // Cached tiles x, x - 1, ... x0, without those that a window leaves out for every row
   int x0 = 0, x = CACHED ? (P + kBN - 1) / kBN - 1 : -1;
-  if (CACHED && p.window > 0 && !p.c.pos)
+  if (CACHED && p.window > 0 && !p.c.pos) {             // (with `start` below P, rows ahead of the tokens too)
+    x = (int)min((int64_t)x, max((int64_t)start + tz + p.window - 1, (int64_t)0) / kBN);
     x0 = (int)min((int64_t)(x + 1), max((int64_t)0, (int64_t)start + ta - p.window + 1) / kBN);
+  }
   if (p.splits > 1) {                                   // this workgroup's part of both
     const int nd = max(d1 - d0, 0), nt = nd + x + 1 - x0;
     const int a = (int)((int64_t)nt * blockIdx.y / p.splits), b = (int)((int64_t)nt * (blockIdx.y + 1) / p.splits);
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
           }
         }
         mx = tile_max(s);
-      } else if (p.window > 0 && start + wz - j0 >= p.window) {
+      } else if (p.window > 0 && (start + wz - j0 >= p.window || j0 + kBN - 1 - (start + wa) >= p.window)) {
         const int qrel = start + ti - j0;
         hidden |= ~seen_bits(qrel - p.window + 1, qrel + p.window);
       }
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         if (more) convert(raws, 0, pks, x - 1);
         unsigned long long bad = 0;
         // (rows that are not held are zeros; only a window hides a held row from some rows)
-        if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window))
+        if (p.window > 0 && (p.c.pos || start + tz - x * kBN >= p.window || x * kBN + kBN - 1 - (start + ta) >= p.window))
           bad = scrub(-2 - x, [&](int i, int ln) { return lds_at(sT) + kTile + ((wave + 4 * (i >> 1)) * kCr + ln / kCp) * 2 * D +
                                                   (((2 * (ln % kCp) + (i & 1)) ^ row_swz<D>((wave + 4 * (i >> 1)) * kCr + ln / kCp)) << 4); },
                       Par<2 * kCt>{});

@@ -1,0 +1,74 @@
+"""GPU tests of the softmax-attention operators at their edges against the fp64 definitions:
+queries that stand before cached rows, pages that no row of the call is on, sums that are not
+numbers, scales that are tiny or not positive, and every way of shaping scores at every head
+size."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as oa
+from attn_util import (assert_out, bf16, cache_norm, host_cache, i32, make_cache, make_table, row_norm, score_error,
+                       spread_positions, up, upload_cache)
+from test_gpu_attn_split import _unsplit
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def _cu(lens):
+    return np.concatenate([[0], np.cumsum(lens)])
+
+
+def _qkv(rng, T, H, H_kv, d):
+    return [bf16(rng.normal(size=(T, h, d))) for h in (H, H_kv, H_kv)]
+
+
+def _slopes(H):
+    return (2.0 ** -np.arange(1, H + 1)).astype(np.float32)
+
+
+def _same_kind(got, ref):
+    """NaN where the definition has NaN and nowhere else."""
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+
+
+# ------------------------------------------------------------------ queries before cached rows
+@pytest.mark.parametrize("d,page,opt", [(64, 16, {}), (128, 64, dict(slopes=True)), (128, 32, dict(softcap=9.0)),
+                                        (256, 128, dict(slopes=True, softcap=20.0))])
+@pytest.mark.parametrize("split", [False, True])
+def test_window_hides_cached_rows_ahead_of_the_query(gdn_lib, d, page, opt, split):
+    """start below cache_len: cached rows further ahead than the window are hidden, those
+    that only some of the tokens see among them, and their NaNs stay away."""
+    print(f"[case] extend, start below cache_len, d={d} page={page} {opt} split={split}", flush=True)
+    rng = np.random.default_rng(d + page)
+    lens, H, H_kv = [70, 5, 33, 2], 4, 2
+    if split:
+        lens, old, start, w = [7, 3], [2500, 1700], [100, 1200], 900
+    else:
+        old, start, w = [400, 131, 300, 90], [0, 60, 290, 500], 45
+    c = make_cache(rng, sum(-(-o // page) for o in old), H_kv, page, d)
+    table = make_table(rng, old, page, c["k"].shape[0])
+    knorm = cache_norm(c)
+    for n, (o, s, L) in enumerate(zip(old, start, lens)):
+        for r in range(o):
+            if r - (s + L - 1) >= w and r % 7 == 0:    # hidden from all of the sequence's tokens
+                c["kv"[r % 2]][table[n, r // page], :, r % page, r % d] = 0x7f
+    edge = start[0] + w + 1                             # seen by tokens 2 and later only
+    c["v"][table[0, edge // page], 0, edge % page, 3] = 0xff
+    q, k, v = _qkv(rng, sum(lens), H, H_kv, d)
+    kw = dict(window=w, softcap=opt.get("softcap", 0.0))
+    slopes = _slopes(H) if opt.get("slopes") else None
+    with np.errstate(invalid="ignore"):
+        ref, mag = oa.attn_extend(q, k, v, _cu(lens), 0.1, cache=c, table=table, cache_len=old, start=start, slopes=slopes, **kw)
+    assert np.isnan(ref).sum() == 2 * (lens[0] - 2)     # two heads of the group, one column
+    args = [up(x, BF16) for x in (q, k, v)] + [i32(_cu(lens))]
+    kw.update(scale=0.1, cache=upload_cache(gdn_lib, c), block_table=i32(table), cache_len=i32(old), start=i32(start),
+              slopes=up(slopes))
+    if split:
+        assert gdn_lib.attn_extend_workspace_size(*args, **kw) > 0
+    got = gdn_lib.attn_extend(*args, **kw).float().cpu().numpy()
+    _same_kind(got, ref)
+    ds = score_error(q, max(row_norm(k), knorm), 0.1, opt.get("softcap", 0.0), 0.5 if opt.get("slopes") else 0.0, max(old))
+    assert_out(got, ref, np.nan_to_num(mag), ds, "extend")
