@@ -660,8 +660,9 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       const int j = first + lane, id = j < ((P + pmask) >> lg) ? page_of(p.c, n, j << lg) : -1;
       const int64_t at = (int64_t)max(id, 0) * p.H_kv + h;
       punit = id < 0 ? -1 : (int)(at << (lg - 4));
-      pks = p.c.k_scale[at];
-      pvs = p.c.v_scale[at];
+      // (rows that are not there are zeros, which another page's scale could turn into NaN)
+      pks = id < 0 ? 1.f : p.c.k_scale[at];
+      pvs = id < 0 ? 1.f : p.c.v_scale[at];
     };
     auto lane_of = [&](int row) __attribute__((always_inline)) { return (row >> lg) - pb; };
     auto unit_of = [&](int pl) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(punit, pl & 63); };   // (-1: not there)

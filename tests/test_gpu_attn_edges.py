@@ -72,3 +72,55 @@ def test_window_hides_cached_rows_ahead_of_the_query(gdn_lib, d, page, opt, spli
     _same_kind(got, ref)
     ds = score_error(q, max(row_norm(k), knorm), 0.1, opt.get("softcap", 0.0), 0.5 if opt.get("slopes") else 0.0, max(old))
     assert_out(got, ref, np.nan_to_num(mag), ds, "extend")
+
+
+# ------------------------------------------------------------------ pages that hold nothing of the call
+def _poison_unowned(c, table, value):
+    """Codes and scales of the pages that no sequence owns, as in memory that was never written."""
+    free = np.setdiff1d(np.arange(c["k"].shape[0]), table[table >= 0])
+    for a in ("k", "v"):
+        c[a][free], c[a + "_scale"][free] = 0x7f, value
+    assert 0 in free
+
+
+def _table_without_page_0(rng, counts, page, pages):
+    t = make_table(rng, counts, page, pages - 1)
+    return np.where(t >= 0, t + 1, t)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, 2.0 ** 127])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 32), (256, 32), (64, 64), (128, 128)])
+def test_extend_scales_of_other_pages_do_not_leak(gdn_lib, d, page, value):
+    print(f"[case] extend, foreign scales {value}, d={d} page={page}", flush=True)
+    rng = np.random.default_rng(d + page)
+    lens, old, H, H_kv = [5, 70, 3], [70, 200, 17], 4, 2
+    c = make_cache(rng, 60, H_kv, page, d)
+    table = _table_without_page_0(rng, old, page, 60)
+    table[1, 1] = -1                                    # a page that is not there
+    knorm = cache_norm(c)
+    _poison_unowned(c, table, value)
+    q, k, v = _qkv(rng, sum(lens), H, H_kv, d)
+    for w in (0, 50):
+        ref, mag = oa.attn_extend(q, k, v, _cu(lens), 0.1, cache=c, table=table, cache_len=old, window=w)
+        got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32(_cu(lens)), scale=0.1, cache=upload_cache(gdn_lib, c),
+                                  block_table=i32(table), cache_len=i32(old), window=w).float().cpu().numpy()
+        assert_out(got, ref, mag, score_error(q, max(row_norm(k), knorm), 0.1), f"window {w}")
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, 2.0 ** 127])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (256, 16), (128, 128)])
+def test_decode_scales_of_other_pages_do_not_leak(gdn_lib, d, page, value):
+    print(f"[case] decode, foreign scales {value}, d={d} page={page}", flush=True)
+    rng = np.random.default_rng(d + page)
+    lens, H, H_kv = [70, 200, 17, 1], 4, 2
+    c = make_cache(rng, 60, H_kv, page, d)
+    table = _table_without_page_0(rng, lens, page, 60)
+    table[1, 1] = 0 if page == 128 else -1
+    if page == 128:
+        table[1, 1] = 99
+    knorm = cache_norm(c)
+    _poison_unowned(c, table, value)
+    q = bf16(rng.normal(size=(len(lens), H, d)))
+    ref, mag, _ = oa.attn_decode(q, c, table, lens, 0.1)
+    got = gdn_lib.attn_decode(up(q, BF16), upload_cache(gdn_lib, c), i32(table), i32(lens), scale=0.1).float().cpu().numpy()
+    assert_out(got, ref, mag, score_error(q, knorm, 0.1), "decode")
