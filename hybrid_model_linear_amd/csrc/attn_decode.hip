@@ -243,7 +243,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
     if (partial) {
 #pragma unroll
       for (int i = 0; i < kG; ++i) hidden |= (bad || r0 + i < rg.lo || r0 + i >= rg.hi ? 1u : 0u) << i;
-      if (r0 >= rg.hi) vs = 1.f;                // (a page behind the last row may hold any scale)
     }
     if (by_pos) {
 #pragma unroll
@@ -261,6 +260,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) decode_kernel(const AttnDecode
       for (int i = 0; i < kG; ++i) s[i >> 2][i & 3] -= slope * (float)abs(qpos - (r0 + i));
     }
     if (__any(hidden != 0)) {
+      // (the lane's rows lie on one page; behind the last row or outside of the window it may hold any scale)
+      if (hidden == (1u << kG) - 1) vs = 1.f;
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
         const bool off = hidden >> i & 1;

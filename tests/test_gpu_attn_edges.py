@@ -124,3 +124,39 @@ def test_decode_scales_of_other_pages_do_not_leak(gdn_lib, d, page, value):
     ref, mag, _ = oa.attn_decode(q, c, table, lens, 0.1)
     got = gdn_lib.attn_decode(up(q, BF16), upload_cache(gdn_lib, c), i32(table), i32(lens), scale=0.1).float().cpu().numpy()
     assert_out(got, ref, mag, score_error(q, knorm, 0.1), "decode")
+
+
+@pytest.mark.parametrize("pos", [False, True])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (256, 16)])
+def test_pages_outside_of_the_window_may_hold_any_scale(gdn_lib, d, page, pos):
+    """Pages none of whose rows is seen: their codes and scales reach nothing."""
+    print(f"[case] hidden pages, d={d} page={page} pos={pos}", flush=True)
+    rng = np.random.default_rng(d + page)
+    lens, H, H_kv, w = [300, 100, 290], 4, 2, 75
+    c = make_cache(rng, 80, H_kv, page, d, track=pos)
+    table = make_table(rng, lens, page, 80)
+    if pos:
+        last = spread_positions(rng, c, table, lens)
+        q_pos, start = last, [x + 1 for x in last]
+    else:
+        q_pos, start = None, None
+    knorm = cache_norm(c)
+    for n, L in enumerate(lens):
+        for j in range(-(-L // page)):
+            rows = np.arange(j * page, min(L, (j + 1) * page))
+            at = c["pos"][table[n, j]].max() if pos else rows.max()
+            if (q_pos[n] if pos else L - 1) - at >= w:  # for every head
+                c["v"][table[n, j], :, 5:9] = 0x7f
+                c["k_scale"][table[n, j]] = c["v_scale"][table[n, j]] = math.nan
+    q = bf16(rng.normal(size=(len(lens), H, d)))
+    g = upload_cache(gdn_lib, c)
+    assert np.isnan(c["v_scale"]).any()
+    ref, mag, _ = oa.attn_decode(q, c, table, lens, 0.1, window=w, q_pos=q_pos)
+    ds = score_error(q, knorm, 0.1)
+    got = gdn_lib.attn_decode(up(q, BF16), g, i32(table), i32(lens), scale=0.1, window=w, q_pos=i32(q_pos)).float().cpu().numpy()
+    assert_out(got, ref, mag, ds, "decode")
+    q, k, v = _qkv(rng, 9, H, H_kv, d)
+    ref, mag = oa.attn_extend(q, k, v, [0, 3, 7, 9], 0.1, cache=c, table=table, cache_len=lens, start=start, window=w)
+    got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32([0, 3, 7, 9]), scale=0.1, cache=g, block_table=i32(table),
+                              cache_len=i32(lens), start=i32(start), window=w).float().cpu().numpy()
+    assert_out(got, ref, mag, score_error(q, max(row_norm(k), knorm), 0.1), "extend")
