@@ -492,6 +492,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const AttnDeco
     }
   }
   if (id < 0) return;
+  if (p.window > 0 && p.c.pos) {                // hidden rows stay as they are, also where a head's sum is NaN
+    const int4 kp = *reinterpret_cast<const int4*>(p.c.pos + (at - p.c.weight));
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (abs(qpos - (e == 0 ? kp.x : e == 1 ? kp.y : e == 2 ? kp.z : kp.w)) >= p.window) w[e] = 0.f;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (r + e >= rg.lo && r + e < rg.hi) at[e] = old[e] + w[e];

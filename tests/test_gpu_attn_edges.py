@@ -160,3 +160,29 @@ def test_pages_outside_of_the_window_may_hold_any_scale(gdn_lib, d, page, pos):
     got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32([0, 3, 7, 9]), scale=0.1, cache=g, block_table=i32(table),
                               cache_len=i32(lens), start=i32(start), window=w).float().cpu().numpy()
     assert_out(got, ref, mag, score_error(q, max(row_norm(k), knorm), 0.1), "extend")
+
+
+# ------------------------------------------------------------------ sums that are not numbers
+@pytest.mark.parametrize("long", [False, True])
+def test_a_nan_sum_leaves_the_weights_of_hidden_rows(gdn_lib, long):
+    """A NaN key that one head sees: the weights of the rows that its window hides stay."""
+    print(f"[case] decode accumulating, NaN sum, long={long}", flush=True)
+    rng = np.random.default_rng(31)
+    lens, H, H_kv, d, page, w = [1700 if long else 300, 90], 4, 2, 64, 16, 60
+    c = make_cache(rng, 120, H_kv, page, d, track=True)
+    table = make_table(rng, lens, page, 120)
+    q_pos = spread_positions(rng, c, table, lens)
+    seen = [i for i in range(lens[0]) if abs(q_pos[0] - c["pos"][table[0, i // page], 0, i % page]) < w]
+    assert 3 < len(seen) < lens[0]
+    c["k"][table[0, seen[2] // page], 0, seen[2] % page, 1] = 0x7f
+    q = bf16(rng.normal(size=(2, H, d)))
+    with np.errstate(invalid="ignore"):
+        ref, _, want = oa.attn_decode(q, c, table, lens, 0.1, window=w, q_pos=q_pos)
+    assert np.isnan(want).sum() == len(seen)
+    g = upload_cache(gdn_lib, c)
+    out = gdn_lib.attn_decode(up(q, BF16), g, i32(table), i32(lens), scale=0.1, window=w, q_pos=i32(q_pos), accumulate=True)
+    _same_kind(out.float().cpu().numpy(), ref)
+    got = host_cache(g)["weight"]
+    _same_kind(got, want)
+    same = want == c["weight"]                          # rows that are not seen, or of no sequence
+    assert same.any() and np.array_equal(got[same], c["weight"][same])
