@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   const float c2 = p.softcap * kLog2e;
   const float cs = SHAPE == kRaw ? c1 : 1.f;
   const float slope = kHasBias && p.slopes ? p.slopes[hq] * kLog2e : 0.f;
-  const float slack = 8.f / cs;            // the maximum in use may lag the true one by 2^8
+  const float slack = fminf(8.f / cs, 3e38f);   // the maximum in use may lag the true one by 2^8 (finite: the first raises it)
 
   // operand addresses in the first K and V tile (kTile bytes each: K, V, K, V)
   uint32_t ka[kKa], va[2][kVa];

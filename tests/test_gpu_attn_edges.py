@@ -186,3 +186,21 @@ def test_a_nan_sum_leaves_the_weights_of_hidden_rows(gdn_lib, long):
     _same_kind(got, want)
     same = want == c["weight"]                          # rows that are not seen, or of no sequence
     assert same.any() and np.array_equal(got[same], c["weight"][same])
+
+
+# ------------------------------------------------------------------ scales
+@pytest.mark.parametrize("scale", [1e-39, 2e-38, 0.0, -0.1])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_that_are_tiny_or_not_positive(gdn_lib, scale, d):
+    print(f"[case] extend scale={scale} d={d}", flush=True)
+    rng = np.random.default_rng(d)
+    T, H = 1100, 2
+    q, k, v = _qkv(rng, T, H, 1, d)
+    ref, mag = oa.attn_extend(q, k, v, [0, T], scale)
+    args = [up(x, BF16) for x in (q, k, v)] + [i32([0, T])]
+    assert gdn_lib.attn_extend_workspace_size(*args, scale=scale) > 0
+    ds = score_error(q, row_norm(k), abs(scale))
+    assert_out(gdn_lib.attn_extend(*args, scale=scale).float().cpu().numpy(), ref, mag, ds, "split")
+    out = torch.empty_like(args[0])
+    _unsplit(gdn_lib, *args, scale=scale, out=out)
+    assert_out(out.float().cpu().numpy(), ref, mag, ds, "whole")
