@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   constexpr bool kHasBias = SHAPE & kBias, kHasCap = SHAPE & kCap;
   const float c1 = kHasCap ? p.scale / p.softcap * 2.0f * kLog2e : p.scale * kLog2e;
   const float c2 = p.softcap * kLog2e;
-  const float cs = SHAPE == kRaw ? c1 : 1.f;
+  float cs = SHAPE == kRaw ? c1 : 1.f;     // (kRaw: of this lane's row, raise() may change it)
   const float slope = kHasBias && p.slopes ? p.slopes[hq] * kLog2e : 0.f;
   const float slack = fminf(8.f / cs, 3e38f);   // the maximum in use may lag the true one by 2^8 (finite: the first raises it)
 
@@ -245,8 +245,12 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     mx = half_max(mx);
     if (__any(mx > m + slack)) {
       mx = fmaxf(m, mx);
-      const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : (m - mx) * cs);
+      const float fct = __builtin_amdgcn_exp2f(m == mx ? 0.f : (m - mx) * (SHAPE == kRaw ? c1 : 1.f));
       m = mx;
+      // From 2^31 on m cs is off by 2^6 and more through its rounding, and weights would overflow
+      // or vanish.  By a power of two it is exact, and as the next lower score is 2^6 away at
+      // least, only the largest has a weight either way.
+      if (SHAPE == kRaw) cs = fabsf(m * c1) >= 0x1p31f ? __uint_as_float(__float_as_uint(c1) & 0x7f800000u) : c1;
       base = m == -INFINITY ? 0.f : m * cs;
       l *= fct;
 #pragma unroll
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
   if (p.splits > 1) {                                   // sums and outputs as they are, for extend_join_kernel
     const int64_t row = ((int64_t)blockIdx.y * p.T + t0 + ti) * p.H + hq;
     const bool none = doc && di < 0;
-    if (hh == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * row) = none ? make_float2(-INFINITY, 0.f) : make_float2(m == -INFINITY ? m : base, l);
+    if (hh == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * row) = none ? make_float2(-INFINITY, 0.f) : make_float2(SHAPE == kRaw ? m * c1 : m, l);
     float* at = p.part_o + row * D;
 #pragma unroll
     for (int d = 0; d < kDT; ++d)

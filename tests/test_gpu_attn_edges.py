@@ -204,3 +204,48 @@ def test_scales_that_are_tiny_or_not_positive(gdn_lib, scale, d):
     out = torch.empty_like(args[0])
     _unsplit(gdn_lib, *args, scale=scale, out=out)
     assert_out(out.float().cpu().numpy(), ref, mag, ds, "whole")
+
+
+@pytest.mark.parametrize("size", [3e3, 3e4, 1e5])
+@pytest.mark.parametrize("cached", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scores_of_any_size(gdn_lib, d, cached, size):
+    """Queries and keys whose scores reach 1e8, 1e10 and 1e12: the key of the largest score is the output,
+    wherever no other comes near it."""
+    print(f"[case] extend, large scores, d={d} cached={cached} size={size}", flush=True)
+    rng = np.random.default_rng(d)
+    lens, H, page = ([40, 9], 2, 32) if cached else ([1200], 2, 32)
+    q, k, v = _qkv(rng, sum(lens), H, 1, d)
+    q, k = bf16(q * size), bf16(k * size)
+    args, kw = [up(x, BF16) for x in (q, k, v)] + [i32(_cu(lens))], dict(scale=0.5)
+    keys, values = [], []
+    old = [900, 70] if cached else [0]
+    if cached:
+        c = make_cache(rng, 40, 1, page, d)
+        c["k_scale"] *= 2.0 ** round(math.log2(size))
+        table = make_table(rng, old, page, 40)
+        kw.update(cache=upload_cache(gdn_lib, c), block_table=i32(table), cache_len=i32(old))
+    for n, (a, b) in enumerate(zip(_cu(lens), _cu(lens)[1:])):
+        ck, cv = oa.cached_rows(c, table[n], old[n], 0)[:2] if cached else (np.zeros((0, d)), np.zeros((0, d)))
+        keys.append(np.concatenate([ck, k[a:b, 0]]))
+        values.append(np.concatenate([cv, v[a:b, 0]]))
+    assert gdn_lib.attn_extend_workspace_size(*args, **kw) > 0
+    whole = torch.empty_like(args[0])
+    _unsplit(gdn_lib, *args, out=whole, **kw)
+    got = [x.float().cpu().numpy() for x in (whole, gdn_lib.attn_extend(*args, **kw))]
+    want, seen = [], []
+    for n, a in enumerate(_cu(lens)[:-1]):
+        for i in range(lens[n]):
+            for h in range(H):
+                s = 0.5 * (keys[n][:old[n] + i + 1] @ q[a + i, h].astype(np.float64))
+                order = np.argsort(-s)
+                # (an fp32 score is off by (d + 4) 2^-24 |q| |k| at most)
+                off = 0.5 * (d + 4) * 2.0 ** -24 * np.linalg.norm(q[a + i, h].astype(np.float64)) * np.linalg.norm(keys[n], axis=1).max()
+                if len(s) > 1 and s[order[0]] - s[order[1]] < 2 * off + 1000:
+                    continue
+                want.append(values[n][order[0]])
+                seen.append([x[a + i, h] for x in got])
+    assert len(want) > 0.8 * sum(lens) * H
+    want = np.stack(want)
+    for j, name in enumerate(("whole", "split")):        # (one weight, rounded to bf16, and the output's rounding)
+        assert_out(np.stack([x[j] for x in seen]), want, np.abs(want), 0.0, name)
