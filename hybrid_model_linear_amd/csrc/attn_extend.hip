@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         spill(bad, hidden, [&](int r, int col) {
           const int row = min(x * kBN + r, P - 1), pg = max(page_of(p.c, n, row), 0);
           const uint32_t w4 = *reinterpret_cast<const uint32_t*>(p.c.v + (page_rows(p.c, pg, h) + (row & pmask)) * D + col);
-          return f8x4_to_bf16(w4, 1.f);
+          return f8x4_to_bf16(w4, p.c.v_scale[(int64_t)pg * p.H_kv + h]);   // (code * scale may pass the largest float)
         });
       };
       auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2]) __attribute__((always_inline)) {

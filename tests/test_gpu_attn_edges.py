@@ -249,3 +249,32 @@ def test_scores_of_any_size(gdn_lib, d, cached, size):
     want = np.stack(want)
     for j, name in enumerate(("whole", "split")):        # (one weight, rounded to bf16, and the output's rounding)
         assert_out(np.stack([x[j] for x in seen]), want, np.abs(want), 0.0, name)
+
+
+# ------------------------------------------------------------------ the largest cached values
+@pytest.mark.parametrize("pos", [False, True])
+def test_a_cached_value_past_the_largest_float_reaches_who_sees_it(gdn_lib, pos):
+    """Values near bf16's largest may round to 2^128 in the cache: infinite for the rows that
+    see them, whether or not a window hides them from others."""
+    print(f"[case] extend, cached 2^128, pos={pos}", flush=True)
+    rng = np.random.default_rng(41)
+    lens, old, H, d, page, w = [60], [100], 2, 64, 16, 80
+    c = make_cache(rng, 8, 1, page, d, track=pos)
+    if pos:
+        c["pos"][:] = 0
+    table = make_table(rng, old, page, 8)
+    if pos:
+        for r in range(100):
+            c["pos"][table[0, r // page], 0, r % page] = r
+    at, row = table[0, 50 // page], 50 % page
+    c["v"][at], c["v_scale"][at] = 0, 2.0 ** 120
+    c["v"][at, 0, row, 9] = 0x78                        # 256
+    q, k, v = _qkv(rng, lens[0], H, 1, d)
+    ref, mag = oa.attn_extend(q, k, v, [0, 60], 0.1, cache=c, table=table, cache_len=old, window=w)
+    got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32([0, 60]), scale=0.1, cache=upload_cache(gdn_lib, c),
+                              block_table=i32(table), cache_len=i32(old), window=w).float().cpu().numpy()
+    sees = np.abs(100 + np.arange(60) - 50) < w
+    assert sees.any() and not sees.all()
+    assert (got[sees, :, 9] == math.inf).all()
+    got[sees, :, 9] = ref[sees, :, 9] = mag[sees, :, 9] = 0.0
+    assert_out(got, ref, mag, score_error(q, max(row_norm(k), cache_norm(c)), 0.1), "beside it")
