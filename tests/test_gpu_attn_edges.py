@@ -278,3 +278,30 @@ def test_a_cached_value_past_the_largest_float_reaches_who_sees_it(gdn_lib, pos)
     assert (got[sees, :, 9] == math.inf).all()
     got[sees, :, 9] = ref[sees, :, 9] = mag[sees, :, 9] = 0.0
     assert_out(got, ref, mag, score_error(q, max(row_norm(k), cache_norm(c)), 0.1), "beside it")
+
+
+# ------------------------------------------------------------------ every way of shaping scores
+SHAPES = {"raw": {}, "negative scale": dict(scale=-0.1), "bias": dict(slopes=True), "cap": dict(softcap=4.0),
+          "cap, negative scale": dict(softcap=4.0, scale=-0.1), "cap and bias": dict(softcap=4.0, slopes=True)}
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("cached", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_extend_shapes_of_scores(gdn_lib, d, cached, shape):
+    print(f"[case] extend d={d} cached={cached} {shape}", flush=True)
+    rng = np.random.default_rng(d)
+    opt, lens, old, H, H_kv, page = SHAPES[shape], [197, 40, 1], [150, 0, 77], 6, 2, 32
+    q, k, v = _qkv(rng, sum(lens), H, H_kv, d)
+    scale, softcap, slopes = opt.get("scale", 0.1), opt.get("softcap", 0.0), _slopes(H) if opt.get("slopes") else None
+    kw, gkw, knorm = {}, {}, row_norm(k)
+    if cached:
+        c = make_cache(rng, 12, H_kv, page, d)
+        table = make_table(rng, old, page, 12)
+        knorm = max(knorm, cache_norm(c))
+        kw, gkw = dict(cache=c, table=table, cache_len=old), dict(cache=upload_cache(gdn_lib, c), block_table=i32(table),
+                                                                  cache_len=i32(old))
+    ref, mag = oa.attn_extend(q, k, v, _cu(lens), scale, softcap=softcap, slopes=slopes, **kw)
+    got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32(_cu(lens)), scale=scale, softcap=softcap, slopes=up(slopes),
+                              **gkw).float().cpu().numpy()
+    assert_out(got, ref, mag, score_error(q, knorm, abs(scale), softcap, 0.5 if opt.get("slopes") else 0.0, 400), shape)
