@@ -928,24 +928,32 @@ hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
 // for a few long walks: 16 tokens over 8000 cached rows, 32 / 8 heads, d = 128: 196 us
 // whole, 25 in 16 parts; 512 over 8000 222 and 106; 64 over 16000, 16 / 2, d = 256: 667 and
 // 62.  Parts cost a launch and their way through memory, about 5 us and 15 with all places
-// taken, and pay where the walk is shortened by more: 1024 new tokens 23 us whole, 36 in
-// two parts; 8 over 600 22 and 18. All parts have a place at once (two workgroups per CU,
-// one at d = 256; twice as many for the sake of uneven sequences: 2 x 256 over 7000, d =
-// 256, 111 -> 128) and four tiles or more.
+// taken by full tiles, and pay where the walk is shortened by more: 1024 new tokens 23 us
+// whole, 36 in two parts; 8 over 600 22 and 18.  All parts have a place at once (two
+// workgroups per CU, one at d = 256; twice as many for the sake of uneven sequences: 2 x 256
+// over 7000, d = 256, 111 -> 128) and four tiles or more.  Tiles do not cross sequences: with
+// many short ones the launch's workgroups are counted, one per sequence at least and up to one
+// more that finds no rows, so that an eighth over is no second round (4 tokens each over 7000
+// rows: 16 sequences, 32 / 8, d = 128: 4 parts 70 us, 16 80; 32 of 16 / 2, d = 256: 3 113, 16
+// 133).  Where fewer than three have a place then, up to four even out the rounds (48
+// sequences, 32 / 8, d = 128: 243 us whole, 215, 16 245; 64 304 in d = 256, 16 / 2, 249, 246; but
+// 64 of 32 / 8, d = 128: 275, 285, 327).
 void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus) {
-  const int64_t wgs = (p.T * (p.H / p.H_kv) + kBM - 1) / kBM * p.H_kv, places = (int64_t)cus * (p.d <= 128 ? 2 : 1);
-  const int64_t fit = places / wgs, most = keys / (4 * 64);
-  int64_t s = fit < most ? fit : most;
+  const int64_t group = p.H / p.H_kv, places = (int64_t)cus * (p.d <= 128 ? 2 : 1);
+  const int64_t wgs = (p.T * group + kBM - 1) / kBM * p.H_kv, grid = (p.T * group / kBM + p.N) * p.H_kv;
+  const int64_t fit = 9 * places / (8 * grid), most = keys / (4 * 64);
+  int64_t s = places / wgs;
+  if (s > (fit >= 3 ? fit : 4)) s = fit >= 3 ? fit : 4;
+  if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;
+  const double tiles = (double)keys / 64, step = p.d == 256 ? 2.5 : 1.25;
+  p.splits = s > 1 && tiles * step * (double)(s - 1) / (double)s > 5 + 15.0 * (double)(s * wgs) / (double)places ? (int)s : 1;
   // Where every CU gets two workgroups (d <= 128) and there are few more, the second ones run
   // from the shortest walk up, so that a long and a short one share a CU: 2 x 1024 tokens, 32 / 8
   // heads, d = 128 34 -> 29 us, 4095, 16 / 4 83 -> 80.  With more of them it is better to go
   // on from the longest (5000 tokens, 16 / 4: 110 us, 118 so), and over a cache, where walks are
   // alike, in the order of the batch (4 x 512 over 7000 rows, 32 / 8: 276 us, 390 so).
-  const int64_t grid = (p.T * (p.H / p.H_kv) / kBM + p.N) * p.H_kv;
   p.fold = p.causal && !p.c.k && p.d <= 128 && grid > cus && 4 * grid <= 9 * (int64_t)cus ? (cus + p.H_kv - 1) / p.H_kv : INT32_MAX;
-  const double tiles = (double)keys / 64, step = p.d == 256 ? 2.5 : 1.25;
-  p.splits = s > 1 && tiles * step * (double)(s - 1) / (double)s > 5 + 15.0 * (double)(s * wgs) / (double)places ? (int)s : 1;
 }
 
 hipError_t launch_attn_extend(const AttnExtendLaunch& p, hipStream_t s) {

@@ -1,0 +1,45 @@
+"""Host-side tests of how attn_extend and attn_decode cut a call and of what they refuse for its
+size (no GPU: workspace queries and calls that fail validation launch nothing)."""
+import ctypes as ct
+
+import pytest
+
+import hybrid_model_linear_amd as gdn
+from hybrid_model_linear_amd import _lib
+from test_attn_host import P, _cache, _extend
+
+CUS = 256            # what the library assumes without a device
+KEYS = 7000
+
+
+def _parts(n, tokens, H, H_kv, d, keys=KEYS, page=64, **kw):
+    """Parts into which the keys of n sequences of so many tokens over `keys` cached rows are cut."""
+    width, T = -(-keys // page), n * tokens
+    a = _extend(_cache(H_kv=H_kv, d=d, page=page, pos=None, num_pages=1 << 20), N=n, T=T, H=H, H_kv=H_kv, d=d, q=P, q_stride=H * d,
+                k=P, k_stride=H_kv * d, v=P, v_stride=H_kv * d, out=1 << 50, out_stride=H * d, table_width=width,
+                table_stride=width, **kw)
+    need = gdn.load().gdn_attn_extend_workspace_size(ct.byref(a))
+    assert need >= 0
+    return max(need // (T * H * (d + 2) * 4), 1)
+
+
+@pytest.mark.parametrize("n,tokens,H,H_kv,d", [(1, 16, 32, 8, 128), (8, 4, 32, 8, 128), (16, 4, 32, 8, 128), (16, 1, 32, 8, 128),
+                                               (32, 4, 32, 8, 128), (8, 4, 16, 2, 256), (32, 4, 16, 2, 256), (64, 4, 16, 2, 128),
+                                               (5, 30, 16, 4, 128), (6, 256, 32, 8, 64)])
+def test_parts_have_a_place_at_once(n, tokens, H, H_kv, d):
+    """Row tiles do not cross sequences: there is one per sequence and kv head at least."""
+    tiles = n * -(-tokens * (H // H_kv) // 128) * H_kv
+    places = CUS * (2 if d <= 128 else 1)
+    parts = _parts(n, tokens, H, H_kv, d)
+    assert parts * tiles <= places * 9 // 8 or parts <= 4
+    assert parts > 1 or 2 * tiles > places // 2
+
+
+@pytest.mark.parametrize("n,tokens,H,H_kv,d,keys", [(64, 4, 32, 8, 128, 7000), (128, 4, 32, 8, 128, 4000), (48, 4, 32, 8, 128, 7000),
+                                                    (64, 4, 16, 2, 256, 7000), (24, 4, 32, 8, 256, 7000)])
+def test_batches_that_fill_the_chip_are_cut_in_four_at_most(n, tokens, H, H_kv, d, keys):
+    assert _parts(n, tokens, H, H_kv, d, keys) <= 4
+
+
+def test_chunks_that_fill_the_chip_are_not_cut():
+    assert _parts(4, 512, 16, 2, 256) == _parts(4, 512, 32, 8, 128) == 1
