@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
     __syncthreads();
     return (unsigned long long)uni(sBad[1]) << 32 | uni(sBad[0]);
   };
-  auto spill = [&](unsigned long long bad, unsigned hidden, auto value4) __attribute__((always_inline)) {
+  auto spill = [&](unsigned long long bad, unsigned hidden, auto row) __attribute__((always_inline)) {
     const int ln = opaque(lane), q32 = ln & 31, hh = ln >> 5;
 #pragma unroll 1
     for (; bad; bad &= bad - 1) {
@@ -416,12 +416,13 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       // row r of the tile is key(i) of the lanes of half (r >> 2) & 1
       const unsigned hid = (unsigned)__shfl((int)hidden, q32 + 32 * (r >> 2 & 1), kWave);
       const bool see = !(hid >> (16 * (r >> 5) + 4 * (r >> 3 & 3) + (r & 3)) & 1);
+      const auto value4 = row(r);
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         asm volatile("" ::: "memory");                  // (no loads ahead: this is the rare path)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-          const uint2 v = value4(r, 32 * d + 8 * r4 + 4 * hh);   // four bf16
+          const uint2 v = value4(32 * d + 8 * r4 + 4 * hh);   // four bf16
           const float x[4] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -596,8 +597,9 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
       return scrub(t, [&](int i, int ln) { return ldsw + kV + kTile + i * 4096 + ln * 16; }, Par<kLd>{});
     };
     auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
-      spill(bad, hidden, [&](int r, int col) {
-        return *reinterpret_cast<const uint2*>(p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D + col);
+      spill(bad, hidden, [&](int r) {
+        const u16* at = p.v + (int64_t)(t0 + min(t * kBN + r, L - 1)) * p.v_stride + (int64_t)h * D;
+        return [=](int col) { return *reinterpret_cast<const uint2*>(at + col); };
       });
     };
     auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2], uint32_t kV) __attribute__((always_inline)) {
@@ -802,10 +804,11 @@ __global__ void __launch_bounds__(kExtThreads, D <= 128 ? 2 : 1) extend_kernel(c
         return bad;
       };
       auto dirty = [&](unsigned long long bad) __attribute__((always_inline)) {
-        spill(bad, hidden, [&](int r, int col) {
+        spill(bad, hidden, [&](int r) {
           const int row = min(x * kBN + r, P - 1), pg = max(page_of(p.c, n, row), 0);
-          const uint32_t w4 = *reinterpret_cast<const uint32_t*>(p.c.v + (page_rows(p.c, pg, h) + (row & pmask)) * D + col);
-          return f8x4_to_bf16(w4, p.c.v_scale[(int64_t)pg * p.H_kv + h]);   // (code * scale may pass the largest float)
+          const uint8_t* at = p.c.v + (page_rows(p.c, pg, h) + (row & pmask)) * D;
+          const float sc = lane_f(pvs, lane_of(row));     // (code * scale may pass the largest float)
+          return [=](int col) { return f8x4_to_bf16(*reinterpret_cast<const uint32_t*>(at + col), sc); };
         });
       };
       auto one = [&](f32x16 (&s)[kN2], f32x16 (&s2)[kN2]) __attribute__((always_inline)) {
