@@ -10,7 +10,7 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_DTYPE, GDN_E_UNSUPPORTED, GDN_E_INDEX, GDN_E_HIP, GDN_E_SCRATCH = range(8)
 GDN_F32, GDN_BF16 = 0, 1
 GDN_MODE_GDN, GDN_MODE_SSD = 0, 1
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 EXPORTED = ["gdn_gate", "gdn_extend", "gdn_decode", "gdn_extend_gated", "gdn_decode_gated",
             "gdn_conv1d", "gdn_conv1d_update", "gdn_validate_slots", "gdn_status_str",
@@ -97,7 +97,7 @@ class AttnExtendArgs(C.Structure):
                 ("cu_seqlens", C.c_void_p), ("cache_len", C.c_void_p), ("start", C.c_void_p),
                 ("block_table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32),
                 ("causal", C.c_int32), ("visible", C.c_void_p), ("doc", C.c_void_p), ("slopes", C.c_void_p),
-                ("window", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float), ("_pad0", C.c_int32),
+                ("window", C.c_int32), ("scale", C.c_float), ("softcap", C.c_float), ("max_cached", C.c_int32),
                 ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
 
 

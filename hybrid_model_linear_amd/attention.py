@@ -194,7 +194,7 @@ def kv_store(k, v, cu_seqlens, cache: KVCache, block_table, cache_len, *, start=
 
 # ------------------------------------------------------------------ attention
 def _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache, block_table,
-                 cache_len, start, out):
+                 cache_len, start, out, max_cached=0):
     T, H, d = q.shape
     H_kv, N = k.shape[1], cu_seqlens.shape[0] - 1
     if cache is not None:
@@ -216,12 +216,12 @@ def _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, do
         _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(cache_len, "cache_len", N),
         _vec(start, "start", N), _at(block_table), ts, tw, 1 if causal else 0, _vec(visible, "visible", N),
         _vec(doc, "doc", T), _vec(slopes, "slopes", H, _F32), window, d ** -0.5 if scale is None else scale,
-        softcap), i
+        softcap, max_cached), i
 
 
 def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0, slopes=None,
                 window: int = 0, doc=None, visible=None, cache: KVCache | None = None, block_table=None,
-                cache_len=None, start=None, out=None, workspace: torch.Tensor | None = None):
+                cache_len=None, start=None, max_cached: int = 0, out=None, workspace: torch.Tensor | None = None):
     """Attention of packed new tokens over their own keys and values and, with `cache`, the
     cache_len[n] rows that each sequence holds already.  q [T, H, d], k, v [T, H_kv, d]
     bf16; cu_seqlens int32 [N+1].
@@ -231,6 +231,8 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
     mask); causal=False lets every token see every other.  doc int32 [T]: a token sees only
     tokens with its own id; a negative id sees nothing and is not seen (output 0).
     start int32 [N]: position of each first token (default: behind the cached rows).
+    max_cached: host hint of the longest cache_len, else the table's width counts (speed
+    only: how the keys of few rows are split).
     workspace: uint8 device tensor of attn_extend_workspace_size bytes (else one is
     allocated where the keys of few rows are split).
     Returns out [T, H, d] bf16 (rows behind the last sequence, and those of sequences with
@@ -239,7 +241,7 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
     if out is None:
         out = _like(q)
     args, i = _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache,
-                           block_table, cache_len, start, out)
+                           block_table, cache_len, start, out, max_cached)
     # (fewer than 512 keys are not split: no query, which short calls would feel)
     ws = None
     if workspace is not None or cache is not None or q.shape[0] >= 512:
@@ -251,12 +253,12 @@ def attn_extend(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap
 
 def attn_extend_workspace_size(q, k, v, cu_seqlens, *, scale=None, causal: bool = True, softcap: float = 0.0,
                                slopes=None, window: int = 0, doc=None, visible=None, cache: KVCache | None = None,
-                               block_table=None, cache_len=None, start=None) -> int:
+                               block_table=None, cache_len=None, start=None, max_cached: int = 0) -> int:
     """Bytes of workspace with which attn_extend splits the keys of these arguments (0: no
     split)."""
     lib = _lib.load()
     args, i = _extend_args(q, k, v, cu_seqlens, scale, causal, softcap, slopes, window, doc, visible, cache,
-                           block_table, cache_len, start, None)
+                           block_table, cache_len, start, None, max_cached)
     return _need("gdn_attn_extend_workspace_size", lib.gdn_attn_extend_workspace_size, args, i)
 
 
@@ -357,7 +359,8 @@ def forward_attn(layer, forward_batch, q, k, v, save_kv_cache: bool = True):
            (negative: a padding row); optional positions int32 [N] of each sequence's first
            new token (default cache_len; needed once rows have been evicted); for extend
            modes cu_seqlens int32 [N+1]; optional accumulate_weights (decode: add the
-           softmax weights to the cache's); optional max_kvlen, a host hint.
+           softmax weights to the cache's); optional max_kvlen, a host hint of the longest
+           sequence.
     q [T, num_heads * head_dim], k, v [T, num_kv_heads * head_dim] (or [T, heads, head_dim]).
     save_kv_cache=False leaves the cache as it is (draft models; extend modes only, since a
     decode step attends to its own stored row).  Target verify leaves it as it is too: the
@@ -388,7 +391,8 @@ def forward_attn(layer, forward_batch, q, k, v, save_kv_cache: bool = True):
         verify = _is_target_verify(fb.forward_mode)
         if verify and getattr(fb, "spec_parents", None) is not None:
             raise ValueError("forward_attn has no token trees: verify a chain")
-        o = attn_extend(q, k, v, fb.cu_seqlens, cache=cache, block_table=table, cache_len=held, start=start, **kw)
+        o = attn_extend(q, k, v, fb.cu_seqlens, cache=cache, block_table=table, cache_len=held, start=start,
+                        max_cached=int(getattr(fb, "max_kvlen", 0) or 0), **kw)
         if save_kv_cache and not verify:
             kv_store(k, v, fb.cu_seqlens, cache, table, held, start=start)
     return o.view(T, H * d)

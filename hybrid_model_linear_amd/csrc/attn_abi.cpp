@@ -119,7 +119,8 @@ int plan_extend(const gdn_attn_extend_args* a, gdn::AttnExtendLaunch& p, int64_t
   if (!a) return GDN_E_NULL;
   if (a->in_dtype != GDN_BF16 || a->out_dtype != GDN_BF16) return GDN_E_DTYPE;
   if (a->d != 64 && a->d != 128 && a->d != 256) return GDN_E_UNSUPPORTED;
-  if (a->N < 0 || a->T < 0 || a->T > INT32_MAX || a->H_kv <= 0 || a->H <= 0 || a->H % a->H_kv != 0) return GDN_E_SHAPE;
+  if (a->N < 0 || a->T < 0 || a->T > INT32_MAX || a->H_kv <= 0 || a->H <= 0 || a->H % a->H_kv != 0 || a->max_cached < 0)
+    return GDN_E_SHAPE;
   int st = check_scores(a->scale, a->softcap, a->window);
   if (st != GDN_OK) return st;
   if (a->cache.k) {
@@ -169,7 +170,11 @@ int plan_extend(const gdn_attn_extend_args* a, gdn::AttnExtendLaunch& p, int64_t
   p.softcap = a->softcap;
   const int64_t group = a->H / a->H_kv;
   int64_t keys = (a->T + a->N - 1) / a->N;               // (a table has room for the new tokens as a rule)
-  if (p.c.k && (int64_t)a->table_width * a->cache.page > keys) keys = (int64_t)a->table_width * a->cache.page;
+  if (p.c.k) {
+    int64_t held = (int64_t)a->table_width * a->cache.page;
+    if (a->max_cached > 0 && a->max_cached + keys < held) held = a->max_cached + keys;
+    if (held > keys) keys = held;
+  }
   if (a->window > 0 && !(p.c.k && a->cache.pos) && keys > a->window + 128 / group + 64) keys = a->window + 128 / group + 64;
   gdn::plan_attn_extend(p, keys, gdn::current_device_cus());
   if (p.splits > 1) {

@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 9
+#define GDN_ABI_VERSION 10
 
 typedef enum gdn_status {
   GDN_OK = 0,
@@ -484,8 +484,9 @@ int gdn_kv_store(const gdn_kv_store_args* args, void* stream);
  * T * (H / H_kv) must stay below 2^31 - 1024 (GDN_E_UNSUPPORTED).
  * With few rows the keys are split over workgroups, whose parts stand in a workspace of
  * gdn_attn_extend_workspace_size bytes (0: none), 256-byte aligned, with any contents (calls in
- * flight at once need their own); without one (NULL) they are not split.  One launch, two
- * with a split. */
+ * flight at once need their own); without one (NULL) they are not split.  The split goes by
+ * the table's width, or by max_cached, a host hint of the longest cache_len (0 = unknown):
+ * speed only, but for the workspace.  One launch, two with a split. */
 typedef struct gdn_attn_extend_args {
   gdn_kv_cache cache;
   int32_t in_dtype;            /* GDN_BF16                         */
@@ -514,7 +515,7 @@ typedef struct gdn_attn_extend_args {
   int32_t window;              /* 0 = none                         */
   float scale;
   float softcap;               /* 0 = none                         */
-  int32_t _pad0;
+  int32_t max_cached;          /* 0 = unknown                      */
   void* workspace;             /* or NULL                          */
   int64_t workspace_bytes;
 } gdn_attn_extend_args;

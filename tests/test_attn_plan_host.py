@@ -1,12 +1,14 @@
 """Host-side tests of how attn_extend and attn_decode cut a call and of what they refuse for its
 size (no GPU: workspace queries and calls that fail validation launch nothing)."""
 import ctypes as ct
+from unittest import mock
 
 import pytest
+import torch
 
 import hybrid_model_linear_amd as gdn
-from hybrid_model_linear_amd import _lib
-from test_attn_host import P, _cache, _extend
+from hybrid_model_linear_amd import _lib, attention
+from test_attn_host import P, _batch, _cache, _extend, _layer
 
 CUS = 256            # what the library assumes without a device
 KEYS = 7000
@@ -43,3 +45,22 @@ def test_batches_that_fill_the_chip_are_cut_in_four_at_most(n, tokens, H, H_kv, 
 
 def test_chunks_that_fill_the_chip_are_not_cut():
     assert _parts(4, 512, 16, 2, 256) == _parts(4, 512, 32, 8, 128) == 1
+
+
+def test_a_hint_of_the_cached_rows_counts_instead_of_the_table():
+    wide = dict(n=8, tokens=16, H=32, H_kv=8, d=128, keys=32768)
+    assert _parts(**wide) > 1
+    assert _parts(**wide, max_cached=200) == 1
+    assert _parts(**wide, max_cached=32768) == _parts(**wide, max_cached=1 << 30) == _parts(**wide)
+    assert 1 < _parts(**dict(wide, n=1), max_cached=1500) < _parts(**dict(wide, n=1))
+    a = _extend(_cache(), max_cached=-1)
+    assert gdn.load().gdn_attn_extend(ct.byref(a), None) == _lib.GDN_E_SHAPE
+
+
+def test_forward_attn_passes_its_hint_on():
+    x = torch.zeros(2, 4 * 64), torch.zeros(2, 2 * 64), torch.zeros(2, 2 * 64)
+    with mock.patch.object(attention, "kv_store"), mock.patch.object(attention, "attn_extend") as ex:
+        ex.return_value = torch.zeros(2, 4, 64)
+        for kw, hint in ((dict(max_kvlen=77), 77), (dict(max_kvlen=None), 0), ({}, 0)):
+            gdn.forward_attn(_layer(), _batch("extend", **kw), *x)
+            assert ex.call_args.kwargs["max_cached"] == hint

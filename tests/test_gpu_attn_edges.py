@@ -305,3 +305,22 @@ def test_extend_shapes_of_scores(gdn_lib, d, cached, shape):
     got = gdn_lib.attn_extend(*(up(x, BF16) for x in (q, k, v)), i32(_cu(lens)), scale=scale, softcap=softcap, slopes=up(slopes),
                               **gkw).float().cpu().numpy()
     assert_out(got, ref, mag, score_error(q, knorm, abs(scale), softcap, 0.5 if opt.get("slopes") else 0.0, 400), shape)
+
+
+# ------------------------------------------------------------------ the hint of the cached rows
+def test_extend_hints_change_the_split_only(gdn_lib):
+    print("[case] extend, max_cached", flush=True)
+    rng = np.random.default_rng(51)
+    lens, old, H, H_kv, d, page = [3, 9, 1], [1700, 40, 0], 4, 2, 128, 32
+    c = make_cache(rng, 60, H_kv, page, d)
+    table = make_table(rng, old, page, 60, width=200)
+    q, k, v = _qkv(rng, sum(lens), H, H_kv, d)
+    ref, mag = oa.attn_extend(q, k, v, _cu(lens), 0.1, cache=c, table=table, cache_len=old)
+    args = [up(x, BF16) for x in (q, k, v)] + [i32(_cu(lens))]
+    kw = dict(scale=0.1, cache=upload_cache(gdn_lib, c), block_table=i32(table), cache_len=i32(old))
+    need = []
+    for hint in (0, 1700, 1, 2 ** 31 - 1):             # (also where it is too small)
+        need.append(gdn_lib.attn_extend_workspace_size(*args, max_cached=hint, **kw))
+        got = gdn_lib.attn_extend(*args, max_cached=hint, **kw).float().cpu().numpy()
+        assert_out(got, ref, mag, score_error(q, max(row_norm(k), cache_norm(c)), 0.1), f"hint {hint}")
+    assert need[0] == need[3] > need[1] > need[2] == 0
