@@ -8,8 +8,9 @@
 and the layer call of the pages:
   forward_attn(layer, forward_batch, q, k, v)   (pymllm RadixAttention.forward)
 
-As in the rest of the binding every step runs in the library's HIP kernels; this module
-checks tensors, allocates what the caller did not supply and passes pointers.
+As in the rest of the binding the operators run in the library's HIP kernels; this module
+checks tensors, allocates what the caller did not supply and passes pointers.  (forward_attn
+forms a decode step's lengths, cache_len + 1, with torch.)
 """
 from __future__ import annotations
 
@@ -347,13 +348,27 @@ def kv_evict_workspace_size(cache: KVCache, block_table, kv_len, budget: int, *,
 
 
 # ------------------------------------------------------------------ layer call
+def _check_layer(layer) -> None:
+    """Refuses layers that ask for another attention than forward_attn's."""
+    if getattr(layer, "is_cross_attention", False):
+        raise ValueError("forward_attn is self-attention: is_cross_attention is not supported")
+    kind = getattr(layer, "attn_type", None)
+    if kind is not None and str(getattr(kind, "value", kind)).lower() != "decoder":
+        raise ValueError(f"forward_attn is a decoder's causal attention, got attn_type {kind!r} (attn_extend has causal=False)")
+    d_v = getattr(layer, "v_head_dim", None)
+    if d_v not in (None, -1, layer.head_dim):
+        raise ValueError(f"keys and values have one head size: head_dim {layer.head_dim}, v_head_dim {d_v}")
+
+
 def forward_attn(layer, forward_batch, q, k, v, save_kv_cache: bool = True):
     """Full-attention layer call of a hybrid model (pymllm RadixAttention.forward), the
     counterpart of forward_gdn: stores the new tokens in the layer's cache and attends.
 
     layer: num_heads, num_kv_heads, head_dim, layer_id; optional scaling (default head_dim
-           ** -0.5), logit_cap (tanh cap, 0 = none), sliding_window_size (-1 or 0 = none),
-           alibi_slopes fp32 [num_heads].
+           ** -0.5), logit_cap (tanh cap, 0 = none), sliding_window_size (-1 or 0 = none; w:
+           a token sees itself and the w - 1 before it), alibi_slopes fp32 [num_heads].  A
+           layer with is_cross_attention, an attn_type other than "decoder" or a v_head_dim
+           other than head_dim raises ValueError.
     forward_batch: forward_mode; kv_pool indexable by layer_id -> KVCache; block_table int32
            [N, width]; cache_len int32 [N], the rows each sequence holds before this call
            (negative: a padding row); optional positions int32 [N] of each sequence's first
@@ -366,6 +381,7 @@ def forward_attn(layer, forward_batch, q, k, v, save_kv_cache: bool = True):
     decode step attends to its own stored row).  Target verify leaves it as it is too: the
     accepted tokens are the caller's to store; token trees (spec_parents) raise ValueError.
     Returns out [T, num_heads * head_dim] bf16."""
+    _check_layer(layer)
     kind = _mode_kind(forward_batch.forward_mode)
     H, H_kv, d = layer.num_heads, layer.num_kv_heads, layer.head_dim
     T = q.shape[0]
