@@ -13,7 +13,7 @@ namespace {
 bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 constexpr int64_t kMaxStride = 1 << 22;     // a 64-row tile's byte offsets stay in 32 bits
-constexpr int64_t kMaxGrid = INT32_MAX;
+constexpr int64_t kMaxGrid = (1 << 24) - 1;   // workgroups of 256 threads: a launch has fewer than 2^32 in a dimension
 constexpr int32_t kMaxWindow = 1 << 30;     // distances are shorter; a window added to one stays in 32 bits
 
 int page_log2(int32_t page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
@@ -101,6 +101,7 @@ int plan_decode(const gdn_attn_decode_args* a, gdn::AttnDecodeLaunch& p, int64_t
   if (a->window > 0 && !a->cache.pos && a->window < rows) rows = a->window;
   gdn::plan_attn_decode(p, rows, gdn::current_device_cus());
   if ((int64_t)p.splits * ((a->H / p.c.H_kv + 15) / 16) * p.c.H_kv * a->N > kMaxGrid) return GDN_E_UNSUPPORTED;
+  if (p.accumulate && a->H + (p.score_cap / 1024 + 2) * p.c.H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;   // (the join: 1024 rows each)
   const int64_t heads = (int64_t)a->N * a->H;
   auto part = [&](int64_t floats) {
     const int64_t at = need;
@@ -204,6 +205,7 @@ int plan_evict(const gdn_kv_evict_args* a, gdn::EvictLaunch& p, int64_t& need) {
   if (a->N == 0) return GDN_OK;
   const int64_t lists = (int64_t)a->N * p.c.H_kv * p.budget;
   const int64_t pages = ((int64_t)p.budget + a->cache.page - 1) / a->cache.page;
+  if (pages > kMaxGrid) return GDN_E_UNSUPPORTED;
   auto part = [&](int64_t bytes) {
     const int64_t at = need;
     need += (bytes + 255) / 256 * 256;
@@ -238,7 +240,8 @@ int gdn_kv_store(const gdn_kv_store_args* a, void* stream) {
   if (a->N > 0 && !a->cache_len) return GDN_E_NULL;
   if (!rows_ok(a->k, a->k_stride, p.c.H_kv, p.c.d) || !rows_ok(a->v, a->v_stride, p.c.H_kv, p.c.d)) return GDN_E_SHAPE;
   if (a->N == 0 || a->T == 0) return GDN_OK;
-  if (((a->T >> p.c.page_log2) + 2 * (int64_t)a->N) * p.c.H_kv > kMaxGrid) return GDN_E_UNSUPPORTED;
+  const int64_t slots = (a->T >> p.c.page_log2) + 2 * (int64_t)a->N;     // pages: a workgroup each, or for half a head
+  if (slots > kMaxGrid || slots * p.c.H_kv > 2 * kMaxGrid) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.T = a->T;
   p.k = static_cast<const gdn::u16*>(a->k);

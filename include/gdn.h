@@ -410,7 +410,8 @@ int gdn_conv1d_update(const gdn_conv_args* args, void* stream);
  * bf16 for the product with the values.  A value that a query does not see does not
  * reach it, whatever it holds (NaN and infinities too).  Positions, given or from lengths,
  * lie in [0, 2^30); softcap is at most 8192 (GDN_E_UNSUPPORTED: near 0 the tanh is off by
- * softcap 2^-22).
+ * softcap 2^-22).  Calls whose launch would have 2^32 threads or more in a dimension are
+ * GDN_E_UNSUPPORTED.
  *
  * The cache.  Pages of `page` rows; row r of a sequence is row r % page of the page
  * block_table[n, r / page] (row stride table_stride, table_width entries per sequence).

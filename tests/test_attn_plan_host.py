@@ -8,7 +8,7 @@ import torch
 
 import hybrid_model_linear_amd as gdn
 from hybrid_model_linear_amd import _lib, attention
-from test_attn_host import P, _batch, _cache, _extend, _layer
+from test_attn_host import P, _batch, _cache, _decode, _evict, _extend, _layer, _store
 
 CUS = 256            # what the library assumes without a device
 KEYS = 7000
@@ -64,3 +64,35 @@ def test_forward_attn_passes_its_hint_on():
         for kw, hint in ((dict(max_kvlen=77), 77), (dict(max_kvlen=None), 0), ({}, 0)):
             gdn.forward_attn(_layer(), _batch("extend", **kw), *x)
             assert ex.call_args.kwargs["max_cached"] == hint
+
+
+# A launch has fewer than 2^32 threads in a dimension, 2^24 - 1 workgroups of 256.
+def test_decode_calls_past_the_largest_launch_are_refused():
+    lib = gdn.load()
+    for H_kv, fits in ((255, True), (256, True), (257, False), (1000, False)):
+        a = _decode(_cache(H_kv=H_kv, d=64), N=65535, H=H_kv, q_stride=H_kv * 64, out_stride=H_kv * 64, out=1 << 50)
+        need = lib.gdn_attn_decode_workspace_size(ct.byref(a))
+        assert (need >= 0) == fits and (fits or need == -_lib.GDN_E_UNSUPPORTED)
+        if not fits:
+            assert lib.gdn_attn_decode(ct.byref(a), None) == _lib.GDN_E_UNSUPPORTED
+    a = _decode(_cache(H_kv=9000, d=64), N=1, H=9000, q_stride=9000 * 64, out_stride=9000 * 64, out=1 << 50, accumulate=1,
+                table_width=1 << 24, table_stride=1 << 24)
+    assert lib.gdn_attn_decode_workspace_size(ct.byref(a)) == -_lib.GDN_E_UNSUPPORTED
+
+
+def test_extend_calls_past_the_largest_launch_are_refused():
+    for N, fits in ((1 << 23, True), (1 << 24, False)):
+        a = _extend(N=N, T=1, H=1, H_kv=1, d=64, q_stride=64, k_stride=64, v_stride=64, out_stride=64)
+        need = gdn.load().gdn_attn_extend_workspace_size(ct.byref(a))
+        assert need == (0 if fits else -_lib.GDN_E_UNSUPPORTED)
+
+
+def test_store_and_evict_calls_past_the_largest_launch_are_refused():
+    lib = gdn.load()
+    many = 1 << 23
+    assert lib.gdn_kv_store(ct.byref(_store(N=many, T=many)), None) == _lib.GDN_E_UNSUPPORTED
+    assert lib.gdn_kv_store(ct.byref(_store(_cache(H_kv=64, d=64), N=1 << 20, T=1 << 20, k_stride=4096, v_stride=4096)), None) == \
+        _lib.GDN_E_UNSUPPORTED
+    wide = dict(table_width=1 << 26, table_stride=1 << 26, budget=1 << 30, N=1)
+    assert lib.gdn_kv_evict_workspace_size(ct.byref(_evict(_cache(page=16), **wide))) == -_lib.GDN_E_UNSUPPORTED
+    assert lib.gdn_kv_evict_workspace_size(ct.byref(_evict(_cache(page=16), **dict(wide, budget=1 << 27)))) > 0
