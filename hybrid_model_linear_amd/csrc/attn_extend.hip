@@ -935,9 +935,9 @@ hipError_t launch_d(const AttnExtendLaunch& p, hipStream_t s) {
 // many short ones the launch's workgroups are counted, one per sequence at least and up to one
 // more that finds no rows, so that an eighth over is no second round (4 tokens each over 7000
 // rows: 16 sequences, 32 / 8, d = 128: 4 parts 70 us, 16 80; 32 of 16 / 2, d = 256: 3 113, 16
-// 133).  Where fewer than three have a place then, up to four even out the rounds (48
-// sequences, 32 / 8, d = 128: 243 us whole, 215, 16 245; 64 304 in d = 256, 16 / 2, 249, 246; but
-// 64 of 32 / 8, d = 128: 275, 285, 327).
+// 133).  Where fewer than three have a place then, up to four even out the rounds (whole, in 4
+// and in 16 parts: 48 sequences, 32 / 8, d = 128 243, 215 and 245 us; 64 of 16 / 2, d = 256 304,
+// 249 and 246; but 64 of 32 / 8, d = 128 275, 285 and 327).
 void plan_attn_extend(AttnExtendLaunch& p, int64_t keys, int cus) {
   const int64_t group = p.H / p.H_kv, places = (int64_t)cus * (p.d <= 128 ? 2 : 1);
   const int64_t wgs = (p.T * group + kBM - 1) / kBM * p.H_kv, grid = (p.T * group / kBM + p.N) * p.H_kv;

@@ -441,7 +441,8 @@ typedef struct gdn_kv_cache {
  * page that holds earlier rows of the sequence keeps the larger of its scale and the new
  * rows' need; where the scale grows, the earlier codes are rounded to it.  A page that
  * starts with the new rows takes their scale.  NaN and infinities are stored as NaN and
- * do not count for the scale.  Rows behind the last one written are left as they are.
+ * do not count for the scale.  (Finite values past 31 2^123, near bf16's largest, may round
+ * to 2^128, which is infinite.)  Rows behind the last one written are left as they are.
  * With cache.pos the rows' positions become start[n], start[n] + 1, ... (start NULL:
  * cache_len[n]); with cache.weight their weights become 0.  k, v: bf16 [T, H_kv, d],
  * 16-byte aligned rows (strides multiples of 8).  Two sequences of one call must not
@@ -532,9 +533,11 @@ int64_t gdn_attn_extend_workspace_size(const gdn_attn_extend_args* args);
  * adds to cache.weight of every row of the sequence the sum of the softmax weights that
  * the kv head's H / H_kv query heads give it; sequences of one call must then not share
  * pages.  N is at most 65535.  max_kvlen is a host hint of the longest kv_len (0 = unknown): speed only.
+ * With cache.pos a window is looked up row by row: all kv_len[n] rows are read.
  * The rows are split over workgroups, whose partial results a second launch joins; they
  * stand in a workspace of gdn_attn_decode_workspace_size bytes (0: none needed), 256-byte
- * aligned, with any contents; calls in flight at once need their own. */
+ * aligned, with any contents; calls in flight at once need their own.  accumulate takes 4
+ * bytes of it per query head and row of the table, whatever max_kvlen says. */
 typedef struct gdn_attn_decode_args {
   gdn_kv_cache cache;
   int32_t in_dtype;            /* GDN_BF16                         */
@@ -567,7 +570,8 @@ int64_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
 /* gdn_kv_evict: cut every sequence to at most `budget` rows per kv head, in place.  Of a
  * sequence of kv_len[n] > budget rows, each kv head keeps the rows with pos > (its largest
  * pos) - recent, then those of largest weight; ties go to the lowest row, a NaN weight
- * ranks below all others, and never more than `budget` rows are kept.  The kept rows at
+ * ranks below all others, and never more than `budget` rows are kept.  (Weights come from
+ * gdn_attn_decode alone: rows that no decode step has attended to yet are ties.)  The kept rows at
  * or past `budget` move, in order, into the dropped rows before it, in order, with their
  * pos and weight; the others stay.  (Attention does not depend on the order of rows, only
  * on their pos.)  The scale of a page that receives rows becomes the largest of its own
