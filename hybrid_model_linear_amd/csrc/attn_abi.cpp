@@ -240,8 +240,8 @@ int gdn_kv_store(const gdn_kv_store_args* a, void* stream) {
   if (a->N > 0 && !a->cache_len) return GDN_E_NULL;
   if (!rows_ok(a->k, a->k_stride, p.c.H_kv, p.c.d) || !rows_ok(a->v, a->v_stride, p.c.H_kv, p.c.d)) return GDN_E_SHAPE;
   if (a->N == 0 || a->T == 0) return GDN_OK;
-  const int64_t slots = (a->T >> p.c.page_log2) + 2 * (int64_t)a->N;     // pages: a workgroup each, or for half a head
-  if (slots > kMaxGrid || slots * p.c.H_kv > 2 * kMaxGrid) return GDN_E_UNSUPPORTED;
+  const int64_t slots = a->cu_seqlens ? (a->T >> p.c.page_log2) + 2 * (int64_t)a->N : a->N;   // pages; for few tokens a workgroup takes two heads
+  if (slots > kMaxGrid || (a->T <= gdn::kFewTokens * (int64_t)a->N && slots * p.c.H_kv > 2 * kMaxGrid)) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.T = a->T;
   p.k = static_cast<const gdn::u16*>(a->k);

@@ -27,6 +27,11 @@ struct CacheRef {
   int table_width;
 };
 
+// Tokens per sequence, on average, up to which a wave takes a page and head, not a workgroup.
+// wave / workgroup, us, 8 heads of 128: 256 sequences of 1 token 6.0 / 13.0, of 8 7.7 / 14.8;
+// 32 of 8 4.4 / 4.7, of 16 5.4 / 5.1, of 64 11.1 / 6.3; one of 8 3.8 / 3.4, of 64 9.3 / 4.1.
+constexpr int kFewTokens = 8;
+
 struct StoreLaunch {
   CacheRef c;
   int N;
