@@ -20,6 +20,10 @@ the softmax attention of the model's other layers (attention.py):
   attn_extend          packed varlen, cached prefix        -> gdn_attn_extend
   attn_decode          one token per sequence, cache       -> gdn_attn_decode
   kv_evict             by accumulated weight, in place     -> gdn_kv_evict
+what a step runs beside its attention (step.py):
+  selective_scan, selective_update  state space scan with a decay matrix -> gdn_selective_scan, _update
+  rms_norm             norm, residual, gate, 8-bit output  -> gdn_rms_norm
+  page_pool, plan_pages, release_pages  a step's block tables and slot maps -> gdn_plan_pages, gdn_release_pages
 and the call shapes of the pages:
   forward_gdn(layer, forward_batch, mixed_qkv, a, b)  (pymllm HybridAttnBackend.forward_gdn)
   forward_attn(layer, forward_batch, q, k, v)         (pymllm RadixAttention.forward)
@@ -39,7 +43,9 @@ __all__ = ["load", "gate", "ssd_gate", "extend", "extend_noalloc", "extend_kerne
            "extend_workspace_size", "decode", "conv1d", "conv1d_update", "validate_slots", "forward_gdn",
            "ssd_combined_fwd", "GDNError", "split_mixed_qkv", "probe_copy", "probe_mfma",
            "KVCache", "kv_cache", "kv_store", "attn_extend", "attn_extend_workspace_size", "attn_decode", "attn_decode_workspace_size",
-           "kv_evict", "kv_evict_workspace_size", "forward_attn"]
+           "kv_evict", "kv_evict_workspace_size", "forward_attn",
+           "selective_scan", "selective_scan_workspace_size", "selective_update", "rms_norm",
+           "PagePool", "StepPlan", "page_pool", "plan_pages", "release_pages"]
 
 
 def load():
@@ -711,3 +717,5 @@ def ssd_combined_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=F
 
 from .attention import (KVCache, attn_decode, attn_decode_workspace_size, attn_extend,  # noqa: E402
                         attn_extend_workspace_size, forward_attn, kv_cache, kv_evict, kv_evict_workspace_size, kv_store)
+from .step import (PagePool, StepPlan, page_pool, plan_pages, release_pages, rms_norm,  # noqa: E402
+                   selective_scan, selective_scan_workspace_size, selective_update)

@@ -8,16 +8,18 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
 
 GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_DTYPE, GDN_E_UNSUPPORTED, GDN_E_INDEX, GDN_E_HIP, GDN_E_SCRATCH = range(8)
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
 GDN_MODE_GDN, GDN_MODE_SSD = 0, 1
-ABI_VERSION = 10
+ABI_VERSION = 11
 
 EXPORTED = ["gdn_gate", "gdn_extend", "gdn_decode", "gdn_extend_gated", "gdn_decode_gated",
             "gdn_conv1d", "gdn_conv1d_update", "gdn_validate_slots", "gdn_status_str",
             "gdn_last_hip_error", "gdn_abi_version", "gdn_extend_workspace_size", "gdn_extend_kernel",
             "gdn_extend_noalloc", "gdn_probe_copy", "gdn_probe_mfma",
             "gdn_kv_store", "gdn_attn_extend", "gdn_attn_extend_workspace_size", "gdn_attn_decode", "gdn_attn_decode_workspace_size",
-            "gdn_kv_evict", "gdn_kv_evict_workspace_size"]
+            "gdn_kv_evict", "gdn_kv_evict_workspace_size",
+            "gdn_selective_scan", "gdn_selective_scan_workspace_size", "gdn_selective_update", "gdn_rms_norm",
+            "gdn_plan_pages", "gdn_release_pages"]
 
 # gdn_extend_kernel results and reason bits (include/gdn.h)
 GDN_KERNEL_RECURRENT, GDN_KERNEL_CHUNKED, GDN_KERNEL_SSD_CHUNKED = 1, 2, 3
@@ -118,6 +120,41 @@ class KVEvictArgs(C.Structure):
                 ("workspace_bytes", C.c_int64)]
 
 
+class SelectiveArgs(C.Structure):
+    _fields_ = [("in_dtype", C.c_int32), ("out_dtype", C.c_int32), ("N", C.c_int32), ("G", C.c_int32),
+                ("T", C.c_int64), ("D", C.c_int64), ("states", C.c_int32), ("dt_softplus", C.c_int32),
+                ("x", C.c_void_p), ("x_stride", C.c_int64), ("dt", C.c_void_p), ("dt_stride", C.c_int64),
+                ("B", C.c_void_p), ("B_stride", C.c_int64), ("C", C.c_void_p), ("C_stride", C.c_int64),
+                ("z", C.c_void_p), ("z_stride", C.c_int64), ("A", C.c_void_p), ("D_skip", C.c_void_p),
+                ("dt_bias", C.c_void_p), ("cu_seqlens", C.c_void_p), ("slot", C.c_void_p),
+                ("has_init", C.c_void_p), ("pool", C.c_void_p), ("num_slots", C.c_int64), ("out", C.c_void_p),
+                ("out_stride", C.c_int64), ("max_seqlen", C.c_int32), ("keep_pool", C.c_int32),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
+class RmsNormArgs(C.Structure):
+    _fields_ = [("in_dtype", C.c_int32), ("out_dtype", C.c_int32), ("weight_dtype", C.c_int32),
+                ("residual_dtype", C.c_int32), ("T", C.c_int64), ("H", C.c_int32), ("d", C.c_int32),
+                ("x", C.c_void_p), ("x_stride", C.c_int64), ("gate", C.c_void_p), ("gate_stride", C.c_int64),
+                ("residual", C.c_void_p), ("residual_stride", C.c_int64), ("weight", C.c_void_p),
+                ("out", C.c_void_p), ("out_stride", C.c_int64), ("scale", C.c_void_p), ("eps", C.c_float),
+                ("offset", C.c_float), ("gate_first", C.c_int32), ("group", C.c_int32)]
+
+
+class PlanPagesArgs(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("capacity", C.c_int64), ("N", C.c_int32), ("page", C.c_int32), ("T", C.c_int64),
+                ("held", C.c_void_p), ("new_len", C.c_void_p), ("start", C.c_void_p), ("block_table", C.c_void_p),
+                ("table_stride", C.c_int64), ("table_width", C.c_int32), ("_pad0", C.c_int32),
+                ("cu_seqlens", C.c_void_p), ("cache_len", C.c_void_p), ("kv_len", C.c_void_p),
+                ("slots", C.c_void_p), ("positions", C.c_void_p), ("seq", C.c_void_p)]
+
+
+class ReleasePagesArgs(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("capacity", C.c_int64), ("N", C.c_int32), ("page", C.c_int32),
+                ("keep", C.c_void_p), ("held", C.c_void_p), ("block_table", C.c_void_p),
+                ("table_stride", C.c_int64), ("table_width", C.c_int32), ("_pad0", C.c_int32)]
+
+
 _lib = None
 
 
@@ -154,11 +191,15 @@ def load(path: str | None = None) -> C.CDLL:
     lib.gdn_probe_mfma.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p]
     lib.gdn_probe_mfma.restype = C.c_int
     for fn, args in (("gdn_kv_store", KVStoreArgs), ("gdn_attn_extend", AttnExtendArgs),
-                     ("gdn_attn_decode", AttnDecodeArgs), ("gdn_kv_evict", KVEvictArgs)):
+                     ("gdn_attn_decode", AttnDecodeArgs), ("gdn_kv_evict", KVEvictArgs),
+                     ("gdn_selective_scan", SelectiveArgs), ("gdn_selective_update", SelectiveArgs),
+                     ("gdn_rms_norm", RmsNormArgs), ("gdn_plan_pages", PlanPagesArgs),
+                     ("gdn_release_pages", ReleasePagesArgs)):
         getattr(lib, fn).argtypes = [C.POINTER(args), C.c_void_p]
         getattr(lib, fn).restype = C.c_int
     for fn, args in (("gdn_attn_extend_workspace_size", AttnExtendArgs),
-                     ("gdn_attn_decode_workspace_size", AttnDecodeArgs), ("gdn_kv_evict_workspace_size", KVEvictArgs)):
+                     ("gdn_attn_decode_workspace_size", AttnDecodeArgs), ("gdn_kv_evict_workspace_size", KVEvictArgs),
+                     ("gdn_selective_scan_workspace_size", SelectiveArgs)):
         getattr(lib, fn).argtypes = [C.POINTER(args)]
         getattr(lib, fn).restype = C.c_int64
     lib.gdn_status_str.argtypes = [C.c_int]

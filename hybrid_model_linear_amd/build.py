@@ -21,7 +21,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gate.hip", "recurrent.hip", "chunk.hip", "ssd.hip", "conv.hip", "validate.hip", "probe.hip",
-           "kv_cache.hip", "attn_decode.hip", "attn_extend.hip", "gdn_abi.cpp", "attn_abi.cpp"]
+           "kv_cache.hip", "attn_decode.hip", "attn_extend.hip", "selective.hip", "norm.hip", "pages.hip", "gdn_abi.cpp",
+           "attn_abi.cpp", "step_abi.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,235 @@
+// The pages of a step (gdn_plan_pages, gdn_release_pages): sums over the requests before
+// each one, then lists that they index.
+//
+// A workgroup of 256 threads looks after a slice of 256 requests, blockIdx.y splits the
+// slice's tokens and pages further.  Every workgroup adds up the requests in front of its
+// slice for itself (they are few, and in the caches), scans its own, and finds the request
+// of a token or page by bisection of the scan in LDS: one launch, and no workgroup waits
+// for another.  The number of free pages, which all of them read first, is written by the
+// last one to finish.
+#include "step_launch.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int64_t pages_of(int64_t rows, int page) { return (rows + page - 1) / page; }
+
+// Inclusive sums over the workgroup's threads of a pair; `a`, `b` become them.
+__device__ __forceinline__ void scan_pair(int64_t& a, int64_t& b, int64_t (&wave_sums)[2][kThreads / kWave]) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int s = 1; s < kWave; s <<= 1) {
+    const int64_t x = __shfl_up(a, s, kWave), y = __shfl_up(b, s, kWave);
+    if (lane >= s) { a += x; b += y; }
+  }
+  if (lane == kWave - 1) { wave_sums[0][wave] = a; wave_sums[1][wave] = b; }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) { a += wave_sums[0][w]; b += wave_sums[1][w]; }
+  __syncthreads();
+}
+
+// Sum of a pair over the workgroup, in every thread.
+__device__ __forceinline__ void sum_pair(int64_t& a, int64_t& b, int64_t (&wave_sums)[2][kThreads / kWave]) {
+#pragma unroll
+  for (int s = kWave / 2; s; s >>= 1) { a += __shfl_xor(a, s, kWave); b += __shfl_xor(b, s, kWave); }
+  if (threadIdx.x % kWave == 0) { wave_sums[0][threadIdx.x / kWave] = a; wave_sums[1][threadIdx.x / kWave] = b; }
+  __syncthreads();
+  a = b = 0;
+  for (int w = 0; w < kThreads / kWave; ++w) { a += wave_sums[0][w]; b += wave_sums[1][w]; }
+  __syncthreads();
+}
+
+// First k in [0, 256) with ends[k] > v (ends non-decreasing, ends[255] > v).
+__device__ __forceinline__ int find(const int64_t* ends, int64_t v) {
+  int lo = 0;
+#pragma unroll
+  for (int s = 128; s; s >>= 1)
+    if (ends[lo + s - 1] <= v) lo += s;
+  return lo;
+}
+
+// True in every thread of the last workgroup of the launch to come here; `arrivals` is 0
+// before and after the launch.
+__device__ __forceinline__ bool last_to_arrive(int32_t* arrivals, int* flag) {
+  const int total = gridDim.x * gridDim.y;
+  if (total == 1) return true;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int before = __hip_atomic_fetch_add(arrivals, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = before == total - 1;
+    if (*flag) __hip_atomic_store(arrivals, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+__device__ __forceinline__ int32_t load_agent(const int32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+struct Request {
+  int64_t held, tokens, lo, need;
+  bool live;
+};
+
+__device__ __forceinline__ Request request_of(const PlanPagesLaunch& p, int n) {
+  Request r{};
+  if (n >= p.N) return r;
+  r.held = p.held[n];
+  const int64_t add = p.new_len[n];
+  r.live = r.held >= 0 && add >= 0;
+  if (!r.live) return r;
+  r.tokens = add;
+  r.lo = pages_of(r.held, p.page);
+  const int64_t hi = pages_of(r.held + add, p.page);
+  r.live = hi <= p.table_width && r.held + add <= INT32_MAX;
+  if (r.live) r.need = hi - r.lo;
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
+  __shared__ int64_t wave_sums[2][kThreads / kWave];
+  __shared__ int64_t token_end[kThreads], page_end[kThreads];   // inclusive sums within the slice
+  __shared__ int32_t held_of[kThreads], lo_of[kThreads];        // held -1: not served
+  __shared__ int flag;
+  const int tid = threadIdx.x, base = blockIdx.x * kThreads, part = blockIdx.y, parts = gridDim.y;
+  const int64_t count = min(max((int64_t)p.pool[0], (int64_t)0), p.capacity);
+  const int32_t* stack = p.pool + 2;
+  int64_t tokens0 = 0, pages0 = 0;
+  for (int n = tid; n < base; n += kThreads) {
+    const Request r = request_of(p, n);
+    tokens0 += r.tokens;
+    pages0 += r.need;
+  }
+  sum_pair(tokens0, pages0, wave_sums);
+  const int n = base + tid;
+  const Request r = request_of(p, n);
+  int64_t te = r.tokens, pe = r.need;
+  scan_pair(te, pe, wave_sums);
+  const bool served = r.live && pages0 + pe <= count && tokens0 + te <= p.T;
+  token_end[tid] = te;
+  page_end[tid] = pe;
+  held_of[tid] = served ? (int32_t)r.held : -1;
+  lo_of[tid] = (int32_t)r.lo;
+  if (part == 0 && n < p.N) {
+    p.cu[n + 1] = (int32_t)min(tokens0 + te, p.T);
+    p.cache_len[n] = served ? (int32_t)r.held : -1;
+    p.kv_len[n] = served ? (int32_t)(r.held + r.tokens) : -1;
+  }
+  if (part == 0 && base == 0 && tid == 0) p.cu[0] = 0;
+  __syncthreads();
+  // new pages, in order
+  const int64_t pages = page_end[kThreads - 1];
+  for (int64_t i = (int64_t)part * kThreads + tid; i < pages; i += (int64_t)parts * kThreads) {
+    const int k = find(page_end, i);
+    const int64_t at = pages0 + i;
+    if (held_of[k] < 0) continue;      // (served: all of its pages are on the stack)
+    const int64_t j = i - (k ? page_end[k - 1] : 0);
+    p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + j] = stack[count - 1 - at];
+  }
+  // tokens; the last slice also those behind the last request
+  const int64_t mine = token_end[kThreads - 1];
+  int64_t stop = min(tokens0 + mine, p.T);
+  if (blockIdx.x == gridDim.x - 1) stop = p.T;
+  for (int64_t t = tokens0 + (int64_t)part * kThreads + tid; t < stop; t += (int64_t)parts * kThreads) {
+    int64_t slot = -1;
+    int32_t position = -1, owner = -1;
+    const int64_t i = t - tokens0;
+    if (i < mine) {
+      const int k = find(token_end, i);
+      if (held_of[k] >= 0) {
+        const int64_t row = held_of[k] + i - (k ? token_end[k - 1] : 0);
+        const int64_t entry = row / p.page;
+        const int64_t id = entry >= lo_of[k] ? stack[count - 1 - (pages0 + (k ? page_end[k - 1] : 0) + entry - lo_of[k])]
+                                             : p.table[(int64_t)(base + k) * p.table_stride + entry];
+        if (id >= 0) slot = id * p.page + row % p.page;
+        owner = base + k;
+        position = p.start ? (int32_t)(p.start[owner] + (row - held_of[k])) : (int32_t)row;
+      }
+    }
+    if (p.slots) p.slots[t] = slot;
+    if (p.positions) p.positions[t] = position;
+    if (p.seq) p.seq[t] = owner;
+  }
+  if (!last_to_arrive(p.pool + 1, &flag)) return;
+  int64_t taken = 0, none = 0;
+  if (gridDim.x * gridDim.y > 1) {
+    for (int m = tid; m < p.N; m += kThreads) {
+      const int32_t a = load_agent(p.cache_len + m), b = load_agent(p.kv_len + m);
+      if (a >= 0) taken += pages_of(b, p.page) - pages_of(a, p.page);
+    }
+  } else {
+    taken = served ? r.need : 0;
+  }
+  sum_pair(taken, none, wave_sums);
+  if (tid == 0) p.pool[0] = (int32_t)(count - taken);
+}
+
+__device__ __forceinline__ int64_t given_back(const ReleasePagesLaunch& p, int n, int64_t& lo) {
+  lo = 0;
+  if (n >= p.N) return 0;
+  const int64_t keep = p.keep[n], held = p.held[n];
+  if (keep < 0 || held <= keep) return 0;
+  lo = pages_of(keep, p.page);
+  const int64_t hi = min(pages_of(held, p.page), (int64_t)p.table_width);
+  return hi > lo ? hi - lo : 0;
+}
+
+__global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p) {
+  __shared__ int64_t wave_sums[2][kThreads / kWave];
+  __shared__ int64_t page_end[kThreads];
+  __shared__ int32_t lo_of[kThreads];
+  __shared__ int flag;
+  const int tid = threadIdx.x, base = blockIdx.x * kThreads, part = blockIdx.y, parts = gridDim.y;
+  const int64_t count = min(max((int64_t)p.pool[0], (int64_t)0), p.capacity);
+  int32_t* stack = p.pool + 2;
+  int64_t before = 0, none = 0, lo;
+  for (int n = tid; n < base; n += kThreads) before += given_back(p, n, lo);
+  sum_pair(before, none, wave_sums);
+  int64_t pe = given_back(p, base + tid, lo);
+  scan_pair(pe, none, wave_sums);
+  page_end[tid] = pe;
+  lo_of[tid] = (int32_t)lo;
+  __syncthreads();
+  const int64_t pages = page_end[kThreads - 1];
+  for (int64_t i = (int64_t)part * kThreads + tid; i < pages; i += (int64_t)parts * kThreads) {
+    const int k = find(page_end, i);
+    const int64_t at = count + before + i;
+    if (at < p.capacity) stack[at] = p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + i - (k ? page_end[k - 1] : 0)];
+  }
+  if (!last_to_arrive(p.pool + 1, &flag)) return;
+  int64_t total = 0;
+  for (int m = tid; m < p.N; m += kThreads) total += given_back(p, m, lo);
+  none = 0;
+  sum_pair(total, none, wave_sums);
+  if (tid == 0) p.pool[0] = (int32_t)min(count + total, p.capacity);
+}
+
+int parts_of(int64_t items, int64_t slices) {
+  // 4096 tokens or pages a workgroup, on average over the slices
+  const int64_t want = (items / slices + 4095) / 4096;
+  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+}  // namespace
+
+hipError_t launch_plan_pages(const PlanPagesLaunch& p, hipStream_t stream) {
+  const int64_t slices = p.N > 0 ? (p.N + kThreads - 1) / kThreads : 1;
+  hipLaunchKernelGGL(plan_kernel, dim3((unsigned)slices, parts_of(p.T, slices)), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_release_pages(const ReleasePagesLaunch& p, hipStream_t stream) {
+  const int64_t slices = (p.N + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL(release_kernel, dim3((unsigned)slices, parts_of((int64_t)p.N * p.table_width, slices)), dim3(kThreads), 0,
+                     stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

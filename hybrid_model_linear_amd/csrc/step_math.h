@@ -1,0 +1,29 @@
+// Scalar functions of the step operators (selective scan, RMS norm), fp32, defined for
+// every input: infinities and NaN come out as the formulas have them.
+#pragma once
+#include "gdn_common.h"
+
+namespace gdn {
+
+// exp(x), x <= 0: 2^(x log2 e) with the product's rounding error and log2 e's own tail
+// carried along (an exponent of 20 rounded to 24 bits alone would cost 2^-20), on the
+// hardware's 2^x.  Below -104 the result is 0 in any case.
+__device__ __forceinline__ float step_exp_nonpos(float x) {
+  x = x < -104.0f ? -104.0f : x;   // (a NaN stays)
+  const float hi = x * 1.4426950408889634f;
+  const float lo = fmaf(x, 1.925963033500e-08f, fmaf(x, 1.4426950408889634f, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return fmaf(e, lo * 0.6931471805599453f, e);
+}
+// log(1 + exp(z))
+__device__ __forceinline__ float step_softplus(float z) {
+  return (z > 0.0f ? z : 0.0f) + gate_log1p_unit(step_exp_nonpos(-fabsf(z)));
+}
+// z / (1 + exp(-z))
+__device__ __forceinline__ float step_silu(float z) {
+  const float e = step_exp_nonpos(-fabsf(z));
+  const float r = gate_rcp(1.0f + e);
+  return z * (z >= 0.0f ? r : e * r);
+}
+
+}  // namespace gdn

@@ -45,7 +45,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 10
+#define GDN_ABI_VERSION 11
 
 typedef enum gdn_status {
   GDN_OK = 0,
@@ -58,7 +58,7 @@ typedef enum gdn_status {
   GDN_E_SCRATCH = 7      /* gdn_extend_noalloc: needs more than its static scratch */
 } gdn_status;
 
-typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 /* gdn_rms_norm outputs */ } gdn_dtype;
 
 enum { GDN_MODE_GDN = 0, GDN_MODE_SSD = 1 };
 
@@ -598,6 +598,189 @@ typedef struct gdn_kv_evict_args {
 } gdn_kv_evict_args;
 int gdn_kv_evict(const gdn_kv_evict_args* args, void* stream);
 int64_t gdn_kv_evict_workspace_size(const gdn_kv_evict_args* args);
+
+/* ---------------------------------------------------------------- selective scan
+ * The state space scan whose decay is a matrix (one per channel and state; the delta-off
+ * mode above has one decay per head).  Channel c, of group g = c / (D / G), has a state h
+ * of `states` values; token by token
+ *     delta = dt[t, c] + dt_bias[c], softplus'd when dt_softplus != 0
+ *     h[i]  = exp(delta A[c, i]) h[i] + delta x[t, c] B[t, g, i]
+ *     y     = sum_i C[t, g, i] h[i] + D_skip[c] x[t, c]
+ *     out[t, c] = z ? y z[t, c] sigmoid(z[t, c]) : y
+ * in fp32, rounded once (nearest even) to out_dtype.
+ *   x, dt, z, out : [T, D]; B, C : [T, G, states], groups contiguous; token strides of
+ *                   at least a row; aligned to their element.  x, dt, B, C, z: in_dtype
+ *   A             : fp32 [D, states], 16-byte aligned (the decay's factor itself, negative
+ *                   in such layers, not its logarithm)
+ *   D_skip, dt_bias : fp32 [D] or NULL (zero)
+ *   pool          : fp32 [num_slots, D, states], 16-byte aligned, read and written in place
+ * Supported: states in {8, 16, 32, 64, 128} (else GDN_E_UNSUPPORTED), D % G == 0, in_dtype
+ * and out_dtype bf16 or fp32.  out must not overlap x, dt, B, C, z or the pool (address
+ * ranges, else GDN_E_SHAPE).
+ *
+ * gdn_selective_scan: packed prompts.  cu_seqlens, slot, has_init (NULL = all 1), padding
+ * tokens, skipped and empty sequences as gdn_extend; keep_pool != 0 leaves the pool as it
+ * is.  max_seqlen is a host hint (an upper bound of the longest sequence, 0 = unknown): it
+ * changes the split over workgroups, never what is computed: long sequences in few
+ * workgroups are cut into segments, whose states a first launch prepares in a workspace of
+ * gdn_selective_scan_workspace_size bytes (0: no segments), 256-byte aligned, with any
+ * contents (calls in flight at once need their own); without one (NULL) there are none.
+ * A segment's start state is folded from those before it, which rounds differently.
+ * gdn_selective_update: one token per row (T = N), row b continues pool[slot[b]], negative
+ * slots as gdn_decode; cu_seqlens, has_init, max_seqlen, keep_pool, workspace ignored. */
+typedef struct gdn_selective_args {
+  int32_t in_dtype;
+  int32_t out_dtype;
+  int32_t N;             /* sequences (scan) or rows (update)    */
+  int32_t G;
+  int64_t T;
+  int64_t D;
+  int32_t states;
+  int32_t dt_softplus;
+  const void* x;
+  int64_t x_stride;
+  const void* dt;
+  int64_t dt_stride;
+  const void* B;
+  int64_t B_stride;
+  const void* C;
+  int64_t C_stride;
+  const void* z;             /* or NULL                          */
+  int64_t z_stride;
+  const float* A;
+  const float* D_skip;       /* [D] or NULL                      */
+  const float* dt_bias;      /* [D] or NULL                      */
+  const int32_t* cu_seqlens; /* [N + 1]                          */
+  const int32_t* slot;       /* [N]                              */
+  const int32_t* has_init;   /* [N] or NULL                      */
+  float* pool;
+  int64_t num_slots;
+  void* out;
+  int64_t out_stride;
+  int32_t max_seqlen;
+  int32_t keep_pool;
+  void* workspace;
+  int64_t workspace_bytes;
+} gdn_selective_args;
+int gdn_selective_scan(const gdn_selective_args* args, void* stream);
+/* Workspace bytes with which a gdn_selective_scan call with these arguments cuts its
+ * sequences, or minus the gdn_status of a call that would be refused. */
+int64_t gdn_selective_scan_workspace_size(const gdn_selective_args* args);
+int gdn_selective_update(const gdn_selective_args* args, void* stream);
+
+/* ---------------------------------------------------------------- root-mean-square norm
+ * The norm in front of a layer (with the residual's addition) and behind a linear-attention
+ * layer (per head, gated), with an output that the next matrix product takes in 8 bits.
+ * A token's row is H parts of d values, each normalised by itself:
+ *     u = x;  residual: u = x + residual, and residual becomes u (rounded to its type);
+ *     gate and gate_first: u = x g sigmoid(g)
+ *     y = u / sqrt(mean(u^2) + eps) (weight + offset);  gate and not gate_first: y g sigmoid(g)
+ * in fp32, from the sum before its rounding.  weight [d] is shared by the H parts (NULL: y
+ * without it and offset).  out: bf16 or fp32, or e4m3 codes with y = code * scale:
+ * scale[t, k] belongs to the k-th `group` values of the token's H d (the last group may be
+ * shorter; group 0: the whole row) and is max |y| / 448, at least 2^-64; a code is y / scale
+ * rounded to nearest even.  Values that are not finite do not count for the scale, and are
+ * stored as NaN.
+ *   x, gate : in_dtype [T, H, d]; residual : bf16 or fp32 [T, H, d]; out [T, H, d]; a row's
+ *   H d values contiguous, token strides of at least H d; aligned to their element
+ *   scale : fp32 [T, ceil(H d / group)], contiguous (e4m3 only, else ignored)
+ * Supported: bf16 or fp32 x, weight and residual; group 0, 64 or 128 (else
+ * GDN_E_UNSUPPORTED); H at most 8192, H d at most 2^20; not both a gate and a residual (GDN_E_UNSUPPORTED).
+ * out, scale and residual must not overlap each other or an input (address ranges, else
+ * GDN_E_SHAPE).  One launch. */
+typedef struct gdn_rms_norm_args {
+  int32_t in_dtype;
+  int32_t out_dtype;         /* GDN_F32, GDN_BF16 or GDN_E4M3    */
+  int32_t weight_dtype;
+  int32_t residual_dtype;
+  int64_t T;
+  int32_t H, d;
+  const void* x;
+  int64_t x_stride;
+  const void* gate;          /* or NULL                          */
+  int64_t gate_stride;
+  void* residual;            /* or NULL                          */
+  int64_t residual_stride;
+  const void* weight;        /* [d] or NULL                      */
+  void* out;
+  int64_t out_stride;
+  float* scale;              /* e4m3 only                        */
+  float eps, offset;
+  int32_t gate_first;
+  int32_t group;
+} gdn_rms_norm_args;
+int gdn_rms_norm(const gdn_rms_norm_args* args, void* stream);
+
+/* ---------------------------------------------------------------- pages of a step
+ * The lengths, block-table entries and slot maps that a step's other calls read, formed on
+ * the GPU from the requests' lengths: a program whose lengths live there (sampled ends,
+ * accepted drafts, replayed graphs) needs no copy to the host.  The free pages are a
+ * stack in device memory:
+ *   pool : int32 [2 + capacity]: the number of free pages, 0 (the library's own), and the
+ *          stack, whose top is pool[1 + pool[0]]
+ * (With `page` larger than any sequence the same calls hand out state slots, one each.)
+ *
+ * gdn_plan_pages: request n holds held[n] rows and brings new_len[n] tokens.  It takes the
+ * pages ceil(held / page) .. ceil((held + new) / page) - 1 of its row of block_table from
+ * the top of the stack, requests and pages in order.  A request is served when
+ *   - held[n] >= 0 and new_len[n] >= 0 (otherwise it is a padding row without tokens),
+ *   - its table has room for held + new rows, fewer than 2^31 (otherwise it takes no page), and
+ *   - the pages and the tokens up to its end fit into the stack and into T (so that from the
+ *     first request that does not fit on none is served).
+ * Outputs, all written whole:
+ *   cu_seqlens [N + 1] : tokens before each request, served or not, at most T
+ *   cache_len [N]      : held[n], or -1 where the request is not served
+ *   kv_len [N]         : held[n] + new_len[n], or -1
+ *   slots, positions, seq [T] : of a served request's i-th token, with row r = held + i:
+ *     page id * page + r % page (-1 where the table holds a negative id), start[n] + i
+ *     (start NULL: r), and n; -1 for every other token.  Each may be NULL.
+ * Entries of block_table that no new page takes are left as they are.  Page ids are handed
+ * out as they stand on the stack; a number of free pages outside [0, capacity] counts as the
+ * nearer end.  N at most 65535, 1 <= page <= 2^30, T below 2^31.
+ *
+ * gdn_release_pages: request n keeps its first keep[n] rows of held[n]: the pages
+ * ceil(keep / page) .. ceil(held / page) - 1 of its table go back on the stack, requests and
+ * pages in order, as far as `capacity` goes; keep[n] < 0 or held[n] <= keep[n]: none.  Table
+ * entries are left as they are.
+ *
+ * Every output must be apart from every input and output (address ranges, else
+ * GDN_E_SHAPE), but for block_table and pool, which are both.  Calls on one pool are
+ * ordered by the caller.  One launch each. */
+typedef struct gdn_plan_pages_args {
+  int32_t* pool;
+  int64_t capacity;
+  int32_t N;
+  int32_t page;
+  int64_t T;
+  const int32_t* held;       /* [N]                              */
+  const int32_t* new_len;    /* [N]                              */
+  const int32_t* start;      /* [N] or NULL                      */
+  int32_t* block_table;      /* [N, table_width]                 */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t _pad0;
+  int32_t* cu_seqlens;       /* [N + 1]                          */
+  int32_t* cache_len;        /* [N]                              */
+  int32_t* kv_len;           /* [N]                              */
+  int64_t* slots;            /* [T] or NULL                      */
+  int32_t* positions;        /* [T] or NULL                      */
+  int32_t* seq;              /* [T] or NULL                      */
+} gdn_plan_pages_args;
+int gdn_plan_pages(const gdn_plan_pages_args* args, void* stream);
+
+typedef struct gdn_release_pages_args {
+  int32_t* pool;
+  int64_t capacity;
+  int32_t N;
+  int32_t page;
+  const int32_t* keep;       /* [N]                              */
+  const int32_t* held;       /* [N]                              */
+  const int32_t* block_table;
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t _pad0;
+} gdn_release_pages_args;
+int gdn_release_pages(const gdn_release_pages_args* args, void* stream);
 
 /* Device-side check of slot[0..n): *flag (device int32) receives 0 when every
  * non-negative slot is < num_slots and no non-negative slot repeats, 1 when one

@@ -25,7 +25,8 @@ The delta-off mode follows the parameter list of the flashinfer page
 dt_limit, initial_states, return_final_states).
 
 oracle.attention holds the softmax-attention operators over the paged 8-bit cache,
-pinned by tests/test_oracle_attention.py.
+pinned by tests/test_oracle_attention.py; oracle.step the selective scan, the RMS norm and
+the pages of a step, pinned by tests/test_oracle_step.py.
 
 Parity pins: every function here is pinned by tests in tests/test_oracle_pins.py
 (closed forms, brute force, exact rational arithmetic, invariants).  No function
@@ -34,8 +35,8 @@ is "parity unpinned".
 from .gdn import (softplus, sigmoid, gdn_gate, ssd_gate, l2_normalize, gdn_extend,
                   gdn_decode, apply_final_states, ssd_combined, causal_conv1d)
 
-from . import attention
+from . import attention, step
 
 __all__ = ["softplus", "sigmoid", "gdn_gate", "ssd_gate", "l2_normalize", "gdn_extend",
            "gdn_decode", "apply_final_states", "ssd_combined", "causal_conv1d",
-           "attention"]
+           "attention", "step"]
