@@ -1,9 +1,19 @@
 // Selective state space scan: packed prompts (gdn_selective_scan) and one token per row
 // (gdn_selective_update).  Per channel c with states h[i]:
 //   h[i] = exp(delta A[c, i]) h[i] + delta x B[i],   y = sum_i C[i] h[i] + D_skip[c] x
-// A thread walks one channel with its states in registers.
+//
+// The scan's bound is vector arithmetic: per token, channel and state a product, an
+// exponential (the time of two to three other instructions here), a product and two fused
+// ones, ~25 cycles of a SIMD for 64 of them, where the bytes of a token and channel are 8
+// (16 states: 0.41 ms of instructions to 0.19 ms of memory at 32768 tokens x 4096 channels).
+// A lane is a channel, the states are dealt out over the 4 or 8 waves of a workgroup: so
+// each wave reads B and C of its states as broadcasts, whole rows of x, dt, z are read and
+// written, and what there is once per token and channel (softplus, gate, conversions) is
+// dealt out over the waves by tokens.  Through LDS go delta and delta x to all waves and each
+// wave's part of y back; two buffers of each, so that a tile of tokens costs one barrier.
 #include "step_launch.h"
 #include "step_math.h"
+#include "tile_ops.h"
 
 namespace gdn {
 
@@ -25,67 +35,237 @@ TokenIn<In> token_in(const SelectiveLaunch& p) {
           p.z_stride};
 }
 
-// Channel of this thread: workgroups do not cross groups.
+int64_t channel_blocks(const SelectiveLaunch& p) { return (p.D / p.G + kBlock - 1) / kBlock * p.G; }
+
+// Channel of this lane: workgroups do not cross groups.
 __device__ __forceinline__ bool channel_of(const SelectiveLaunch& p, int blk, int64_t& c, int& g) {
   const int64_t dg = p.D / p.G;
   const int per = (int)((dg + kBlock - 1) / kBlock);
   g = blk / per;
-  const int64_t in = (int64_t)(blk % per) * kBlock + threadIdx.x;
-  c = g * dg + in;
+  const int64_t in = (int64_t)(blk % per) * kBlock + threadIdx.x % kBlock;
+  c = g * dg + (in < dg ? in : dg - 1);
   return in < dg;
 }
 
-// One token of one channel: h is updated, y returned.
-template <typename In, int NS>
-__device__ __forceinline__ float token_step(const SelectiveLaunch& p, const TokenIn<In>& in, int64_t t, int64_t c, int g,
-                                            const float* A, float bias, float skip, float (&h)[NS]) {
-  const float x = Elem<In>::load(in.x, t * in.x_stride + c);
-  float delta = Elem<In>::load(in.dt, t * in.dt_stride + c) + bias;
-  if (p.softplus_on) delta = step_softplus(delta);
-  const float dx = delta * x;
-  float y = skip * x;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const float b = Elem<In>::load(in.B, t * in.B_stride + (int64_t)g * NS + i);
-    const float cc = Elem<In>::load(in.C, t * in.C_stride + (int64_t)g * NS + i);
-    h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(delta * (A[i] * kLog2e)), dx * b);
-    y = fmaf(cc, h[i], y);
+// ------------------------------------------------------------------ scan
+// Waves that the states are dealt out over, and tokens of a tile.
+template <int NS> constexpr int kWaves = NS <= 32 ? 4 : 8;
+template <int NS> constexpr int kTile = NS <= 32 ? 16 : 8;
+
+enum Pass {
+  kWhole,      // a workgroup walks a sequence
+  kStates,     // ... a segment, for its last state (from zeros; the first one from the sequence's start) and its sum of delta
+  kSegment     // ... a segment, from the state that the segments before it leave
+};
+
+template <typename In, typename Out, int NS, int kPass>
+__global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
+  constexpr int NW = kWaves<NS>, SPL = NS / NW, TT = kTile<NS>, TW = TT / NW;
+  constexpr int kOut = kPass != kStates;                    // y is formed
+  constexpr int kBC = kOut ? 2 : 1;                         // B, or B and C
+  constexpr int kValues = TT * kBC * NS, kFill = (kValues + NW * kWave - 1) / (NW * kWave);   // of a tile; of a thread
+  static_assert(TT % NW == 0 && NS % NW == 0, "tiles divide evenly");
+  __shared__ __attribute__((aligned(16))) float2 steps[2][TT][kBlock];           // delta, delta x
+  __shared__ __attribute__((aligned(16))) float bc[2][TT][NW][kBC][SPL];
+  __shared__ float part[kOut ? 2 : 1][kOut ? TT : 1][kOut ? NW : 1][kBlock];     // each wave's part of y
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int blk = blockIdx.x % blocks, rest = blockIdx.x / blocks;
+  const int cuts = kPass == kWhole ? 1 : kPass == kStates ? p.segs - 1 : p.segs;
+  const int n = rest / cuts, seg = rest % cuts;
+  int64_t c;
+  int g;
+  const bool mine = channel_of(p, blk, c, g);
+  const int32_t slot = p.slot[n];
+  if (slot < 0) return;
+  int64_t first = p.cu[n], end = p.cu[n + 1];
+  bool last = true;
+  if constexpr (kPass != kWhole) {
+    first += seg * p.seg_len;
+    if (seg > 0 && first >= end) return;
+    last = seg == p.segs - 1 || first + p.seg_len >= end;
+    if (!last) end = first + p.seg_len;
   }
-  if (in.z) y *= step_silu(Elem<In>::load(in.z, t * in.z_stride + c));
-  return y;
+  const int64_t at = c * NS + wave * SPL;                   // this lane's states in an [D, states] matrix
+  const int64_t seg_row = ((int64_t)n * p.segs + seg) * p.D;
+  float* state = p.pool + (int64_t)slot * p.D * NS + at;
+  const bool init = !p.has_init || p.has_init[n] != 0;
+  float A[SPL], h[SPL];
+#pragma unroll
+  for (int i = 0; i < SPL; ++i) A[i] = p.A[at + i] * kLog2e;
+  if constexpr (kPass == kSegment) {
+    // The first segment's start state stands in the row that no segment's last state takes
+    // (the pool's slot is written by this launch).
+    const float* from = p.seg_state + (seg_row - (int64_t)seg * p.D) * NS + at;
+    const float* sums = p.seg_delta + (seg_row - (int64_t)seg * p.D) + c;
+    const int64_t row = p.D * NS;
+    if (seg == 0) from += (p.segs - 1) * row;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) h[i] = from[i];
+    for (int s = 1; s < seg; ++s) {
+      const float sum = sums[s * p.D];
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(sum * A[i]), from[s * row + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) h[i] = init && seg == 0 ? state[i] : 0.0f;
+    if constexpr (kPass == kStates) {
+      if (seg == 0 && mine)
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) p.seg_state[(seg_row + (int64_t)(p.segs - 1) * p.D) * NS + at + i] = h[i];
+    }
+  }
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
+
+  // A tile's operands in registers: of TW tokens (this wave's share), and of B and C.  Rows past
+  // the end are read as the last one and count as zeros.
+  float rx[TW], rdt[TW], rz[TW], rbc[kFill];
+  auto fetch = [&](int64_t t0) {
+#pragma unroll
+    for (int q = 0; q < TW; ++q) {
+      const int64_t t = min(t0 + wave * TW + q, end - 1);
+      rx[q] = Elem<In>::load(in.x + t * in.x_stride, c);
+      rdt[q] = Elem<In>::load(in.dt + t * in.dt_stride, c);
+      if (kOut && in.z) rz[q] = Elem<In>::load(in.z + t * in.z_stride, c);
+    }
+#pragma unroll
+    for (int k = 0; k < kFill; ++k) {
+      const int e = k * NW * kWave + threadIdx.x, i = e % (kBC * NS);
+      if (kValues % (NW * kWave) != 0 && e >= kValues) break;
+      const int64_t t = min(t0 + e / (kBC * NS), end - 1);
+      rbc[k] = i < NS ? Elem<In>::load(in.B + t * in.B_stride, g * NS + i)
+                      : Elem<In>::load(in.C + t * in.C_stride, g * NS + i - NS);
+    }
+  };
+  // Their part that is the same for all states, into LDS.
+  auto stage = [&](int64_t t0, int buf) {
+#pragma unroll
+    for (int q = 0; q < TW; ++q) {
+      const int k = wave * TW + q;
+      float delta = rdt[q] + bias;
+      if (p.softplus_on) delta = step_softplus(delta);
+      const bool live = t0 + k < end;
+      steps[buf][k][lane] = make_float2(live ? delta : 0.0f, live ? delta * rx[q] : 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < kFill; ++k) {
+      const int e = k * NW * kWave + threadIdx.x, i = e % (kBC * NS), t = e / (kBC * NS), s = i % NS;
+      if (kValues % (NW * kWave) != 0 && e >= kValues) break;
+      bc[buf][t][s / SPL][i / NS][s % SPL] = t0 + t < end ? rbc[k] : 0.0f;
+    }
+  };
+  float sum = 0.0f;                                          // of delta (kStates)
+  float x[TW], z[TW];                                        // of the tile being walked
+  if (first < end) {
+    fetch(first);
+    stage(first, 0);
+  }
+#pragma unroll
+  for (int q = 0; q < TW; ++q) { x[q] = rx[q]; z[q] = rz[q]; }
+  if (first < end) fetch(first + TT);
+  lds_sync();
+  int buf = 0;
+  for (int64_t t0 = first; t0 < end; t0 += TT, buf ^= 1) {
+#pragma unroll
+    for (int k = 0; k < TT; ++k) {
+      const float2 d = steps[buf][k][lane];
+      float y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) {
+        h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(d.x * A[i]), d.y * bc[buf][k][wave][0][i]);
+        if constexpr (kOut) y = fmaf(bc[buf][k][wave][kBC - 1][i], h[i], y);
+      }
+      if constexpr (kOut) part[buf][k][wave][lane] = y;
+      else sum += d.x;
+    }
+    // the next tile: staged behind this one, its successor fetched
+    const int64_t next = t0 + TT;
+    float nx[TW], nz[TW];
+    if (next < end) stage(next, buf ^ 1);
+#pragma unroll
+    for (int q = 0; q < TW; ++q) { nx[q] = rx[q]; nz[q] = rz[q]; }
+    if (next < end) fetch(next + TT);
+    lds_sync();
+    if constexpr (kOut) {
+#pragma unroll
+      for (int q = 0; q < TW; ++q) {
+        const int k = wave * TW + q;
+        float y = skip * x[q];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) y += part[buf][k][w][lane];
+        if (in.z) y *= step_silu(z[q]);
+        if (t0 + k < end && mine) Elem<Out>::store(static_cast<Out*>(p.out) + (t0 + k) * p.out_stride, c, y);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < TW; ++q) { x[q] = nx[q]; z[q] = nz[q]; }
+  }
+  if (!mine) return;
+  if constexpr (kPass == kStates) {
+    float* to = p.seg_state + seg_row * NS + at;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) to[i] = h[i];
+    if (wave == 0) p.seg_delta[seg_row + c] = sum;
+  } else if (last && !p.keep_pool) {
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) state[i] = h[i];
+  }
 }
 
-template <typename In, typename Out, int NS, bool kUpdate>
-__global__ void __launch_bounds__(kBlock) selective_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
+template <typename In, typename Out, int NS>
+void launch_scan(const SelectiveLaunch& p, hipStream_t stream) {
+  const int64_t blocks = channel_blocks(p);
+  const dim3 block(kWaves<NS> * kWave);
+  const TokenIn<In> in = token_in<In>(p);
+  auto grid = [&](int cuts) { return dim3((unsigned)(blocks * p.N * cuts)); };
+  if (p.segs == 1) {
+    hipLaunchKernelGGL((scan_kernel<In, Out, NS, kWhole>), grid(1), block, 0, stream, p, in, (int)blocks);
+    return;
+  }
+  hipLaunchKernelGGL((scan_kernel<In, Out, NS, kStates>), grid(p.segs - 1), block, 0, stream, p, in, (int)blocks);
+  hipLaunchKernelGGL((scan_kernel<In, Out, NS, kSegment>), grid(p.segs), block, 0, stream, p, in, (int)blocks);
+}
+
+// ------------------------------------------------------------------ update
+// One token: a thread takes a channel with its states in registers.
+template <typename In, typename Out, int NS>
+__global__ void __launch_bounds__(kBlock) update_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
   const int n = blockIdx.x / blocks;
   int64_t c;
   int g;
   if (!channel_of(p, blockIdx.x % blocks, c, g)) return;
   const int32_t slot = p.slot[n];
   if (slot < 0) return;
-  const int64_t first = kUpdate ? n : p.cu[n], end = kUpdate ? n + 1 : p.cu[n + 1];
   const float* A = p.A + c * NS;
   float* state = p.pool + ((int64_t)slot * p.D + c) * NS;
-  const bool init = kUpdate || !p.has_init || p.has_init[n] != 0;
-  float h[NS];
+  const float x = Elem<In>::load(in.x, n * in.x_stride + c);
+  float delta = Elem<In>::load(in.dt, n * in.dt_stride + c) + (p.dt_bias ? p.dt_bias[c] : 0.0f);
+  if (p.softplus_on) delta = step_softplus(delta);
+  const float dx = delta * x;
+  float y = p.D_skip ? p.D_skip[c] * x : 0.0f;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) h[i] = init ? state[i] : 0.0f;
-  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
-  for (int64_t t = first; t < end; ++t)
-    Elem<Out>::store(static_cast<Out*>(p.out), t * p.out_stride + c, token_step<In, NS>(p, in, t, c, g, A, bias, skip, h));
-  if (!kUpdate && p.keep_pool) return;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) state[i] = h[i];
+  for (int i = 0; i < NS; ++i) {
+    const float b = Elem<In>::load(in.B, n * in.B_stride + (int64_t)g * NS + i);
+    const float cc = Elem<In>::load(in.C, n * in.C_stride + (int64_t)g * NS + i);
+    const float h = fmaf(state[i], __builtin_amdgcn_exp2f(delta * (A[i] * kLog2e)), dx * b);
+    state[i] = h;
+    y = fmaf(cc, h, y);
+  }
+  if (in.z) y *= step_silu(Elem<In>::load(in.z, n * in.z_stride + c));
+  Elem<Out>::store(static_cast<Out*>(p.out), n * p.out_stride + c, y);
 }
 
-template <typename In, typename Out, bool kUpdate>
-void launch(const SelectiveLaunch& p, hipStream_t stream) {
-  const int64_t dg = p.D / p.G;
-  const int blocks = (int)((dg + kBlock - 1) / kBlock * p.G);
-  const dim3 grid((unsigned)(blocks * (int64_t)p.N)), block(kBlock);
-  const TokenIn<In> in = token_in<In>(p);
+template <typename In, typename Out, int NS>
+void launch_update(const SelectiveLaunch& p, hipStream_t stream) {
+  const int64_t blocks = channel_blocks(p);
+  hipLaunchKernelGGL((update_kernel<In, Out, NS>), dim3((unsigned)(blocks * p.N)), dim3(kBlock), 0, stream, p, token_in<In>(p),
+                     (int)blocks);
+}
+
+template <typename In, typename Out>
+void launch_states(const SelectiveLaunch& p, bool update, hipStream_t stream) {
 #define SELECTIVE(NS) \
-  case NS: hipLaunchKernelGGL((selective_kernel<In, Out, NS, kUpdate>), grid, block, 0, stream, p, in, blocks); break
+  case NS: if (update) launch_update<In, Out, NS>(p, stream); else launch_scan<In, Out, NS>(p, stream); break
   switch (p.states) {
     SELECTIVE(8);
     SELECTIVE(16);
@@ -96,19 +276,35 @@ void launch(const SelectiveLaunch& p, hipStream_t stream) {
 #undef SELECTIVE
 }
 
-template <bool kUpdate>
-hipError_t launch_types(const SelectiveLaunch& p, hipStream_t stream) {
+hipError_t launch_types(const SelectiveLaunch& p, bool update, hipStream_t stream) {
   if (p.in_bf16) {
-    if (p.out_bf16) launch<u16, u16, kUpdate>(p, stream); else launch<u16, float, kUpdate>(p, stream);
+    if (p.out_bf16) launch_states<u16, u16>(p, update, stream); else launch_states<u16, float>(p, update, stream);
   } else {
-    if (p.out_bf16) launch<float, u16, kUpdate>(p, stream); else launch<float, float, kUpdate>(p, stream);
+    if (p.out_bf16) launch_states<float, u16>(p, update, stream); else launch_states<float, float>(p, update, stream);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_selective_scan(const SelectiveLaunch& p, hipStream_t stream) { return launch_types<false>(p, stream); }
-hipError_t launch_selective_update(const SelectiveLaunch& p, hipStream_t stream) { return launch_types<true>(p, stream); }
+void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus) {
+  // Cutting costs nearly twice the arithmetic (the states are formed twice), so it pays where
+  // the uncut launch leaves the chip mostly empty.
+  p.segs = 1;
+  p.seg_len = longest;
+  const int64_t wgs = channel_blocks(p) * p.N;
+  const int waves = p.states <= 32 ? 4 : 8;
+  const int64_t places = (int64_t)cus * 16 / waves;     // four waves a SIMD
+  if (wgs * 4 > places || longest < 256) return;
+  int64_t segs = places / wgs;
+  if (segs > (longest + 127) / 128) segs = (longest + 127) / 128;
+  if (segs > 64) segs = 64;
+  if (segs < 2) return;
+  p.seg_len = ((longest + segs - 1) / segs + 15) / 16 * 16;
+  p.segs = (int)((longest + p.seg_len - 1) / p.seg_len);
+}
+
+hipError_t launch_selective_scan(const SelectiveLaunch& p, hipStream_t stream) { return launch_types(p, false, stream); }
+hipError_t launch_selective_update(const SelectiveLaunch& p, hipStream_t stream) { return launch_types(p, true, stream); }
 
 }  // namespace gdn

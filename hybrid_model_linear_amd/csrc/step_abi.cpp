@@ -35,7 +35,9 @@ bool rows_ok(const void* p, int64_t n, int64_t stride, int64_t width, int64_t si
   return aligned(p, size) && stride >= width && stride <= (int64_t)1 << 40 && n <= INT32_MAX;
 }
 
-int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunch& p) {
+// Descriptor of a scan or update; need receives the workspace bytes with which a scan's sequences are cut.
+int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunch& p, int64_t& need) {
+  need = 0;
   if (!a) return GDN_E_NULL;
   if (!float_type(a->in_dtype) || !float_type(a->out_dtype)) return GDN_E_DTYPE;
   if (a->N < 0 || a->T < 0 || a->T > INT32_MAX || a->G <= 0 || a->D <= 0 || a->D > 1 << 24 || a->D % a->G != 0 ||
@@ -89,6 +91,14 @@ int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunc
   p.out = a->out;
   p.out_stride = a->out_stride;
   p.keep_pool = a->keep_pool != 0;
+  p.segs = 1;
+  if (update || a->N == 0) return GDN_OK;
+  gdn::plan_selective_scan(p, a->max_seqlen > 0 && a->max_seqlen < a->T ? a->max_seqlen : a->T, gdn::current_device_cus());
+  if (p.segs == 1) return GDN_OK;
+  const int64_t rows = (int64_t)a->N * p.segs * a->D, states = rows * a->states * 4;   // (a multiple of 32 bytes)
+  p.seg_state = static_cast<float*>(a->workspace);
+  p.seg_delta = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(a->workspace) + states);
+  need = states + rows * 4;
   return GDN_OK;
 }
 
@@ -160,20 +170,25 @@ extern "C" {
 
 int64_t gdn_selective_scan_workspace_size(const gdn_selective_args* a) {
   gdn::SelectiveLaunch p{};
-  const int st = plan_selective(a, false, p);
-  return st == GDN_OK ? 0 : -(int64_t)st;
+  int64_t need = 0;
+  const int st = plan_selective(a, false, p, need);
+  return st == GDN_OK ? need : -(int64_t)st;
 }
 
 int gdn_selective_scan(const gdn_selective_args* a, void* stream) {
   gdn::SelectiveLaunch p{};
-  const int st = plan_selective(a, false, p);
+  int64_t need = 0;
+  const int st = plan_selective(a, false, p, need);
   if (st != GDN_OK || a->N == 0) return st;
+  if (!a->workspace) p.segs = 1;
+  else if (need > 0 && (a->workspace_bytes < need || !aligned(a->workspace, 256))) return GDN_E_SHAPE;
   return gdn::status_of_hip(gdn::launch_selective_scan(p, (hipStream_t)stream));
 }
 
 int gdn_selective_update(const gdn_selective_args* a, void* stream) {
   gdn::SelectiveLaunch p{};
-  const int st = plan_selective(a, true, p);
+  int64_t need = 0;
+  const int st = plan_selective(a, true, p, need);
   if (st != GDN_OK || a->N == 0) return st;
   return gdn::status_of_hip(gdn::launch_selective_update(p, (hipStream_t)stream));
 }

@@ -36,7 +36,15 @@ struct SelectiveLaunch {
   void* out;
   int64_t out_stride;
   int keep_pool;
+  // Sequences cut into segments of seg_len tokens, the last of `segs` taking the rest; segs 1: not cut.
+  int segs;
+  int64_t seg_len;
+  float* seg_state;           // [N, segs, D, states]
+  float* seg_delta;           // [N, segs, D]
 };
+
+// Segments of a scan on a card of this many CUs: segs and seg_len.
+void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus);
 
 struct NormLaunch {
   int64_t T;
@@ -96,5 +104,6 @@ hipError_t launch_plan_pages(const PlanPagesLaunch& p, hipStream_t stream);
 hipError_t launch_release_pages(const ReleasePagesLaunch& p, hipStream_t stream);
 
 int status_of_hip(hipError_t e);
+int current_device_cus();
 
 }  // namespace gdn
