@@ -117,55 +117,68 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   }
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
 
-  // A tile's operands in registers: of TW tokens (this wave's share), and of B and C.  Rows past
-  // the end are read as the last one and count as zeros.
-  float rx[TW], rdt[TW], rz[TW], rbc[kFill];
-  auto fetch = [&](int64_t t0) {
+  // A tile's operands in registers: of TW tokens (this wave's share), and of B and C.  Whole tiles
+  // are fetched one ahead, straight into the registers that the next turn reads (a branch around
+  // the loads, or a conversion behind them, would wait for them here); without z its loads read x.
+  In rx[TW], rdt[TW], rz[TW], rbc[kFill];
+  const uint32_t at_c = (uint32_t)c * sizeof(In), at_out = (uint32_t)c * sizeof(Out);
+  const int64_t row0 = first + wave * TW;
+  const In *x_at = in.x + row0 * in.x_stride, *dt_at = in.dt + row0 * in.dt_stride;
+  const int64_t z_stride = in.z ? in.z_stride : in.x_stride;
+  const In* z_at = in.z ? in.z + row0 * z_stride : x_at;
+  Out* out_at = static_cast<Out*>(p.out) + row0 * p.out_stride;
+  auto of = [&](const In* row) { return *reinterpret_cast<const In*>(reinterpret_cast<const char*>(row) + at_c); };
+  const In* bc_at[kFill];                                   // this thread's values of B and C
+  int64_t bc_step[kFill];
+  int bc_token[kFill], bc_to[kFill];                        // their token of the tile; their place in LDS
+#pragma unroll
+  for (int k = 0; k < kFill; ++k) {
+    const int e = k * NW * kWave + threadIdx.x, i = e % (kBC * NS), s = i % NS;
+    bc_token[k] = e / (kBC * NS);                           // (past the tile: read as its first, not written)
+    const int64_t stride = i < NS ? in.B_stride : in.C_stride;
+    bc_at[k] = (i < NS ? in.B : in.C) + (first + (bc_token[k] < TT ? bc_token[k] : 0)) * stride + (int64_t)g * NS + s;
+    bc_to[k] = ((bc_token[k] * NW + s / SPL) * kBC + i / NS) * SPL + s % SPL;
+    bc_step[k] = TT * stride;
+  }
+  auto fetch = [&]() {
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
-      const int64_t t = min(t0 + wave * TW + q, end - 1);
-      rx[q] = Elem<In>::load(in.x + t * in.x_stride, c);
-      rdt[q] = Elem<In>::load(in.dt + t * in.dt_stride, c);
-      if (kOut && in.z) rz[q] = Elem<In>::load(in.z + t * in.z_stride, c);
+      rx[q] = of(x_at + q * in.x_stride);
+      rdt[q] = of(dt_at + q * in.dt_stride);
+      if (kOut) rz[q] = of(z_at + q * z_stride);
     }
 #pragma unroll
-    for (int k = 0; k < kFill; ++k) {
-      const int e = k * NW * kWave + threadIdx.x, i = e % (kBC * NS);
-      if (kValues % (NW * kWave) != 0 && e >= kValues) break;
-      const int64_t t = min(t0 + e / (kBC * NS), end - 1);
-      rbc[k] = i < NS ? Elem<In>::load(in.B + t * in.B_stride, g * NS + i)
-                      : Elem<In>::load(in.C + t * in.C_stride, g * NS + i - NS);
-    }
+    for (int k = 0; k < kFill; ++k) rbc[k] = *bc_at[k];
   };
-  // Their part that is the same for all states, into LDS.
-  auto stage = [&](int64_t t0, int buf) {
+  auto advance = [&](bool on) {
+    x_at += on ? TT * in.x_stride : 0;
+    dt_at += on ? TT * in.dt_stride : 0;
+    z_at += on ? TT * z_stride : 0;
+#pragma unroll
+    for (int k = 0; k < kFill; ++k) bc_at[k] += on ? bc_step[k] : 0;
+  };
+  // Their part that is the same for all states, into LDS; tokens from `left` on count as zeros.
+  auto stage = [&](int buf, int left) {
+    float delta[TW];
+#pragma unroll
+    for (int q = 0; q < TW; ++q) delta[q] = Elem<In>::load(&rdt[q], 0) + bias;
+    if (p.softplus_on) {
+#pragma unroll
+      for (int q = 0; q < TW; ++q) delta[q] = step_softplus(delta[q]);
+    }
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
       const int k = wave * TW + q;
-      float delta = rdt[q] + bias;
-      if (p.softplus_on) delta = step_softplus(delta);
-      const bool live = t0 + k < end;
-      steps[buf][k][lane] = make_float2(live ? delta : 0.0f, live ? delta * rx[q] : 0.0f);
+      const bool live = k < left;
+      steps[buf][k][lane] = make_float2(live ? delta[q] : 0.0f, live ? delta[q] * Elem<In>::load(&rx[q], 0) : 0.0f);
     }
+    float* to = &bc[buf][0][0][0][0];
 #pragma unroll
-    for (int k = 0; k < kFill; ++k) {
-      const int e = k * NW * kWave + threadIdx.x, i = e % (kBC * NS), t = e / (kBC * NS), s = i % NS;
-      if (kValues % (NW * kWave) != 0 && e >= kValues) break;
-      bc[buf][t][s / SPL][i / NS][s % SPL] = t0 + t < end ? rbc[k] : 0.0f;
-    }
+    for (int k = 0; k < kFill; ++k)
+      if (kValues % (NW * kWave) == 0 || bc_token[k] < TT) to[bc_to[k]] = bc_token[k] < left ? Elem<In>::load(&rbc[k], 0) : 0.0f;
   };
   float sum = 0.0f;                                          // of delta (kStates)
-  float x[TW], z[TW];                                        // of the tile being walked
-  if (first < end) {
-    fetch(first);
-    stage(first, 0);
-  }
-#pragma unroll
-  for (int q = 0; q < TW; ++q) { x[q] = rx[q]; z[q] = rz[q]; }
-  if (first < end) fetch(first + TT);
-  lds_sync();
-  int buf = 0;
-  for (int64_t t0 = first; t0 < end; t0 += TT, buf ^= 1) {
+  auto walk = [&](int buf) {
 #pragma unroll
     for (int k = 0; k < TT; ++k) {
       const float2 d = steps[buf][k][lane];
@@ -178,27 +191,74 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
       if constexpr (kOut) part[buf][k][wave][lane] = y;
       else sum += d.x;
     }
-    // the next tile: staged behind this one, its successor fetched
-    const int64_t next = t0 + TT;
-    float nx[TW], nz[TW];
-    if (next < end) stage(next, buf ^ 1);
+  };
+  In x[TW], z[TW];                                           // of the tile being walked
+  auto keep = [&]() {
 #pragma unroll
-    for (int q = 0; q < TW; ++q) { nx[q] = rx[q]; nz[q] = rz[q]; }
-    if (next < end) fetch(next + TT);
-    lds_sync();
+    for (int q = 0; q < TW; ++q) { x[q] = rx[q]; z[q] = rz[q]; }
+  };
+  auto finish = [&](int buf, const In (&xs)[TW], const In (&zs)[TW], int left) {
     if constexpr (kOut) {
+      float y[TW];
 #pragma unroll
       for (int q = 0; q < TW; ++q) {
-        const int k = wave * TW + q;
-        float y = skip * x[q];
+        y[q] = skip * Elem<In>::load(&xs[q], 0);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) y += part[buf][k][w][lane];
-        if (in.z) y *= step_silu(z[q]);
-        if (t0 + k < end && mine) Elem<Out>::store(static_cast<Out*>(p.out) + (t0 + k) * p.out_stride, c, y);
+        for (int w = 0; w < NW; ++w) y[q] += part[buf][wave * TW + q][w][lane];
       }
+      if (in.z) {
+#pragma unroll
+        for (int q = 0; q < TW; ++q) y[q] *= step_silu(Elem<In>::load(&zs[q], 0));
+      }
+#pragma unroll
+      for (int q = 0; q < TW; ++q)
+        if (wave * TW + q < left && mine)
+          Elem<Out>::store(reinterpret_cast<Out*>(reinterpret_cast<char*>(out_at + q * p.out_stride) + at_out), 0, y[q]);
+      out_at += TT * p.out_stride;
+    }
+  };
+  const int64_t tiles = first < end ? (end - first) / TT : 0;
+  const int tail = first < end ? (int)((end - first) % TT) : 0;
+  int buf = 0;
+  if (tiles > 0) {
+    fetch();
+    stage(0, TT);
+    keep();
+    advance(tiles > 1);
+    fetch();
+    lds_sync();
+    for (int64_t k = 0; k < tiles; ++k, buf ^= 1) {
+      walk(buf);
+      // the next tile: staged behind this one, its successor fetched (the last one again where there is none)
+      stage(buf ^ 1, TT);
+      In was_x[TW], was_z[TW];
+#pragma unroll
+      for (int q = 0; q < TW; ++q) { was_x[q] = x[q]; was_z[q] = z[q]; }
+      keep();
+      advance(k + 2 < tiles);
+      fetch();
+      lds_sync();
+      finish(buf, was_x, was_z, TT);
+    }
+    advance(true);
+  }
+  if (tail > 0) {
+    // (`buf` is the other one than the last walk's, which may still be read)
+#pragma unroll
+    for (int q = 0; q < TW; ++q) {
+      const bool there = wave * TW + q < tail;
+      rx[q] = there ? of(x_at + q * in.x_stride) : In(0);
+      rdt[q] = there ? of(dt_at + q * in.dt_stride) : In(0);
+      if (kOut) rz[q] = there ? of(z_at + q * z_stride) : In(0);
     }
 #pragma unroll
-    for (int q = 0; q < TW; ++q) { x[q] = nx[q]; z[q] = nz[q]; }
+    for (int k = 0; k < kFill; ++k) rbc[k] = bc_token[k] < tail ? *bc_at[k] : In(0);
+    stage(buf, tail);
+    keep();
+    lds_sync();
+    walk(buf);
+    lds_sync();
+    finish(buf, x, z, tail);
   }
   if (!mine) return;
   if constexpr (kPass == kStates) {

@@ -5,19 +5,17 @@
 
 namespace gdn {
 
-// exp(x), x <= 0: 2^(x log2 e) with the product's rounding error and log2 e's own tail
-// carried along (an exponent of 20 rounded to 24 bits alone would cost 2^-20), on the
-// hardware's 2^x.  Below -104 the result is 0 in any case.
-__device__ __forceinline__ float step_exp_nonpos(float x) {
-  x = x < -104.0f ? -104.0f : x;   // (a NaN stays)
-  const float hi = x * 1.4426950408889634f;
-  const float lo = fmaf(x, 1.925963033500e-08f, fmaf(x, 1.4426950408889634f, -hi));
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return fmaf(e, lo * 0.6931471805599453f, e);
-}
-// log(1 + exp(z))
+// log(1 + exp(z)) = max(z, 0) + log1p(e), e = exp(-|z|): the exponent's product with log2 e
+// loses up to |z| 2^-24, which is carried along (lo; past 2^-16 e is 0 anyway, and an infinite
+// |z| has none); log1p(e) as log(w) of the rounded w = 1 + e plus what the rounding took away
+// (r / w, and 1 / w is near 1 where r counts).
 __device__ __forceinline__ float step_softplus(float z) {
-  return (z > 0.0f ? z : 0.0f) + gate_log1p_unit(step_exp_nonpos(-fabsf(z)));
+  const float a = -fabsf(z), hi = a * 1.4426950408889634f;
+  const float lo = fminf(fmaxf(fmaf(a, 1.4426950408889634f, -hi), -1.5e-5f), 1.5e-5f);
+  float e = __builtin_amdgcn_exp2f(hi);
+  e = fmaf(e, lo * 0.6931471805599453f, e);
+  const float w = 1.0f + e, r = e - (w - 1.0f);
+  return (z > 0.0f ? z : 0.0f) + fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, r);
 }
 // z / (1 + exp(-z)).  The exponential's argument is rounded once, which is worth |z| 2^-23 of
 // the result at most (2^-19 at z = -20, where silu is 4e-8); past exp's range the result is -0.
