@@ -127,7 +127,13 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   const int64_t z_stride = in.z ? in.z_stride : in.x_stride;
   const In* z_at = in.z ? in.z + row0 * z_stride : x_at;
   Out* out_at = static_cast<Out*>(p.out) + row0 * p.out_stride;
-  auto of = [&](const In* row) { return *reinterpret_cast<const In*>(reinterpret_cast<const char*>(row) + at_c); };
+  // (the empty statement keeps the sum of a row's scalar address and the channel's 32-bit offset for the load itself)
+  auto of = [&](const In* row) {
+    auto* from = (const __attribute__((address_space(1))) char*)row;
+    uint32_t off = at_c;
+    asm("" : "+s"(from), "+v"(off));
+    return *(const __attribute__((address_space(1))) In*)(from + off);
+  };
   const In* bc_at[kFill];                                   // this thread's values of B and C
   int64_t bc_step[kFill];
   int bc_token[kFill], bc_to[kFill];                        // their token of the tile; their place in LDS
@@ -178,18 +184,41 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
       if (kValues % (NW * kWave) == 0 || bc_token[k] < TT) to[bc_to[k]] = bc_token[k] < left ? Elem<In>::load(&rbc[k], 0) : 0.0f;
   };
   float sum = 0.0f;                                          // of delta (kStates)
+  // The tile's tokens in turn, LDS reads a step of kStep tokens ahead of their use.
+  constexpr int kStep = SPL <= 4 ? 2 : 1;
   auto walk = [&](int buf) {
+    float2 d[2][kStep];
+    float b[2][kStep][SPL], cc[2][kStep][SPL];
+    auto read = [&](int s) {
 #pragma unroll
-    for (int k = 0; k < TT; ++k) {
-      const float2 d = steps[buf][k][lane];
-      float y = 0.0f;
+      for (int j = 0; j < kStep; ++j) {
+        const int k = s * kStep + j;
+        d[s & 1][j] = steps[buf][k][lane];
 #pragma unroll
-      for (int i = 0; i < SPL; ++i) {
-        h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(d.x * A[i]), d.y * bc[buf][k][wave][0][i]);
-        if constexpr (kOut) y = fmaf(bc[buf][k][wave][kBC - 1][i], h[i], y);
+        for (int i = 0; i < SPL; ++i) {
+          b[s & 1][j][i] = bc[buf][k][wave][0][i];
+          if constexpr (kOut) cc[s & 1][j][i] = bc[buf][k][wave][kBC - 1][i];
+        }
       }
-      if constexpr (kOut) part[buf][k][wave][lane] = y;
-      else sum += d.x;
+    };
+    read(0);
+#pragma unroll
+    for (int s = 0; s < TT / kStep; ++s) {
+      if (s + 1 < TT / kStep) read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const float2 dd = d[s & 1][j];
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) {
+          h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(dd.x * A[i]), dd.y * b[s & 1][j][i]);
+          if constexpr (kOut) y = fmaf(cc[s & 1][j][i], h[i], y);
+        }
+        if constexpr (kOut) part[buf][s * kStep + j][wave][lane] = y;
+        else sum += dd.x;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   In x[TW], z[TW];                                           // of the tile being walked
@@ -212,8 +241,14 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
       }
 #pragma unroll
       for (int q = 0; q < TW; ++q)
-        if (wave * TW + q < left && mine)
-          Elem<Out>::store(reinterpret_cast<Out*>(reinterpret_cast<char*>(out_at + q * p.out_stride) + at_out), 0, y[q]);
+        if (wave * TW + q < left && mine) {
+          auto* to = (__attribute__((address_space(1))) char*)(out_at + q * p.out_stride);
+          uint32_t off = at_out;
+          asm("" : "+s"(to), "+v"(off));
+          Out v;
+          Elem<Out>::store(&v, 0, y[q]);
+          *(__attribute__((address_space(1))) Out*)(to + off) = v;
+        }
       out_at += TT * p.out_stride;
     }
   };
