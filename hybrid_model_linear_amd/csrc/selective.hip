@@ -77,42 +77,45 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   const bool mine = channel_of(p, blk, c, g);
   const int32_t slot = p.slot[n];
   if (slot < 0) return;
-  int64_t first = p.cu[n], end = p.cu[n + 1];
+  int64_t first = __builtin_amdgcn_readfirstlane(p.cu[n]), end = __builtin_amdgcn_readfirstlane(p.cu[n + 1]);
+  // A sequence of `pieces` segments keeps its states in that many rows of the workspace from
+  // 2 (its first token / seg_len) on: one for each segment but the last, and its start state
+  // (whose slot of the pool the last segment writes).  One segment needs none.
   bool last = true;
+  int pieces = 1;
+  int64_t seg_row = 0;
   if constexpr (kPass != kWhole) {
-    first += seg * p.seg_len;
-    if (seg > 0 && first >= end) return;
-    last = seg == p.segs - 1 || first + p.seg_len >= end;
-    if (!last) end = first + p.seg_len;
+    const int len = (int)p.seg_len;
+    pieces = max(1, min(((int)(end - first) + len - 1) / len, p.segs));
+    if (seg >= (kPass == kStates ? pieces - 1 : pieces)) return;
+    seg_row = 2 * ((int)first / len) * p.D;
+    last = seg == pieces - 1;
+    first += (int64_t)seg * len;
+    if (!last) end = first + len;
   }
   const int64_t at = c * NS + wave * SPL;                   // this lane's states in an [D, states] matrix
-  const int64_t seg_row = ((int64_t)n * p.segs + seg) * p.D;
   float* state = p.pool + (int64_t)slot * p.D * NS + at;
   const bool init = !p.has_init || p.has_init[n] != 0;
   float A[SPL], h[SPL];
 #pragma unroll
   for (int i = 0; i < SPL; ++i) A[i] = p.A[at + i] * kLog2e;
-  if constexpr (kPass == kSegment) {
-    // The first segment's start state stands in the row that no segment's last state takes
-    // (the pool's slot is written by this launch).
-    const float* from = p.seg_state + (seg_row - (int64_t)seg * p.D) * NS + at;
-    const float* sums = p.seg_delta + (seg_row - (int64_t)seg * p.D) + c;
-    const int64_t row = p.D * NS;
-    if (seg == 0) from += (p.segs - 1) * row;
+  const int64_t row = p.D * NS;
+  float* kept = p.seg_state + seg_row * NS + at;            // of the sequence's first segment
+  if (kPass == kSegment && pieces > 1) {
+    const float* from = seg == 0 ? kept + (pieces - 1) * row : kept;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) h[i] = from[i];
     for (int s = 1; s < seg; ++s) {
-      const float sum = sums[s * p.D];
+      const float sum = p.seg_delta[seg_row + s * p.D + c];
 #pragma unroll
       for (int i = 0; i < SPL; ++i) h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(sum * A[i]), from[s * row + i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < SPL; ++i) h[i] = init && seg == 0 ? state[i] : 0.0f;
-    if constexpr (kPass == kStates) {
-      if (seg == 0 && mine)
+    if (kPass == kStates && seg == 0 && mine) {
 #pragma unroll
-        for (int i = 0; i < SPL; ++i) p.seg_state[(seg_row + (int64_t)(p.segs - 1) * p.D) * NS + at + i] = h[i];
+      for (int i = 0; i < SPL; ++i) kept[(pieces - 1) * row + i] = h[i];
     }
   }
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
@@ -128,10 +131,9 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   const In* z_at = in.z ? in.z + row0 * z_stride : x_at;
   Out* out_at = static_cast<Out*>(p.out) + row0 * p.out_stride;
   // (the empty statement keeps the sum of a row's scalar address and the channel's 32-bit offset for the load itself)
-  auto of = [&](const In* row) {
+  auto of = [&](const In* row, uint32_t off) {
     auto* from = (const __attribute__((address_space(1))) char*)row;
-    uint32_t off = at_c;
-    asm("" : "+s"(from), "+v"(off));
+    asm("" : "+s"(from));
     return *(const __attribute__((address_space(1))) In*)(from + off);
   };
   const In* bc_at[kFill];                                   // this thread's values of B and C
@@ -147,11 +149,13 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
     bc_step[k] = TT * stride;
   }
   auto fetch = [&]() {
+    uint32_t off = at_c;
+    asm("" : "+v"(off));
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
-      rx[q] = of(x_at + q * in.x_stride);
-      rdt[q] = of(dt_at + q * in.dt_stride);
-      if (kOut) rz[q] = of(z_at + q * z_stride);
+      rx[q] = of(x_at + q * in.x_stride, off);
+      rdt[q] = of(dt_at + q * in.dt_stride, off);
+      if (kOut) rz[q] = of(z_at + q * z_stride, off);
     }
 #pragma unroll
     for (int k = 0; k < kFill; ++k) rbc[k] = *bc_at[k];
@@ -228,6 +232,8 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   };
   auto finish = [&](int buf, const In (&xs)[TW], const In (&zs)[TW], int left) {
     if constexpr (kOut) {
+      uint32_t off = at_out;
+      asm("" : "+v"(off));
       float y[TW];
 #pragma unroll
       for (int q = 0; q < TW; ++q) {
@@ -243,8 +249,7 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
       for (int q = 0; q < TW; ++q)
         if (wave * TW + q < left && mine) {
           auto* to = (__attribute__((address_space(1))) char*)(out_at + q * p.out_stride);
-          uint32_t off = at_out;
-          asm("" : "+s"(to), "+v"(off));
+          asm("" : "+s"(to));
           Out v;
           Elem<Out>::store(&v, 0, y[q]);
           *(__attribute__((address_space(1))) Out*)(to + off) = v;
@@ -282,9 +287,9 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
       const bool there = wave * TW + q < tail;
-      rx[q] = there ? of(x_at + q * in.x_stride) : In(0);
-      rdt[q] = there ? of(dt_at + q * in.dt_stride) : In(0);
-      if (kOut) rz[q] = there ? of(z_at + q * z_stride) : In(0);
+      rx[q] = there ? of(x_at + q * in.x_stride, at_c) : In(0);
+      rdt[q] = there ? of(dt_at + q * in.dt_stride, at_c) : In(0);
+      if (kOut) rz[q] = there ? of(z_at + q * z_stride, at_c) : In(0);
     }
 #pragma unroll
     for (int k = 0; k < kFill; ++k) rbc[k] = bc_token[k] < tail ? *bc_at[k] : In(0);
@@ -297,10 +302,9 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   }
   if (!mine) return;
   if constexpr (kPass == kStates) {
-    float* to = p.seg_state + seg_row * NS + at;
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) to[i] = h[i];
-    if (wave == 0) p.seg_delta[seg_row + c] = sum;
+    for (int i = 0; i < SPL; ++i) kept[seg * row + i] = h[i];
+    if (wave == 0) p.seg_delta[seg_row + seg * p.D + c] = sum;
   } else if (last && !p.keep_pool) {
 #pragma unroll
     for (int i = 0; i < SPL; ++i) state[i] = h[i];
@@ -383,20 +387,22 @@ hipError_t launch_types(const SelectiveLaunch& p, bool update, hipStream_t strea
 }  // namespace
 
 void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus) {
-  // Cutting costs nearly twice the arithmetic (the states are formed twice), so it pays where
-  // the uncut launch leaves the chip mostly empty.
+  // In tokens of one workgroup: uncut, the longest sequence walks alone while the others share
+  // the chip, which is full at 1.4 workgroups of four waves per CU (0.7 of eight); cut, all
+  // tokens cost 1.5 times as much (the states are formed twice), plus one segment and a launch.
+  // Measured, us, 16 states, uncut / cut: one of 4096 x 4096 channels 429 / 135, two 428 / 249, four
+  // 451 / 441, eight 617 / 811; one of 256 x 1024 32 / 17; 8192 and 31 of 500 x 4096 922 / 686.
+  // Segments: four workgroups (two of eight waves) a CU, no shorter than two tiles.
   p.segs = 1;
   p.seg_len = longest;
-  const int64_t wgs = channel_blocks(p) * p.N;
-  const int waves = p.states <= 32 ? 4 : 8;
-  const int64_t places = (int64_t)cus * 16 / waves;     // four waves a SIMD
-  if (wgs * 4 > places || longest < 256) return;
-  int64_t segs = places / wgs;
-  if (segs > (longest + 127) / 128) segs = (longest + 127) / 128;
-  if (segs > 64) segs = 64;
-  if (segs < 2) return;
-  p.seg_len = ((longest + segs - 1) / segs + 15) / 16 * 16;
-  p.segs = (int)((longest + p.seg_len - 1) / p.seg_len);
+  const int eight = p.states > 32;
+  const int64_t work = channel_blocks(p) * p.T;
+  int64_t len = work / (eight ? 2 * cus : 4 * cus) / 16 * 16;
+  if (len < longest / 128) len = longest / 128;
+  len = (len < 32 ? 32 : len + 15) / 16 * 16;
+  if (15 * work / (eight ? 7 * cus : 14 * cus) + len + 80 >= longest) return;
+  p.seg_len = len;
+  p.segs = (int)((longest + len - 1) / len);
 }
 
 hipError_t launch_selective_scan(const SelectiveLaunch& p, hipStream_t stream) { return launch_types(p, false, stream); }

@@ -62,7 +62,7 @@ int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunc
       meet(o, rows(a->z, a->T, a->z_stride, a->D, in)) || meet(o, pool))
     return GDN_E_SHAPE;
   const int64_t dg = a->D / a->G;
-  if ((dg + 63) / 64 * a->G * a->N > kMaxGrid) return GDN_E_UNSUPPORTED;
+  if ((dg + 63) / 64 * a->G * a->N > kMaxGrid / 2) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.G = a->G;
   p.T = a->T;
@@ -93,9 +93,15 @@ int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunc
   p.keep_pool = a->keep_pool != 0;
   p.segs = 1;
   if (update || a->N == 0) return GDN_OK;
-  gdn::plan_selective_scan(p, a->max_seqlen > 0 && a->max_seqlen < a->T ? a->max_seqlen : a->T, gdn::current_device_cus());
+  // (without a hint: four times the average, which ragged batches seldom exceed by much)
+  int64_t longest = a->max_seqlen > 0 ? a->max_seqlen : (a->T + a->N - 1) / a->N * 4;
+  gdn::plan_selective_scan(p, longest < a->T ? longest : a->T, gdn::current_device_cus());
   if (p.segs == 1) return GDN_OK;
-  const int64_t rows = (int64_t)a->N * p.segs * a->D, states = rows * a->states * 4;   // (a multiple of 32 bytes)
+  if ((dg + 63) / 64 * a->G * a->N * p.segs > kMaxGrid / 2) {
+    p.segs = 1;
+    return GDN_OK;
+  }
+  const int64_t rows = (2 * (a->T / p.seg_len) + 1) * a->D, states = rows * a->states * 4;   // (a multiple of 32 bytes)
   p.seg_state = static_cast<float*>(a->workspace);
   p.seg_delta = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(a->workspace) + states);
   need = states + rows * 4;

@@ -39,8 +39,8 @@ struct SelectiveLaunch {
   // Sequences cut into segments of seg_len tokens, the last of `segs` taking the rest; segs 1: not cut.
   int segs;
   int64_t seg_len;
-  float* seg_state;           // [N, segs, D, states]
-  float* seg_delta;           // [N, segs, D]
+  float* seg_state;           // [2 (T / seg_len) + 1, D, states]
+  float* seg_delta;           // [2 (T / seg_len) + 1, D]
 };
 
 // Segments of a scan on a card of this many CUs: segs and seg_len.
