@@ -326,39 +326,92 @@ void launch_scan(const SelectiveLaunch& p, hipStream_t stream) {
 }
 
 // ------------------------------------------------------------------ update
-// One token: a thread takes a channel with its states in registers.
-template <typename In, typename Out, int NS>
-__global__ void __launch_bounds__(kBlock) update_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
-  const int n = blockIdx.x / blocks;
-  int64_t c;
-  int g;
-  if (!channel_of(p, blockIdx.x % blocks, c, g)) return;
-  const int32_t slot = p.slot[n];
-  if (slot < 0) return;
-  const float* A = p.A + c * NS;
-  float* state = p.pool + ((int64_t)slot * p.D + c) * NS;
-  const float x = Elem<In>::load(in.x, n * in.x_stride + c);
-  float delta = Elem<In>::load(in.dt, n * in.dt_stride + c) + (p.dt_bias ? p.dt_bias[c] : 0.0f);
-  if (p.softplus_on) delta = step_softplus(delta);
-  const float dx = delta * x;
-  float y = p.D_skip ? p.D_skip[c] * x : 0.0f;
+// One token per row: the states are read and written once and little else is (memory-bound).
+// A lane takes four states of a channel, NS / 4 lanes a channel, whose sum over the states is
+// formed across them; a workgroup takes 1024 / NS channels of kRows rows, for which A is loaded
+// once and whose states are all in flight together.
+template <typename In, bool kVec>
+__device__ __forceinline__ void load_four(const In* p, float (&v)[4]) {
+  if constexpr (!kVec) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const float b = Elem<In>::load(in.B, n * in.B_stride + (int64_t)g * NS + i);
-    const float cc = Elem<In>::load(in.C, n * in.C_stride + (int64_t)g * NS + i);
-    const float h = fmaf(state[i], __builtin_amdgcn_exp2f(delta * (A[i] * kLog2e)), dx * b);
-    state[i] = h;
-    y = fmaf(cc, h, y);
+    for (int i = 0; i < 4; ++i) v[i] = Elem<In>::load(p, i);
+  } else if constexpr (sizeof(In) == 4) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
   }
-  if (in.z) y *= step_silu(Elem<In>::load(in.z, n * in.z_stride + c));
-  Elem<Out>::store(static_cast<Out*>(p.out), n * p.out_stride + c, y);
+}
+
+template <typename In, typename Out, int NS, int kRows, bool kVec>
+__global__ void __launch_bounds__(256) update_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
+  constexpr int kLanes = NS / 4, kChannels = 256 / kLanes;
+  const int blk = blockIdx.x % blocks, n0 = blockIdx.x / blocks * kRows;
+  const int dg = (int)(p.D / p.G), per = (dg + kChannels - 1) / kChannels, g = blk / per;
+  const int within = blk % per * kChannels + threadIdx.x / kLanes, i0 = threadIdx.x % kLanes * 4;
+  const bool mine = within < dg;
+  const int64_t c = (int64_t)g * dg + (mine ? within : dg - 1), at = c * NS + i0;
+  int32_t slot[kRows];
+  float4 state[kRows];
+  float x[kRows], dt[kRows], z[kRows], b[kRows][4], cc[kRows][4];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) slot[r] = n0 + r < p.N ? p.slot[n0 + r] : -1;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (slot[r] < 0) continue;
+    const int64_t n = n0 + r, bc = (int64_t)g * NS + i0;
+    state[r] = *reinterpret_cast<const float4*>(p.pool + (int64_t)slot[r] * p.D * NS + at);
+    x[r] = Elem<In>::load(in.x + n * in.x_stride, c);
+    dt[r] = Elem<In>::load(in.dt + n * in.dt_stride, c);
+    if (in.z) z[r] = Elem<In>::load(in.z + n * in.z_stride, c);
+    load_four<In, kVec>(in.B + n * in.B_stride + bc, b[r]);
+    load_four<In, kVec>(in.C + n * in.C_stride + bc, cc[r]);
+  }
+  const float4 a4 = *reinterpret_cast<const float4*>(p.A + at);
+  const float A[4] = {a4.x * kLog2e, a4.y * kLog2e, a4.z * kLog2e, a4.w * kLog2e};
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (slot[r] < 0) continue;
+    float delta = dt[r] + bias;
+    if (p.softplus_on) delta = step_softplus(delta);
+    const float dx = delta * x[r];
+    float h[4] = {state[r].x, state[r].y, state[r].z, state[r].w}, y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(delta * A[i]), dx * b[r][i]);
+      y = fmaf(cc[r][i], h[i], y);
+    }
+    y = group_sum<kLanes>(y);
+    if (!mine) continue;
+    *reinterpret_cast<float4*>(p.pool + (int64_t)slot[r] * p.D * NS + at) = make_float4(h[0], h[1], h[2], h[3]);
+    if (i0 == 0) {
+      y = fmaf(skip, x[r], y);
+      if (in.z) y *= step_silu(z[r]);
+      Elem<Out>::store(static_cast<Out*>(p.out) + (n0 + r) * p.out_stride, c, y);
+    }
+  }
 }
 
 template <typename In, typename Out, int NS>
 void launch_update(const SelectiveLaunch& p, hipStream_t stream) {
-  const int64_t blocks = channel_blocks(p);
-  hipLaunchKernelGGL((update_kernel<In, Out, NS>), dim3((unsigned)(blocks * p.N)), dim3(kBlock), 0, stream, p, token_in<In>(p),
-                     (int)blocks);
+  constexpr int kChannels = 1024 / NS;
+  const int64_t blocks = (p.D / p.G + kChannels - 1) / kChannels * p.G;
+  const TokenIn<In> in = token_in<In>(p);
+  const auto four = [](const In* q, int64_t stride) { return reinterpret_cast<uintptr_t>(q) % (4 * sizeof(In)) == 0 && stride % 4 == 0; };
+  const bool vec = four(in.B, in.B_stride) && four(in.C, in.C_stride);
+#define UPDATE(ROWS, VEC)                                                                                             \
+  hipLaunchKernelGGL((update_kernel<In, Out, NS, ROWS, VEC>), dim3((unsigned)(blocks * ((p.N + ROWS - 1) / ROWS))), \
+                     dim3(256), 0, stream, p, in, (int)blocks)
+  // One row a workgroup while that leaves places free: latency.
+  if (blocks * p.N < 4096) {
+    if (vec) UPDATE(1, true); else UPDATE(1, false);
+  } else {
+    if (vec) UPDATE(4, true); else UPDATE(4, false);
+  }
+#undef UPDATE
 }
 
 template <typename In, typename Out>

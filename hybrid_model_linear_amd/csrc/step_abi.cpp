@@ -62,7 +62,9 @@ int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunc
       meet(o, rows(a->z, a->T, a->z_stride, a->D, in)) || meet(o, pool))
     return GDN_E_SHAPE;
   const int64_t dg = a->D / a->G;
-  if ((dg + 63) / 64 * a->G * a->N > kMaxGrid / 2) return GDN_E_UNSUPPORTED;
+  // (the scan's workgroups have up to 512 threads, 64 channels each; the update's 1024 / states channels)
+  const int64_t per = update ? 1024 / a->states : 64;
+  if ((dg + per - 1) / per * a->G * a->N > kMaxGrid / 2) return GDN_E_UNSUPPORTED;
   p.N = a->N;
   p.G = a->G;
   p.T = a->T;
