@@ -2,8 +2,7 @@
 // (gdn_rms_norm).  Each value is read once and written once, a few dozen operations apart:
 // memory is the bound, so a row stays on chip between its two reductions (the parts' sums of
 // squares, and in 8 bits the groups' maxima).
-//   row_kernel : a row in the registers of 1, 4 or 16 waves, 8 values (or, where rows are
-//                unaligned or odd, one) per thread and piece.
+//   row_kernel : a row in the registers of 1, 4 or 16 waves, 8 values per thread and piece.
 //   lds_kernel : parts that no power of two of lanes covers: the row in LDS.  Rows too long
 //                for either are read again for each pass (from the caches).
 #include "step_launch.h"
@@ -40,105 +39,140 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 }
 
 // ------------------------------------------------------------------ rows in registers
-// V consecutive values at element i of a row operand.
-template <int V>
-__device__ __forceinline__ void load_values(const void* p, int bf16, int64_t i, float (&v)[V]) {
-  if constexpr (V == 8) {
-    if (bf16) {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const u16*>(p) + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight values in a row from element i on, n of them there (the others are 0 and not written).
+// kWhole: all eight, in aligned pieces; else at any element (the card takes wide loads and
+// stores at any address), with a row's last values one by one.
+struct __attribute__((packed, aligned(1))) Loose4 { uint32_t u[4]; };
+struct __attribute__((packed, aligned(1))) Loose2 { uint32_t u[2]; };
+
+template <bool kWhole>
+__device__ __forceinline__ void load_values(const void* p, int bf16, int64_t i, int n, float (&v)[8]) {
+  if (!kWhole && n < 8) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(u[k] << 16);
-        v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    for (int k = 0; k < 8; ++k)
+      v[k] = k >= n ? 0.0f : bf16 ? bf16_to_f32(static_cast<const u16*>(p)[i + k]) : static_cast<const float*>(p)[i + k];
+    return;
+  }
+  if (bf16) {
+    const u16* at = static_cast<const u16*>(p) + i;
+    uint32_t u[4];
+    if constexpr (kWhole) {
+      const uint4 w = *reinterpret_cast<const uint4*>(at);
+      u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+    } else {
+      const Loose4 w = *reinterpret_cast<const Loose4*>(at);
+      u[0] = w.u[0]; u[1] = w.u[1]; u[2] = w.u[2]; u[3] = w.u[3];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  } else {
+    const float* at = static_cast<const float*>(p) + i;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (kWhole) {
+        const float4 w = reinterpret_cast<const float4*>(at)[k];
+        v[4 * k] = w.x; v[4 * k + 1] = w.y; v[4 * k + 2] = w.z; v[4 * k + 3] = w.w;
+      } else {
+        const Loose4 w = reinterpret_cast<const Loose4*>(at)[k];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[4 * k + m] = __uint_as_float(w.u[m]);
       }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
-  } else {
-    v[0] = bf16 ? bf16_to_f32(static_cast<const u16*>(p)[i]) : static_cast<const float*>(p)[i];
   }
 }
-template <int V>
-__device__ __forceinline__ void store_values(void* p, int bf16, int64_t i, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    if (bf16) {
-      bf16x8 b;
+template <bool kWhole>
+__device__ __forceinline__ void store_values(void* p, int bf16, int64_t i, int n, const float (&v)[8]) {
+  if (!kWhole && n < 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) b[k] = (__bf16)v[k];
-      *reinterpret_cast<bf16x8*>(static_cast<u16*>(p) + i) = b;
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
+    for (int k = 0; k < 8; ++k)
+      if (k < n) {
+        if (bf16) static_cast<u16*>(p)[i + k] = f32_to_bf16(v[k]);
+        else static_cast<float*>(p)[i + k] = v[k];
+      }
+    return;
+  }
+  if (bf16) {
+    bf16x8 b;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = (__bf16)v[k];
+    u16* at = static_cast<u16*>(p) + i;
+    if constexpr (kWhole) *reinterpret_cast<bf16x8*>(at) = b;
+    else *reinterpret_cast<Loose4*>(at) = __builtin_bit_cast(Loose4, b);
   } else {
-    if (bf16) static_cast<u16*>(p)[i] = f32_to_bf16(v[0]);
-    else static_cast<float*>(p)[i] = v[0];
+    float* at = static_cast<float*>(p) + i;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 w = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      if constexpr (kWhole) reinterpret_cast<float4*>(at)[k] = w;
+      else reinterpret_cast<Loose4*>(at)[k] = __builtin_bit_cast(Loose4, w);
+    }
   }
 }
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
-    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+template <bool kWhole>
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int n, const float (&v)[8]) {
+  int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
+  int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+  b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+  if constexpr (kWhole) {
     *reinterpret_cast<uint2*>(p + i) = make_uint2((uint32_t)a, (uint32_t)b);
+  } else if (n == 8) {
+    *reinterpret_cast<Loose2*>(p + i) = {{(uint32_t)a, (uint32_t)b}};
   } else {
-    p[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0], 0.0f, 0, false);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[i + k] = (uint8_t)((k < 4 ? a : b) >> (k % 4 * 8));
   }
 }
 
-// A row of W = H d <= 64 V K RW values over RW waves: piece j of thread r holds the values
-// (64 RW j + r) V on.  part_lanes: lanes of a part for H > 1 (V = 8: d / 8, a power of two up
-// to 64).  A value past W is 0 and takes part in nothing.
-template <int V, int K, int RW>
+// A row of W = H d <= 512 K RW values over RW waves: piece j of thread r holds the values
+// 8 (64 RW j + r) on.  part_lanes: lanes of a part for H > 1 (d / 8, a power of two up to 64).
+// A value past W is 0 and takes part in nothing.
+template <bool kWhole, int K, int RW>
 __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaunch p, int part_lanes) {
   constexpr int kRows = RW >= 4 ? 1 : 4 / RW, kRowThreads = RW * kWave;
-  __shared__ float sums[kRows][RW];
-  __shared__ float tops[kRows][V == 1 ? K * RW : RW];
+  __shared__ float sums[kRows][RW], tops[kRows][RW];
   const int row = threadIdx.x / kRowThreads, r = threadIdx.x % kRowThreads, wave = r / kWave;
   const int64_t t = (int64_t)blockIdx.x * kRows + row;
-  const bool here = t < p.T;
   const int W = p.H * p.d;
-  float u[K][V], g[K][V];
-  int at[K];
+  float u[K][8], g[K][8];
+  int at[K], n[K];                                          // a piece's first value and how many are there
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    at[j] = (j * kRowThreads + r) * V;
-    if (!here || at[j] >= W) at[j] = -1;
+    at[j] = (j * kRowThreads + r) * 8;
+    n[j] = t < p.T ? max(0, min(8, W - at[j])) : 0;
   }
 #pragma unroll
   for (int j = 0; j < K; ++j) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) u[j][v] = 0.0f;
-    if (at[j] >= 0) load_values<V>(p.x, p.in_bf16, t * p.x_stride + at[j], u[j]);
+    for (int v = 0; v < 8; ++v) u[j][v] = 0.0f;
+    if (n[j] > 0) load_values<kWhole>(p.x, p.in_bf16, t * p.x_stride + at[j], n[j], u[j]);
   }
   if (p.residual) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (at[j] >= 0) load_values<V>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], g[j]);
+      if (n[j] > 0) load_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], n[j], g[j]);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (at[j] < 0) continue;
+      if (n[j] == 0) continue;
 #pragma unroll
-      for (int v = 0; v < V; ++v) u[j][v] += g[j][v];
-      store_values<V>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], u[j]);
+      for (int v = 0; v < 8; ++v) u[j][v] += g[j][v];
+      store_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], n[j], u[j]);
     }
   } else if (p.gate) {
 #pragma unroll
     for (int j = 0; j < K; ++j) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) g[j][v] = 0.0f;
-      if (at[j] >= 0) load_values<V>(p.gate, p.in_bf16, t * p.gate_stride + at[j], g[j]);
+      for (int v = 0; v < 8; ++v) g[j][v] = 0.0f;
+      if (n[j] > 0) load_values<kWhole>(p.gate, p.in_bf16, t * p.gate_stride + at[j], n[j], g[j]);
     }
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int v = 0; v < 8; ++v) {
         g[j][v] = step_silu(g[j][v]);
         if (p.gate_first) u[j][v] *= g[j][v];
       }
@@ -150,7 +184,7 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum = fmaf(u[j][v], u[j][v], sum);
+      for (int v = 0; v < 8; ++v) sum = fmaf(u[j][v], u[j][v], sum);
     sum = group_sum<64>(sum);
     if constexpr (RW > 1) {
       if (r % kWave == 0) sums[row][wave] = sum;
@@ -167,30 +201,30 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
     for (int j = 0; j < K; ++j) {
       float sum = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum = fmaf(u[j][v], u[j][v], sum);
+      for (int v = 0; v < 8; ++v) sum = fmaf(u[j][v], u[j][v], sum);
       rstd[j] = 1.0f / sqrtf(lanes_sum(sum, part_lanes) / (float)p.d + p.eps);
     }
   }
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    float w[V];
+    if (p.weight && n[j] > 0) {
+      float w[8];
+      load_values<kWhole>(p.weight, p.weight_bf16, p.H == 1 ? at[j] : at[j] & (p.d - 1), n[j], w);   // (parts are powers of two)
 #pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = 1.0f;
-    if (p.weight && at[j] >= 0) {
-      load_values<V>(p.weight, p.weight_bf16, p.H == 1 ? at[j] : at[j] & (p.d - 1), w);   // (parts are powers of two)
+      for (int v = 0; v < 8; ++v) u[j][v] *= rstd[j] * (w[v] + p.offset);
+    } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) w[v] += p.offset;
+      for (int v = 0; v < 8; ++v) u[j][v] *= rstd[j];
     }
+    if (p.gate && !p.gate_first) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      u[j][v] *= rstd[j] * w[v];
-      if (p.gate && !p.gate_first) u[j][v] *= g[j][v];
+      for (int v = 0; v < 8; ++v) u[j][v] *= g[j][v];
     }
   }
   if (p.out_dtype != GDN_E4M3) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (at[j] >= 0) store_values<V>(p.out, p.out_dtype == GDN_BF16, t * p.out_stride + at[j], u[j]);
+      if (n[j] > 0) store_values<kWhole>(p.out, p.out_dtype == GDN_BF16, t * p.out_stride + at[j], n[j], u[j]);
     return;
   }
   // the groups' largest magnitudes (fmaxf passes NaN over; infinities are looked for)
@@ -200,7 +234,7 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
   for (int j = 0; j < K; ++j) {
     top[j] = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) top[j] = fmaxf(top[j], fabsf(u[j][v]));
+    for (int v = 0; v < 8; ++v) top[j] = fmaxf(top[j], fabsf(u[j][v]));
     odd |= top[j] == __uint_as_float(0x7f800000u);
   }
   if (odd) {
@@ -208,7 +242,7 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
     for (int j = 0; j < K; ++j) {
       top[j] = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int v = 0; v < 8; ++v) {
         top[j] = fmaxf(top[j], finite_abs(u[j][v]));
         u[j][v] = nan_unless_finite(u[j][v]);
       }
@@ -227,37 +261,31 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = m;
-  } else if constexpr (V == 8) {
+  } else {
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = lanes_max(top[j], p.group / 8);
-  } else {                      // a wave's piece is 64 values: one group, or half of one
-#pragma unroll
-    for (int j = 0; j < K; ++j) top[j] = lanes_max(top[j], 64);
-    if (p.group == 128) {
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (r % kWave == 0) tops[row][j * RW + wave] = top[j];
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < K; ++j) top[j] = fmaxf(top[j], tops[row][(j * RW + wave) ^ 1]);
-    }
   }
+  const int shift = p.groups == 1 ? 20 : p.group == 64 ? 6 : 7;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (at[j] < 0) continue;
+    if (n[j] == 0) continue;
     const float scale = fmaxf(top[j] / 448.0f, kMinScale), inv = 1.0f / scale;
-    const int shift = p.groups == 1 ? 20 : p.group == 64 ? 6 : 7;
     if ((at[j] & ((1 << shift) - 1)) == 0) p.scale[t * p.groups + (at[j] >> shift)] = scale;
-    float c[V];
+    float c[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = u[j][v] * inv;
-    store_codes<V>(static_cast<uint8_t*>(p.out), t * p.out_stride + at[j], c);
+    for (int v = 0; v < 8; ++v) c[v] = u[j][v] * inv;
+    store_codes<kWhole>(static_cast<uint8_t*>(p.out), t * p.out_stride + at[j], n[j], c);
   }
 }
 
 // ------------------------------------------------------------------ rows of any shape
 __device__ __forceinline__ float load_any(const void* p, int bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const u16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ void store_any(void* p, int bf16, int64_t i, float v) {
+  if (bf16) static_cast<u16*>(p)[i] = f32_to_bf16(v);
+  else static_cast<float*>(p)[i] = v;
 }
 
 // A workgroup takes a row; its waves take the row's parts in turn for the sums of squares, then
@@ -277,10 +305,7 @@ __global__ void __launch_bounds__(256) lds_kernel(NormLaunch p) {
     if (p.gate && p.gate_first) u *= step_silu(load_any(p.gate, p.in_bf16, gr + e));
     return u;
   };
-  auto put_residual = [&](int e, float u) {
-    const float v[1] = {u};
-    store_values<1>(p.residual, p.residual_bf16, rr + e, v);
-  };
+  auto put_residual = [&](int e, float u) { store_any(p.residual, p.residual_bf16, rr + e, u); };
   if constexpr (kStage) {
     for (int e = threadIdx.x; e < width; e += 256) {
       const float u = value(e);
@@ -309,8 +334,7 @@ __global__ void __launch_bounds__(256) lds_kernel(NormLaunch p) {
   if (p.out_dtype != GDN_E4M3) {
     for (int e = threadIdx.x; e < width; e += 256) {
       const float u = kStage ? kept[e] : value(e);
-      const float y[1] = {result(e, u)};
-      store_values<1>(p.out, p.out_dtype == GDN_BF16, orow + e, y);
+      store_any(p.out, p.out_dtype == GDN_BF16, orow + e, result(e, u));
       if (!kStage && p.residual) put_residual(e, u);
     }
     return;
@@ -327,8 +351,8 @@ __global__ void __launch_bounds__(256) lds_kernel(NormLaunch p) {
     if (lane == 0) p.scale[t * p.groups + k] = scale;
     for (int e = lo + lane; e < hi; e += kWave) {
       const float u = kStage ? 0.0f : value(e);
-      const float c[1] = {nan_unless_finite(kStage ? kept[e] : result(e, u)) * inv};
-      store_codes<1>(static_cast<uint8_t*>(p.out), orow + e, c);
+      const float c = nan_unless_finite(kStage ? kept[e] : result(e, u)) * inv;
+      static_cast<uint8_t*>(p.out)[orow + e] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.0f, 0, false);
       if (!kStage && p.residual) put_residual(e, u);
     }
   }
@@ -339,11 +363,25 @@ bool wide(const void* p, int64_t stride, int64_t size) {   // 8 values at a time
   return reinterpret_cast<uintptr_t>(p) % piece == 0 && stride * size % piece == 0;
 }
 
-template <int V, int K, int RW>
+template <bool kWhole, int K, int RW>
 void launch_rows(const NormLaunch& p, int part_lanes, hipStream_t stream) {
   constexpr int kRows = RW >= 4 ? 1 : 4 / RW;
-  hipLaunchKernelGGL((row_kernel<V, K, RW>), dim3((unsigned)((p.T + kRows - 1) / kRows)), dim3(RW > 4 ? RW * kWave : 256), 0,
+  hipLaunchKernelGGL((row_kernel<kWhole, K, RW>), dim3((unsigned)((p.T + kRows - 1) / kRows)), dim3(RW > 4 ? RW * kWave : 256), 0,
                      stream, p, part_lanes);
+}
+
+template <bool kWhole>
+void launch_row_sizes(const NormLaunch& p, int64_t W, int part_lanes, hipStream_t stream) {
+  // A wave a row up to 1024 values where there are rows for every wave of the chip, else four
+  // waves, which are done sooner.
+  const bool many = p.T >= 1024;
+  if (many && W <= 512) launch_rows<kWhole, 1, 1>(p, part_lanes, stream);
+  else if (many && W <= 1024) launch_rows<kWhole, 2, 1>(p, part_lanes, stream);
+  else if (W <= 2048) launch_rows<kWhole, 1, 4>(p, part_lanes, stream);
+  else if (W <= 4096) launch_rows<kWhole, 2, 4>(p, part_lanes, stream);
+  else if (W <= 8192) launch_rows<kWhole, 4, 4>(p, part_lanes, stream);
+  else if (W <= 16384) launch_rows<kWhole, 2, 16>(p, part_lanes, stream);
+  else launch_rows<kWhole, 4, 16>(p, part_lanes, stream);
 }
 
 }  // namespace
@@ -351,27 +389,13 @@ void launch_rows(const NormLaunch& p, int part_lanes, hipStream_t stream) {
 hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream) {
   const int64_t W = (int64_t)p.H * p.d, in = p.in_bf16 ? 2 : 4, res = p.residual_bf16 ? 2 : 4;
   const int64_t out = p.out_dtype == GDN_E4M3 ? 1 : p.out_dtype == GDN_BF16 ? 2 : 4;
-  const bool eight = W % 8 == 0 && wide(p.x, p.x_stride, in) && (!p.gate || wide(p.gate, p.gate_stride, in)) &&
+  const bool whole = W % 8 == 0 && wide(p.x, p.x_stride, in) && (!p.gate || wide(p.gate, p.gate_stride, in)) &&
                      (!p.residual || wide(p.residual, p.residual_stride, res)) && wide(p.out, p.out_stride, out) &&
                      reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
   const int lanes = p.d / 8;
-  const bool parts = p.H == 1 || (eight && p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
-  if (parts && eight && W <= 32768) {
-    // A wave a row up to 2048 values where there are rows for every wave of the chip, else four
-    // waves, which are done sooner.
-    const bool many = p.T >= 1024;
-    if (many && W <= 512) launch_rows<8, 1, 1>(p, lanes, stream);
-    else if (many && W <= 1024) launch_rows<8, 2, 1>(p, lanes, stream);
-    else if (W <= 2048) launch_rows<8, 1, 4>(p, lanes, stream);
-    else if (W <= 4096) launch_rows<8, 2, 4>(p, lanes, stream);
-    else if (W <= 8192) launch_rows<8, 4, 4>(p, lanes, stream);
-    else if (W <= 16384) launch_rows<8, 2, 16>(p, lanes, stream);
-    else launch_rows<8, 4, 16>(p, lanes, stream);
-  } else if (p.H == 1 && W <= 8192) {
-    if (W <= 256) launch_rows<1, 4, 1>(p, lanes, stream);
-    else if (W <= 1024) launch_rows<1, 4, 4>(p, lanes, stream);
-    else if (W <= 4096) launch_rows<1, 4, 16>(p, lanes, stream);
-    else launch_rows<1, 8, 16>(p, lanes, stream);
+  const bool parts = p.H == 1 || (p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
+  if (parts && W <= 32768) {
+    if (whole) launch_row_sizes<true>(p, W, lanes, stream); else launch_row_sizes<false>(p, W, lanes, stream);
   } else if ((W + p.H) * 4 <= 65536) {
     hipLaunchKernelGGL(lds_kernel<true>, dim3((unsigned)p.T), dim3(256), (W + p.H) * sizeof(float), stream, p);
   } else {

@@ -43,7 +43,7 @@ __device__ __forceinline__ void sum_pair(int64_t& a, int64_t& b, int64_t (&wave_
 }
 
 // First k in [0, 256) with ends[k] > v (ends non-decreasing, ends[255] > v).
-__device__ __forceinline__ int find(const int64_t* ends, int64_t v) {
+__device__ __forceinline__ int find(const int32_t* ends, int32_t v) {
   int lo = 0;
 #pragma unroll
   for (int s = 128; s; s >>= 1)
@@ -73,6 +73,9 @@ __device__ __forceinline__ int32_t load_agent(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// A sum as LDS holds it: what counts lies below 2^31 (the tokens below T, the pages below the capacity).
+__device__ __forceinline__ int32_t narrow(int64_t v) { return (int32_t)min(v, (int64_t)INT32_MAX); }
+
 struct Request {
   int64_t held, tokens, lo, need;
   bool live;
@@ -95,7 +98,7 @@ __device__ __forceinline__ Request request_of(const PlanPagesLaunch& p, int n) {
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   __shared__ int64_t wave_sums[2][kThreads / kWave];
-  __shared__ int64_t token_end[kThreads], page_end[kThreads];   // inclusive sums within the slice
+  __shared__ int32_t token_end[kThreads], page_end[kThreads];   // inclusive sums within the slice
   __shared__ int32_t held_of[kThreads], lo_of[kThreads];        // held -1: not served
   __shared__ int flag;
   const int tid = threadIdx.x, base = blockIdx.x * kThreads, part = blockIdx.y, parts = gridDim.y;
@@ -113,8 +116,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   int64_t te = r.tokens, pe = r.need;
   scan_pair(te, pe, wave_sums);
   const bool served = r.live && pages0 + pe <= count && tokens0 + te <= p.T;
-  token_end[tid] = te;
-  page_end[tid] = pe;
+  token_end[tid] = narrow(te);
+  page_end[tid] = narrow(pe);
   held_of[tid] = served ? (int32_t)r.held : -1;
   lo_of[tid] = (int32_t)r.lo;
   if (part == 0 && n < p.N) {
@@ -124,35 +127,37 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   }
   if (part == 0 && base == 0 && tid == 0) p.cu[0] = 0;
   __syncthreads();
-  // new pages, in order
-  const int64_t pages = page_end[kThreads - 1];
-  for (int64_t i = (int64_t)part * kThreads + tid; i < pages; i += (int64_t)parts * kThreads) {
-    const int k = find(page_end, i);
-    const int64_t at = pages0 + i;
-    if (held_of[k] < 0) continue;      // (served: all of its pages are on the stack)
-    const int64_t j = i - (k ? page_end[k - 1] : 0);
-    p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + j] = stack[count - 1 - at];
+  // new pages, in order (a served request's are all on the stack, below `left`)
+  const int stride = parts * kThreads, place = part * kThreads + tid;
+  const int32_t left = (int32_t)max(count - pages0, (int64_t)0);
+  const int32_t pages = min(page_end[kThreads - 1], left);
+  for (int64_t i = place; i < pages; i += stride) {
+    const int k = find(page_end, (int32_t)i);
+    if (held_of[k] < 0) continue;
+    p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + (i - (k ? page_end[k - 1] : 0))] = stack[left - 1 - i];
   }
   // tokens; the last slice also those behind the last request
-  const int64_t mine = token_end[kThreads - 1];
-  int64_t stop = min(tokens0 + mine, p.T);
-  if (blockIdx.x == gridDim.x - 1) stop = p.T;
-  for (int64_t t = tokens0 + (int64_t)part * kThreads + tid; t < stop; t += (int64_t)parts * kThreads) {
+  const int32_t mine = token_end[kThreads - 1];
+  const int32_t room = (int32_t)max(p.T - tokens0, (int64_t)0);
+  const int32_t stop = blockIdx.x == gridDim.x - 1 ? room : min(mine, room);
+  const uint32_t page = p.page;
+  for (int64_t i64 = place; i64 < stop; i64 += stride) {
+    const int32_t i = (int32_t)i64;
     int64_t slot = -1;
     int32_t position = -1, owner = -1;
-    const int64_t i = t - tokens0;
     if (i < mine) {
       const int k = find(token_end, i);
       if (held_of[k] >= 0) {
-        const int64_t row = held_of[k] + i - (k ? token_end[k - 1] : 0);
-        const int64_t entry = row / p.page;
-        const int64_t id = entry >= lo_of[k] ? stack[count - 1 - (pages0 + (k ? page_end[k - 1] : 0) + entry - lo_of[k])]
-                                             : p.table[(int64_t)(base + k) * p.table_stride + entry];
-        if (id >= 0) slot = id * p.page + row % p.page;
+        const uint32_t in = i - (k ? token_end[k - 1] : 0), row = held_of[k] + in;
+        const uint32_t entry = row / page, rest = row - entry * page;
         owner = base + k;
-        position = p.start ? (int32_t)(p.start[owner] + (row - held_of[k])) : (int32_t)row;
+        const int32_t id = entry >= (uint32_t)lo_of[k] ? stack[left - 1 - ((k ? page_end[k - 1] : 0) + (int32_t)entry - lo_of[k])]
+                                                       : p.table[(int64_t)owner * p.table_stride + entry];
+        if (id >= 0) slot = (int64_t)id * page + rest;
+        position = (int32_t)((p.start ? (uint32_t)p.start[owner] : (uint32_t)held_of[k]) + in);
       }
     }
+    const int64_t t = tokens0 + i;
     if (p.slots) p.slots[t] = slot;
     if (p.positions) p.positions[t] = position;
     if (p.seq) p.seq[t] = owner;
@@ -183,8 +188,7 @@ __device__ __forceinline__ int64_t given_back(const ReleasePagesLaunch& p, int n
 
 __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p) {
   __shared__ int64_t wave_sums[2][kThreads / kWave];
-  __shared__ int64_t page_end[kThreads];
-  __shared__ int32_t lo_of[kThreads];
+  __shared__ int32_t page_end[kThreads], lo_of[kThreads];
   __shared__ int flag;
   const int tid = threadIdx.x, base = blockIdx.x * kThreads, part = blockIdx.y, parts = gridDim.y;
   const int64_t count = min(max((int64_t)p.pool[0], (int64_t)0), p.capacity);
@@ -194,14 +198,14 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p)
   sum_pair(before, none, wave_sums);
   int64_t pe = given_back(p, base + tid, lo);
   scan_pair(pe, none, wave_sums);
-  page_end[tid] = pe;
+  page_end[tid] = narrow(pe);
   lo_of[tid] = (int32_t)lo;
   __syncthreads();
-  const int64_t pages = page_end[kThreads - 1];
+  // (as far as the stack's capacity goes)
+  const int64_t pages = min((int64_t)page_end[kThreads - 1], p.capacity - count - before);
   for (int64_t i = (int64_t)part * kThreads + tid; i < pages; i += (int64_t)parts * kThreads) {
-    const int k = find(page_end, i);
-    const int64_t at = count + before + i;
-    if (at < p.capacity) stack[at] = p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + i - (k ? page_end[k - 1] : 0)];
+    const int k = find(page_end, (int32_t)i);
+    stack[count + before + i] = p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + i - (k ? page_end[k - 1] : 0)];
   }
   if (!last_to_arrive(p.pool + 1, &flag)) return;
   int64_t total = 0;
@@ -212,9 +216,9 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p)
 }
 
 int parts_of(int64_t items, int64_t slices) {
-  // 4096 tokens or pages a workgroup, on average over the slices
-  const int64_t want = (items / slices + 4095) / 4096;
-  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+  // 1024 tokens or pages a workgroup, on average over the slices
+  const int64_t want = (items / slices + 1023) / 1024;
+  return (int)(want < 1 ? 1 : want > 256 ? 256 : want);
 }
 
 }  // namespace
