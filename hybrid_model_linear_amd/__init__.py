@@ -25,7 +25,7 @@ what a step runs beside its attention (step.py):
   rms_norm             norm, residual, gate, 8-bit output  -> gdn_rms_norm
   page_pool, plan_pages, release_pages  a step's block tables and slot maps -> gdn_plan_pages, gdn_release_pages
 and the call shapes of the pages:
-  forward_gdn(layer, forward_batch, mixed_qkv, a, b)  (pymllm HybridAttnBackend.forward_gdn)
+  forward_gdn(layer, forward_batch, mixed_qkv, a, b)  (pymllm HybridAttnBackend.forward_gdn; z: its gated norm too)
   forward_attn(layer, forward_batch, q, k, v)         (pymllm RadixAttention.forward)
   ssd_combined_fwd(x, dt, A, B, C, ...)               (flashinfer.mamba.ssd_combined_fwd subset)
 """
@@ -576,7 +576,8 @@ def _mode_kind(forward_mode) -> str:
     raise ValueError(f"Invalid forward mode: {forward_mode=}")
 
 
-def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, b: torch.Tensor):
+def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                z: torch.Tensor | None = None):
     """GDN layer call of a hybrid model (pymllm HybridAttnBackend.forward_gdn).
 
     layer: num_k_heads, num_v_heads, head_k_dim, head_v_dim, A_log [H_v] fp32,
@@ -596,6 +597,9 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
     same slots, and the conv (with silu) runs first -- gdn_conv1d / gdn_conv1d_update,
     leaving the conv pool unwritten in target verify (with spec_parents the conv
     windows follow the token tree).
+    z (the layer's output gate, [T, H_v * d_v] like the output): the gated norm behind the
+    layer runs too, per head: rms_norm(out, layer.norm_weight [d_v], gate=z) with
+    layer.norm_eps (default 1e-6).
     Returns out [T, H_v * d_v] in mixed_qkv's dtype."""
     kind = _mode_kind(forward_batch.forward_mode)
     H_qk, H_v = layer.num_k_heads, layer.num_v_heads
@@ -643,6 +647,8 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
                    spec_slot=forward_batch.spec_state_slots if verify else None,
                    spec_parent=getattr(forward_batch, "spec_parents", None) if verify else None,
                    keep_pool=verify)
+    if z is not None:
+        o = rms_norm(o, layer.norm_weight, eps=float(getattr(layer, "norm_eps", 1e-6)), gate=z.view(T, H_v, d_v))
     return o.view(T, H_v * d_v)
 
 

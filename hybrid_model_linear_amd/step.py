@@ -33,29 +33,27 @@ def _code(t, name: str) -> int:
     return code
 
 
-def _matrix(t, name: str, n: int, width: int, dtype) -> int:
-    """Row stride of an [n, width] matrix with unit column stride."""
-    if t.dtype is not dtype or t.shape != (n, width):
-        raise ValueError(f"{name} must be {dtype} [{n}, {width}], got {t.dtype} {tuple(t.shape)}")
-    if t.is_contiguous():
-        return width
-    if width > 1 and t.stride(1) != 1:
+def _matrix(t, name: str, shape, dtype) -> int:
+    """Row stride of a matrix of this shape and type with unit column stride."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {tuple(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride (strides {t.stride()})")
-    return t.stride(0) if n > 1 else width
+    return row if shape[0] > 1 else shape[1]
 
 
 def _grouped(t, name: str, n: int, states: int, dtype) -> tuple[int, int]:
     """(token stride, groups) of B or C: [n, G, states] with contiguous groups, or [n, states]."""
     if t.dim() == 2:
-        return _matrix(t, name, n, states, dtype), 1
-    if t.dim() != 3 or t.dtype is not dtype or t.shape[0] != n or t.shape[2] != states:
+        return _matrix(t, name, (n, states), dtype), 1
+    if t.dtype is not dtype or t.dim() != 3 or t.shape[0] != n or t.shape[2] != states:
         raise ValueError(f"{name} must be {dtype} [{n}, G, {states}] or [{n}, {states}], got {t.dtype} {tuple(t.shape)}")
-    g, st = t.shape[1], t.stride()
-    if t.is_contiguous():
-        return g * states, g
-    if (states > 1 and st[2] != 1) or (g > 1 and st[1] != states):
-        raise ValueError(f"{name} must have contiguous groups (strides {st})")
-    return st[0] if n > 1 else g * states, g
+    g = t.shape[1]
+    row, group, col = t.stride()
+    if (states > 1 and col != 1) or (g > 1 and group != states):
+        raise ValueError(f"{name} must have contiguous groups (strides {t.stride()})")
+    return row if n > 1 else g * states, g
 
 
 # ------------------------------------------------------------------ selective scan
@@ -63,7 +61,8 @@ def _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_so
                     max_seqlen, keep_pool):
     if x.dim() != 2 or A.dim() != 2:
         raise ValueError(f"x must be [T, D] and A [D, states], got {tuple(x.shape)} and {tuple(A.shape)}")
-    T, width = x.shape
+    shape = x.shape
+    T, width = shape
     states, N = A.shape[1], slot.shape[0]
     i = _place(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, has_init, out)
     kind = x.dtype
@@ -79,17 +78,19 @@ def _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_so
     if out is None:   # (a query of the workspace reads no buffer: an aligned stand-in for the output)
         o, os, oc = 256, width, _CODES.get(out_dtype, -1)
     else:
-        o, os, oc = out.data_ptr(), _matrix(out, "out", T, width, out.dtype), _code(out, "out")
+        o, os, oc = out.data_ptr(), _matrix(out, "out", shape, out.dtype), _code(out, "out")
     return _lib.SelectiveArgs(
-        code, oc, N, G, T, width, states, 1 if dt_softplus else 0, x.data_ptr(), _matrix(x, "x", T, width, kind),
-        dt.data_ptr(), _matrix(dt, "dt", T, width, kind), B.data_ptr(), bs, C.data_ptr(), cs, _at(z),
-        0 if z is None else _matrix(z, "z", T, width, kind), A.data_ptr(), _vec(D, "D", width, _F32),
+        code, oc, N, G, T, width, states, 1 if dt_softplus else 0, x.data_ptr(), _matrix(x, "x", shape, kind),
+        dt.data_ptr(), _matrix(dt, "dt", shape, kind), B.data_ptr(), bs, C.data_ptr(), cs, _at(z),
+        0 if z is None else _matrix(z, "z", shape, kind), A.data_ptr(), _vec(D, "D", width, _F32),
         _vec(dt_bias, "dt_bias", width, _F32), _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(slot, "slot", N),
         _vec(has_init, "has_init", N), pool.data_ptr(), pool.shape[0], o, os, max_seqlen, 1 if keep_pool else 0, None, 0), i
 
 
 def _new_out(x, out_dtype):
-    return torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    if x.is_contiguous():
+        return torch.empty_like(x) if out_dtype is None else torch.empty_like(x, dtype=out_dtype)
+    return x.new_empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype)
 
 
 def selective_scan(x, dt, A, B, C, cu_seqlens, slot, pool, *, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
@@ -114,7 +115,10 @@ def selective_scan(x, dt, A, B, C, cu_seqlens, slot, pool, *, D=None, z=None, dt
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     args, i = _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_softplus, has_init, out, None,
                               max_seqlen, keep_pool)
-    ws = _attach("gdn_selective_scan", lib.gdn_selective_scan_workspace_size, args, i, workspace)
+    # (no sequence of fewer than 113 tokens is cut: no query, which short calls would feel)
+    ws = None
+    if workspace is not None or args.T > 112:
+        ws = _attach("gdn_selective_scan", lib.gdn_selective_scan_workspace_size, args, i, workspace)
     _run("gdn_selective_scan", lib.gdn_selective_scan, args, i)
     del ws
     return out
@@ -154,13 +158,12 @@ def _token_rows(t, name: str, shape, dtype=None) -> int:
     """Token stride of a tensor of this shape whose rows are contiguous."""
     if t.shape != shape or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name} must be {dtype or 'a tensor'} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    width = shape[1] * shape[2] if len(shape) == 3 else shape[1]
-    if t.is_contiguous():
-        return width
     st = t.stride()
     if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
         raise ValueError(f"{name} must have contiguous rows (strides {st})")
-    return st[0] if shape[0] > 1 else width
+    if shape[0] > 1:
+        return st[0]
+    return shape[1] * shape[2] if len(shape) == 3 else shape[1]
 
 
 def rms_norm(x, weight=None, *, eps: float = 1e-6, offset: float = 0.0, residual=None, gate=None, gate_first: bool = False,
@@ -180,7 +183,7 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, offset: float = 0.0, residual
     H = x.shape[1] if x.dim() == 3 else 1
     code = _code(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = _new_out(x, out_dtype)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     out_code = _OUT_CODES.get(out.dtype)
@@ -190,7 +193,7 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, offset: float = 0.0, residual
     if f8:
         groups = -(-H * d // group) if group > 0 else 1
         if scale is None:
-            scale = torch.empty((T, groups), dtype=_F32, device=x.device)
+            scale = x.new_empty((T, groups), dtype=_F32)
         elif scale.dtype is not _F32 or scale.shape != (T, groups) or not scale.is_contiguous():
             raise ValueError(f"scale must be contiguous fp32 [{T}, {groups}], got {scale.dtype} {tuple(scale.shape)}")
     elif scale is not None:
@@ -260,18 +263,17 @@ def plan_pages(pool: PagePool, block_table, held, new, page: int, tokens: int, *
     N = held.shape[0]
     i = _place(pool._state, block_table, held, new, start)
     ts, tw = _table(block_table, N)
-    if out is None:
-        dev, e = held.device, torch.empty
-        out = StepPlan(e(N + 1, dtype=_I32, device=dev), e(N, dtype=_I32, device=dev), e(N, dtype=_I32, device=dev),
-                       e(tokens, dtype=_I64, device=dev), e(tokens, dtype=_I32, device=dev),
-                       e(tokens, dtype=_I32, device=dev))
+    if out is None:      # (two allocations; the tensors are parts of them)
+        small = held.new_empty(3 * N + 1 + 2 * tokens).split_with_sizes((N + 1, N, N, tokens, tokens))
+        out = StepPlan(small[0], small[1], small[2], held.new_empty(tokens, dtype=_I64), small[3], small[4])
+        at = [t.data_ptr() for t in out]
     else:
         _place(pool._state, *out)
+        at = [_vec(t, name, n, dtype) for t, name, n, dtype in zip(
+            out, StepPlan._fields, (N + 1, N, N, tokens, tokens, tokens), (_I32, _I32, _I32, _I64, _I32, _I32))]
     args = _lib.PlanPagesArgs(
         pool._state.data_ptr(), pool._capacity, N, page, tokens, _vec(held, "held", N), _vec(new, "new", N),
-        _vec(start, "start", N), block_table.data_ptr(), ts, tw, 0, _vec(out[0], "cu_seqlens", N + 1),
-        _vec(out[1], "cache_len", N), _vec(out[2], "kv_len", N), _vec(out[3], "slots", tokens, _I64),
-        _vec(out[4], "positions", tokens), _vec(out[5], "seq", tokens))
+        _vec(start, "start", N), block_table.data_ptr(), ts, tw, 0, *at)
     _run("gdn_plan_pages", lib.gdn_plan_pages, args, i)
     return out
 

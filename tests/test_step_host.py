@@ -182,12 +182,12 @@ def test_shape_helpers():
     p = torch.zeros(5, 40, dtype=bf)
     assert step._grouped(p[:, 8:40].unflatten(1, (2, 16)), "B", 5, 16, bf) == (40, 2)
     assert step._grouped(p[:, 8:24], "B", 5, 16, bf) == (40, 1)
-    assert step._matrix(p[:1, 3:9], "x", 1, 6, bf) == 6
+    assert step._matrix(p[:1, 3:9], "x", (1, 6), bf) == 6
     assert step._token_rows(p[:, 8:].unflatten(1, (4, 8)), "x", torch.Size((5, 4, 8))) == 40
     for bad in (lambda: step._grouped(p.unflatten(1, (2, 20))[:, :, :16], "B", 5, 16, bf),
                 lambda: step._grouped(p.unflatten(1, (2, 20)), "B", 5, 16, bf),
-                lambda: step._matrix(p.T, "x", 40, 5, bf), lambda: step._matrix(p, "x", 5, 40, torch.float32),
-                lambda: step._matrix(p[:, ::2], "x", 5, 20, bf),
+                lambda: step._matrix(p.T, "x", (40, 5), bf), lambda: step._matrix(p, "x", (5, 40), torch.float32),
+                lambda: step._matrix(p[:, ::2], "x", (5, 20), bf),
                 lambda: step._token_rows(p.unflatten(1, (4, 10))[:, :, :8], "x", torch.Size((5, 4, 8)))):
         with pytest.raises(ValueError):
             bad()
