@@ -59,7 +59,7 @@ enum Pass {
 };
 
 template <typename In, typename Out, int NS, int kPass>
-__global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
+__global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLaunch p, TokenIn<In> in, int blocks) {
   constexpr int NW = kWaves<NS>, SPL = NS / NW, TT = kTile<NS>, TW = TT / NW;
   constexpr int kOut = kPass != kStates;                    // y is formed
   constexpr int kBC = kOut ? 2 : 1;                         // B, or B and C
@@ -120,10 +120,11 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
   }
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.D_skip ? p.D_skip[c] : 0.0f;
 
-  // A tile's operands in registers: of TW tokens (this wave's share), and of B and C.  Whole tiles
-  // are fetched one ahead, straight into the registers that the next turn reads (a branch around
-  // the loads, or a conversion behind them, would wait for them here); without z its loads read x.
-  In rx[TW], rdt[TW], rz[TW], rbc[kFill];
+  // A tile's operands in registers: of TW tokens (this wave's share), and of B and C.  Tiles are
+  // fetched two ahead, in turn into two sets of registers from which they are staged and finished
+  // without being moved (a copy, a branch around the loads, or a conversion behind them, would wait
+  // for them); without z its loads read x.
+  struct Operands { In x[TW], dt[TW], z[TW], bc[kFill]; } set[2];
   const uint32_t at_c = (uint32_t)c * sizeof(In), at_out = (uint32_t)c * sizeof(Out);
   const int64_t row0 = first + wave * TW;
   const In *x_at = in.x + row0 * in.x_stride, *dt_at = in.dt + row0 * in.dt_stride;
@@ -148,30 +149,32 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
     bc_to[k] = ((bc_token[k] * NW + s / SPL) * kBC + i / NS) * SPL + s % SPL;
     bc_step[k] = TT * stride;
   }
-  auto fetch = [&]() {
+  auto fetch = [&](Operands& r) __attribute__((always_inline)) {
     uint32_t off = at_c;
     asm("" : "+v"(off));
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
-      rx[q] = of(x_at + q * in.x_stride, off);
-      rdt[q] = of(dt_at + q * in.dt_stride, off);
-      if (kOut) rz[q] = of(z_at + q * z_stride, off);
+      r.x[q] = of(x_at + q * in.x_stride, off);
+      r.dt[q] = of(dt_at + q * in.dt_stride, off);
+      if (kOut) r.z[q] = of(z_at + q * z_stride, off);
     }
 #pragma unroll
-    for (int k = 0; k < kFill; ++k) rbc[k] = *bc_at[k];
+    for (int k = 0; k < kFill; ++k) r.bc[k] = *bc_at[k];
   };
-  auto advance = [&](bool on) {
+  auto advance = [&](bool on) __attribute__((always_inline)) {
     x_at += on ? TT * in.x_stride : 0;
     dt_at += on ? TT * in.dt_stride : 0;
     z_at += on ? TT * z_stride : 0;
 #pragma unroll
     for (int k = 0; k < kFill; ++k) bc_at[k] += on ? bc_step[k] : 0;
   };
-  // Their part that is the same for all states, into LDS; tokens from `left` on count as zeros.
-  auto stage = [&](int buf, int left) {
+  // Their part that is the same for all states, into LDS; tokens from `left` on count as zeros
+  // (`whole`: there are none).
+  auto stage = [&](int buf, const Operands& r, auto whole, int left) __attribute__((always_inline)) {
+    constexpr bool kAll = decltype(whole)::value;
     float delta[TW];
 #pragma unroll
-    for (int q = 0; q < TW; ++q) delta[q] = Elem<In>::load(&rdt[q], 0) + bias;
+    for (int q = 0; q < TW; ++q) delta[q] = Elem<In>::load(&r.dt[q], 0) + bias;
     if (p.softplus_on) {
 #pragma unroll
       for (int q = 0; q < TW; ++q) delta[q] = step_softplus(delta[q]);
@@ -179,21 +182,22 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
       const int k = wave * TW + q;
-      const bool live = k < left;
-      steps[buf][k][lane] = make_float2(live ? delta[q] : 0.0f, live ? delta[q] * Elem<In>::load(&rx[q], 0) : 0.0f);
+      const bool live = kAll || k < left;
+      steps[buf][k][lane] = make_float2(live ? delta[q] : 0.0f, live ? delta[q] * Elem<In>::load(&r.x[q], 0) : 0.0f);
     }
     float* to = &bc[buf][0][0][0][0];
 #pragma unroll
     for (int k = 0; k < kFill; ++k)
-      if (kValues % (NW * kWave) == 0 || bc_token[k] < TT) to[bc_to[k]] = bc_token[k] < left ? Elem<In>::load(&rbc[k], 0) : 0.0f;
+      if (kValues % (NW * kWave) == 0 || bc_token[k] < TT)
+        to[bc_to[k]] = kAll || bc_token[k] < left ? Elem<In>::load(&r.bc[k], 0) : 0.0f;
   };
   float sum = 0.0f;                                          // of delta (kStates)
   // The tile's tokens in turn, LDS reads a step of kStep tokens ahead of their use.
   constexpr int kStep = SPL <= 4 ? 2 : 1;
-  auto walk = [&](int buf) {
+  auto walk = [&](int buf) __attribute__((always_inline)) {
     float2 d[2][kStep];
     float b[2][kStep][SPL], cc[2][kStep][SPL];
-    auto read = [&](int s) {
+    auto read = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
         const int k = s * kStep + j;
@@ -222,32 +226,32 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
         if constexpr (kOut) part[buf][s * kStep + j][wave][lane] = y;
         else sum += dd.x;
       }
+      if constexpr (!kOut) {       // (no write keeps the steps apart: what they form is not to be formed all at once)
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) asm volatile("" : "+v"(h[i]));
+        lds_order();
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  In x[TW], z[TW];                                           // of the tile being walked
-  auto keep = [&]() {
-#pragma unroll
-    for (int q = 0; q < TW; ++q) { x[q] = rx[q]; z[q] = rz[q]; }
-  };
-  auto finish = [&](int buf, const In (&xs)[TW], const In (&zs)[TW], int left) {
+  auto finish = [&](int buf, const Operands& r, auto whole, int left) __attribute__((always_inline)) {
     if constexpr (kOut) {
       uint32_t off = at_out;
       asm("" : "+v"(off));
       float y[TW];
 #pragma unroll
       for (int q = 0; q < TW; ++q) {
-        y[q] = skip * Elem<In>::load(&xs[q], 0);
+        y[q] = skip * Elem<In>::load(&r.x[q], 0);
 #pragma unroll
         for (int w = 0; w < NW; ++w) y[q] += part[buf][wave * TW + q][w][lane];
       }
       if (in.z) {
 #pragma unroll
-        for (int q = 0; q < TW; ++q) y[q] *= step_silu(Elem<In>::load(&zs[q], 0));
+        for (int q = 0; q < TW; ++q) y[q] *= step_silu(Elem<In>::load(&r.z[q], 0));
       }
 #pragma unroll
       for (int q = 0; q < TW; ++q)
-        if (wave * TW + q < left && mine) {
+        if ((decltype(whole)::value || wave * TW + q < left) && mine) {
           auto* to = (__attribute__((address_space(1))) char*)(out_at + q * p.out_stride);
           asm("" : "+s"(to));
           Out v;
@@ -257,48 +261,49 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave) scan_kernel(SelectiveLaunch
       out_at += TT * p.out_stride;
     }
   };
-  const int64_t tiles = first < end ? (end - first) / TT : 0;
-  const int tail = first < end ? (int)((end - first) % TT) : 0;
-  int buf = 0;
+  const int tokens = first < end ? (int)(end - first) : 0, tiles = tokens / TT, tail = tokens % TT;
   if (tiles > 0) {
-    fetch();
-    stage(0, TT);
-    keep();
+    fetch(set[0]);
+    stage(0, set[0], Par<1>{}, TT);
     advance(tiles > 1);
-    fetch();
+    fetch(set[1]);
     lds_sync();
-    for (int64_t k = 0; k < tiles; ++k, buf ^= 1) {
-      walk(buf);
-      // the next tile: staged behind this one, its successor fetched (the last one again where there is none)
-      stage(buf ^ 1, TT);
-      In was_x[TW], was_z[TW];
-#pragma unroll
-      for (int q = 0; q < TW; ++q) { was_x[q] = x[q]; was_z[q] = z[q]; }
-      keep();
-      advance(k + 2 < tiles);
-      fetch();
+    // Tile k: walked; the next one staged behind it; finished; the one after the next fetched (the
+    // last one again where there is none).
+    auto turn = [&](auto parity, int k) __attribute__((always_inline)) {
+      constexpr int kBuf = decltype(parity)::value;
+      walk(kBuf);
+      stage(1 - kBuf, set[1 - kBuf], Par<1>{}, TT);
       lds_sync();
-      finish(buf, was_x, was_z, TT);
+      finish(kBuf, set[kBuf], Par<1>{}, TT);
+      advance(k + 2 < tiles);
+      fetch(set[kBuf]);
+    };
+    int k = 0;
+    for (; k + 1 < tiles; k += 2) {
+      turn(Par<0>{}, k);
+      turn(Par<1>{}, k + 1);
     }
+    if (k < tiles) turn(Par<0>{}, k);
     advance(true);
   }
   if (tail > 0) {
-    // (`buf` is the other one than the last walk's, which may still be read)
+    Operands r;
 #pragma unroll
     for (int q = 0; q < TW; ++q) {
       const bool there = wave * TW + q < tail;
-      rx[q] = there ? of(x_at + q * in.x_stride, at_c) : In(0);
-      rdt[q] = there ? of(dt_at + q * in.dt_stride, at_c) : In(0);
-      if (kOut) rz[q] = there ? of(z_at + q * z_stride, at_c) : In(0);
+      r.x[q] = there ? of(x_at + q * in.x_stride, at_c) : In(0);
+      r.dt[q] = there ? of(dt_at + q * in.dt_stride, at_c) : In(0);
+      if (kOut) r.z[q] = there ? of(z_at + q * z_stride, at_c) : In(0);
     }
 #pragma unroll
-    for (int k = 0; k < kFill; ++k) rbc[k] = bc_token[k] < tail ? *bc_at[k] : In(0);
-    stage(buf, tail);
-    keep();
+    for (int k = 0; k < kFill; ++k) r.bc[k] = bc_token[k] < tail ? *bc_at[k] : In(0);
+    lds_sync();                     // (the last turns' buffers have been read)
+    stage(0, r, Par<0>{}, tail);
     lds_sync();
-    walk(buf);
+    walk(0);
     lds_sync();
-    finish(buf, x, z, tail);
+    finish(0, r, Par<0>{}, tail);
   }
   if (!mine) return;
   if constexpr (kPass == kStates) {
