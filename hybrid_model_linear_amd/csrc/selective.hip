@@ -410,11 +410,12 @@ void launch_update(const SelectiveLaunch& p, hipStream_t stream) {
 #define UPDATE(ROWS, VEC)                                                                                             \
   hipLaunchKernelGGL((update_kernel<In, Out, NS, ROWS, VEC>), dim3((unsigned)(blocks * ((p.N + ROWS - 1) / ROWS))), \
                      dim3(256), 0, stream, p, in, (int)blocks)
-  // One row a workgroup while that leaves places free: latency.
+  // One row a workgroup while that leaves places free (latency), else two: 256 rows x 4096 channels
+  // 31.2 us with one, 29.9 with two, 31.2 with four, 38 with eight.
   if (blocks * p.N < 4096) {
     if (vec) UPDATE(1, true); else UPDATE(1, false);
   } else {
-    if (vec) UPDATE(4, true); else UPDATE(4, false);
+    if (vec) UPDATE(2, true); else UPDATE(2, false);
   }
 #undef UPDATE
 }
