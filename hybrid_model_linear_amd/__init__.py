@@ -616,6 +616,9 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
         # without a speculative buffer the verify pass would write the state after the
         # rejected draft tokens into the pool (and read a token tree as a chain)
         raise ValueError("target verify needs forward_batch.spec_states and spec_state_slots")
+    norm_weight = getattr(layer, "norm_weight", None)
+    if z is not None and (norm_weight is None or z.shape != (T, H_v * d_v)):
+        raise ValueError(f"z [{T}, {H_v * d_v}] goes with layer.norm_weight")
     conv_w = getattr(layer, "conv_weight", None)
     if conv_w is not None:
         if conv_w.dim() == 3:
@@ -648,7 +651,7 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
                    spec_parent=getattr(forward_batch, "spec_parents", None) if verify else None,
                    keep_pool=verify)
     if z is not None:
-        o = rms_norm(o, layer.norm_weight, eps=float(getattr(layer, "norm_eps", 1e-6)), gate=z.view(T, H_v, d_v))
+        o = rms_norm(o, norm_weight, eps=float(getattr(layer, "norm_eps", 1e-6)), gate=z.view(T, H_v, d_v))
     return o.view(T, H_v * d_v)
 
 

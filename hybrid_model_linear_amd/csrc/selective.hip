@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
   int64_t seg_row = 0;
   if constexpr (kPass != kWhole) {
     const int len = (int)p.seg_len;
-    pieces = max(1, min(((int)(end - first) + len - 1) / len, p.segs));
+    pieces = max(1, min((int)(((uint32_t)(end - first) + len - 1) / (uint32_t)len), p.segs));
     if (seg >= (kPass == kStates ? pieces - 1 : pieces)) return;
     seg_row = 2 * ((int)first / len) * p.D;
     last = seg == pieces - 1;
@@ -108,7 +108,10 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
     for (int s = 1; s < seg; ++s) {
       const float sum = p.seg_delta[seg_row + s * p.D + c];
 #pragma unroll
-      for (int i = 0; i < SPL; ++i) h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(sum * A[i]), from[s * row + i]);
+      for (int i = 0; i < SPL; ++i) {
+        const float e = from[s * row + i];     // (a state of 0 stays 0 where a growing factor overflows)
+        h[i] = h[i] != 0.0f ? fmaf(h[i], __builtin_amdgcn_exp2f(sum * A[i]), e) : e;
+      }
     }
   } else {
 #pragma unroll

@@ -38,7 +38,7 @@ def _matrix(t, name: str, shape, dtype) -> int:
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {tuple(t.shape)}")
     row, col = t.stride()
-    if col != 1 and shape[1] > 1:
+    if col != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name} must have unit column stride (strides {t.stride()})")
     return row if shape[0] > 1 else shape[1]
 
@@ -51,7 +51,7 @@ def _grouped(t, name: str, n: int, states: int, dtype) -> tuple[int, int]:
         raise ValueError(f"{name} must be {dtype} [{n}, G, {states}] or [{n}, {states}], got {t.dtype} {tuple(t.shape)}")
     g = t.shape[1]
     row, group, col = t.stride()
-    if (states > 1 and col != 1) or (g > 1 and group != states):
+    if n > 0 and ((states > 1 and col != 1) or (g > 1 and group != states)):
         raise ValueError(f"{name} must have contiguous groups (strides {t.stride()})")
     return row if n > 1 else g * states, g
 
@@ -159,7 +159,7 @@ def _token_rows(t, name: str, shape, dtype=None) -> int:
     if t.shape != shape or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name} must be {dtype or 'a tensor'} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     st = t.stride()
-    if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
+    if shape[0] > 0 and ((shape[-1] > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2])):
         raise ValueError(f"{name} must have contiguous rows (strides {st})")
     if shape[0] > 1:
         return st[0]

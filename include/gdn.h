@@ -610,7 +610,7 @@ int64_t gdn_kv_evict_workspace_size(const gdn_kv_evict_args* args);
  * in fp32, rounded once (nearest even) to out_dtype.
  *   x, dt, z, out : [T, D]; B, C : [T, G, states], groups contiguous; token strides of
  *                   at least a row; aligned to their element.  x, dt, B, C, z: in_dtype
- *   A             : fp32 [D, states], 16-byte aligned (the decay's factor itself, negative
+ *   A             : fp32 [D, states], 16-byte aligned (the exponent's factor itself, negative
  *                   in such layers, not its logarithm)
  *   D_skip, dt_bias : fp32 [D] or NULL (zero)
  *   pool          : fp32 [num_slots, D, states], 16-byte aligned, read and written in place
@@ -675,7 +675,8 @@ int gdn_selective_update(const gdn_selective_args* args, void* stream);
  *     u = x;  residual: u = x + residual, and residual becomes u (rounded to its type);
  *     gate and gate_first: u = x g sigmoid(g)
  *     y = u / sqrt(mean(u^2) + eps) (weight + offset);  gate and not gate_first: y g sigmoid(g)
- * in fp32, from the sum before its rounding.  weight [d] is shared by the H parts (NULL: y
+ * in fp32 (whose range the sum of u^2 must not leave), from the sum x + residual before its
+ * rounding.  weight [d] is shared by the H parts (NULL: y
  * without it and offset).  out: bf16 or fp32, or e4m3 codes with y = code * scale:
  * scale[t, k] belongs to the k-th `group` values of the token's H d (the last group may be
  * shorter; group 0: the whole row) and is max |y| / 448, at least 2^-64; a code is y / scale

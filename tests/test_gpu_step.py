@@ -50,7 +50,7 @@ def scan_case(rng, lens, D, S, G, dtype, *, skip=(), pad=0, z=True, skipw=True, 
         c["D"] = None
     if not bias:
         c["dt_bias"] = None
-    proj = up(np.concatenate([np.zeros((T, 3)), h["B"].reshape(T, -1), h["C"].reshape(T, -1)], 1), dtype)
+    proj = up(np.concatenate([np.zeros((T, 3)), h["B"].reshape(T, G * S), h["C"].reshape(T, G * S)], 1), dtype)
     g = dict(x=up(h["x"], dtype), dt=up(h["dt"], dtype), A=up(f["A"], F32), B=proj[:, 3:3 + G * S].unflatten(1, (G, S)),
              C=proj[:, 3 + G * S:].unflatten(1, (G, S)), slot=i32(slot), pool=up(f["pool"], F32), cu=i32(c["cu"]),
              D=up(c["D"], F32), dt_bias=up(c["dt_bias"], F32), z=None)

@@ -39,6 +39,32 @@ def test_scan_in_segments(gdn_lib, S, G, dtype, hint):
         assert (ws[need:] == 0xFF).all(), "past the workspace"
 
 
+def test_scan_without_tokens(gdn_lib):
+    """T = 0: every slot keeps its state, or is cleared."""
+    print("[case] no tokens", flush=True)
+    rng = np.random.default_rng(9)
+    c, g = scan_case(rng, [0, 0, 0], 40, 16, 1, BF)
+    before = g["pool"].clone()
+    assert call_scan(gdn_lib, g, has_init=i32([1, 0, 1])).shape == (0, 40)
+    cleared = int(c["slot"][1])
+    assert (g["pool"][cleared] == 0).all()
+    before[cleared] = 0
+    assert torch.equal(g["pool"], before)
+
+
+def test_scan_segments_with_growing_states(gdn_lib):
+    """Positive factors that overflow over a segment leave states of 0 as they are."""
+    print("[case] growing", flush=True)
+    rng = np.random.default_rng(10)
+    c, g = scan_case(rng, [1200], 64, 16, 1, F32, z=False, skipw=False)
+    for t in (g["x"], g["pool"]):
+        t.zero_()
+    g["A"].fill_(3.0)
+    g["dt"].fill_(2.0)
+    out = call_scan(gdn_lib, g, max_seqlen=1200)
+    assert (out == 0).all() and (g["pool"] == 0).all()
+
+
 def test_scan_workspace_refusals_and_without_one(gdn_lib):
     print("[case] workspace", flush=True)
     rng = np.random.default_rng(1)
@@ -291,6 +317,10 @@ def test_forward_gdn_with_its_gated_norm(gdn_lib, mode):
     plain = gdn_lib.forward_gdn(layer, fb(), mixed, a, b)
     got = gdn_lib.forward_gdn(layer, fb(), mixed, a, b, z)
     assert got.shape == (T, 512)
+    with pytest.raises(ValueError):
+        gdn_lib.forward_gdn(SimpleNamespace(**{**vars(layer), "norm_weight": None}), fb(), mixed, a, b, z)
+    with pytest.raises(ValueError):
+        gdn_lib.forward_gdn(layer, fb(), mixed, a, b, z[:, :256])
     check_norm(dict(x=host(plain).reshape(T, 4, 128), weight=host(layer.norm_weight), gate=host(z).reshape(T, 4, 128), residual=None),
                got, None, BF, 0, "gated")
 
