@@ -3,8 +3,8 @@
 // memory is the bound, so a row stays on chip between its two reductions (the parts' sums of
 // squares, and in 8 bits the groups' maxima).
 //   row_kernel : a row in the registers of 1, 4 or 16 waves, 8 values per thread and piece.
-//   lds_kernel : parts that no power of two of lanes covers: the row in LDS.  Rows too long
-//                for either are read again for each pass (from the caches).
+//   lds_kernel : parts that no power of two of lanes covers, and rows of fewer than 8 values: the
+//                row in LDS.  Rows too long for either are read again for each pass (from the caches).
 #include "step_launch.h"
 #include "step_math.h"
 
@@ -39,136 +39,118 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 }
 
 // ------------------------------------------------------------------ rows in registers
-// Eight values in a row from element i on, n of them there (the others are 0 and not written).
-// kWhole: all eight, in aligned pieces; else at any element (the card takes wide loads and
-// stores at any address), with a row's last values one by one.
+// Eight values from element i of a row operand on.  kWhole: in aligned pieces; else at any
+// element (the card takes wide loads and stores at any address).
 struct __attribute__((packed, aligned(1))) Loose4 { uint32_t u[4]; };
 struct __attribute__((packed, aligned(1))) Loose2 { uint32_t u[2]; };
 
 template <bool kWhole>
-__device__ __forceinline__ void load_values(const void* p, int bf16, int64_t i, int n, float (&v)[8]) {
-  if (!kWhole && n < 8) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = k >= n ? 0.0f : bf16 ? bf16_to_f32(static_cast<const u16*>(p)[i + k]) : static_cast<const float*>(p)[i + k];
-    return;
-  }
-  if (bf16) {
-    const u16* at = static_cast<const u16*>(p) + i;
-    uint32_t u[4];
-    if constexpr (kWhole) {
-      const uint4 w = *reinterpret_cast<const uint4*>(at);
-      u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
-    } else {
-      const Loose4 w = *reinterpret_cast<const Loose4*>(at);
-      u[0] = w.u[0]; u[1] = w.u[1]; u[2] = w.u[2]; u[3] = w.u[3];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(u[k] << 16);
-      v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-    }
+__device__ __forceinline__ Loose4 load_piece(const void* p) {
+  if constexpr (kWhole) {
+    const uint4 w = *static_cast<const uint4*>(p);
+    return {{w.x, w.y, w.z, w.w}};
   } else {
-    const float* at = static_cast<const float*>(p) + i;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if constexpr (kWhole) {
-        const float4 w = reinterpret_cast<const float4*>(at)[k];
-        v[4 * k] = w.x; v[4 * k + 1] = w.y; v[4 * k + 2] = w.z; v[4 * k + 3] = w.w;
-      } else {
-        const Loose4 w = reinterpret_cast<const Loose4*>(at)[k];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) v[4 * k + m] = __uint_as_float(w.u[m]);
-      }
-    }
+    return *static_cast<const Loose4*>(p);
   }
 }
 template <bool kWhole>
-__device__ __forceinline__ void store_values(void* p, int bf16, int64_t i, int n, const float (&v)[8]) {
-  if (!kWhole && n < 8) {
+__device__ __forceinline__ void load_values(const void* p, int bf16, int64_t i, float (&v)[8]) {
+  if (bf16) {
+    const Loose4 w = load_piece<kWhole>(static_cast<const u16*>(p) + i);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) {
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w.u[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w.u[k] & 0xffff0000u);
+    }
+  } else {
+    const Loose4 a = load_piece<kWhole>(static_cast<const float*>(p) + i), b = load_piece<kWhole>(static_cast<const float*>(p) + i + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = __uint_as_float(a.u[k]);
+      v[4 + k] = __uint_as_float(b.u[k]);
+    }
+  }
+}
+// The values from `lo` on are written (0: all; 8: none).
+template <bool kWhole>
+__device__ __forceinline__ void store_piece(void* p, const Loose4& w) {
+  if constexpr (kWhole) *static_cast<uint4*>(p) = make_uint4(w.u[0], w.u[1], w.u[2], w.u[3]);
+  else *static_cast<Loose4*>(p) = w;
+}
+template <bool kWhole>
+__device__ __forceinline__ void store_values(void* p, int bf16, int64_t i, int lo, const float (&v)[8]) {
+  if (lo == 0) {
+    if (bf16) {
+      bf16x8 b;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = (__bf16)v[k];
+      store_piece<kWhole>(static_cast<u16*>(p) + i, __builtin_bit_cast(Loose4, b));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        store_piece<kWhole>(static_cast<float*>(p) + i + 4 * k,
+                            __builtin_bit_cast(Loose4, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3])));
+    }
+  } else if (!kWhole && lo < 8) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (k >= lo) {
         if (bf16) static_cast<u16*>(p)[i + k] = f32_to_bf16(v[k]);
         else static_cast<float*>(p)[i + k] = v[k];
       }
-    return;
-  }
-  if (bf16) {
-    bf16x8 b;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) b[k] = (__bf16)v[k];
-    u16* at = static_cast<u16*>(p) + i;
-    if constexpr (kWhole) *reinterpret_cast<bf16x8*>(at) = b;
-    else *reinterpret_cast<Loose4*>(at) = __builtin_bit_cast(Loose4, b);
-  } else {
-    float* at = static_cast<float*>(p) + i;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 w = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-      if constexpr (kWhole) reinterpret_cast<float4*>(at)[k] = w;
-      else reinterpret_cast<Loose4*>(at)[k] = __builtin_bit_cast(Loose4, w);
-    }
   }
 }
 template <bool kWhole>
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int lo, const float (&v)[8]) {
   int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
   int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
   b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
-  if constexpr (kWhole) {
-    *reinterpret_cast<uint2*>(p + i) = make_uint2((uint32_t)a, (uint32_t)b);
-  } else if (n == 8) {
-    *reinterpret_cast<Loose2*>(p + i) = {{(uint32_t)a, (uint32_t)b}};
-  } else {
+  if (lo == 0) {
+    if constexpr (kWhole) *reinterpret_cast<uint2*>(p + i) = make_uint2((uint32_t)a, (uint32_t)b);
+    else *reinterpret_cast<Loose2*>(p + i) = {{(uint32_t)a, (uint32_t)b}};
+  } else if (!kWhole && lo < 8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[i + k] = (uint8_t)((k < 4 ? a : b) >> (k % 4 * 8));
+    for (int k = 1; k < 8; ++k)
+      if (k >= lo) p[i + k] = (uint8_t)((k < 4 ? a : b) >> (k % 4 * 8));
   }
 }
 
-// A row of W = H d <= 512 K RW values over RW waves: piece j of thread r holds the values
-// 8 (64 RW j + r) on.  part_lanes: lanes of a part for H > 1 (d / 8, a power of two up to 64).
-// A value past W is 0 and takes part in nothing.
+// A row of W = H d values, 8 <= W <= 512 K RW, over RW waves: piece j of thread r holds the values
+// 8 (64 RW j + r) on.  A row's last piece, where it is short, begins earlier, at W - 8, and its
+// first `lo` values, which are another piece's too, are 0 and not written; a piece past the row
+// is all of that: every load is whole, in the row, and under no branch (one that is waits for its
+// data before the next is sent).  part_lanes: lanes of a part for H > 1 (d / 8, a power of two up
+// to 64).
 template <bool kWhole, int K, int RW>
 __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaunch p, int part_lanes) {
   constexpr int kRows = RW >= 4 ? 1 : 4 / RW, kRowThreads = RW * kWave;
   __shared__ float sums[kRows][RW], tops[kRows][RW];
   const int row = threadIdx.x / kRowThreads, r = threadIdx.x % kRowThreads, wave = r / kWave;
-  const int64_t t = (int64_t)blockIdx.x * kRows + row;
+  const int64_t asked = (int64_t)blockIdx.x * kRows + row, t = min(asked, p.T - 1);
   const int W = p.H * p.d;
   float u[K][8], g[K][8];
-  int at[K], n[K];                                          // a piece's first value and how many are there
+  int at[K], lo[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    at[j] = (j * kRowThreads + r) * 8;
-    n[j] = t < p.T ? max(0, min(8, W - at[j])) : 0;
+    const int from = (j * kRowThreads + r) * 8;
+    at[j] = min(from, W - 8);
+    lo[j] = asked < p.T ? min(from - at[j], 8) : 8;
   }
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v) u[j][v] = 0.0f;
-    if (n[j] > 0) load_values<kWhole>(p.x, p.in_bf16, t * p.x_stride + at[j], n[j], u[j]);
-  }
+  for (int j = 0; j < K; ++j) load_values<kWhole>(p.x, p.in_bf16, t * p.x_stride + at[j], u[j]);
   if (p.residual) {
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-      if (n[j] > 0) load_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], n[j], g[j]);
+    for (int j = 0; j < K; ++j) load_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], g[j]);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (n[j] == 0) continue;
 #pragma unroll
       for (int v = 0; v < 8; ++v) u[j][v] += g[j][v];
-      store_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], n[j], u[j]);
+      store_values<kWhole>(p.residual, p.residual_bf16, t * p.residual_stride + at[j], lo[j], u[j]);
     }
   } else if (p.gate) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-#pragma unroll
-      for (int v = 0; v < 8; ++v) g[j][v] = 0.0f;
-      if (n[j] > 0) load_values<kWhole>(p.gate, p.in_bf16, t * p.gate_stride + at[j], n[j], g[j]);
-    }
+    for (int j = 0; j < K; ++j) load_values<kWhole>(p.gate, p.in_bf16, t * p.gate_stride + at[j], g[j]);
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
@@ -177,6 +159,10 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
         if (p.gate_first) u[j][v] *= g[j][v];
       }
   }
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int v = 0; v < 8; ++v) u[j][v] = v < lo[j] ? 0.0f : u[j][v];
   // 1 / sqrt(mean + eps) of every piece's part
   float rstd[K];
   if (p.H == 1) {
@@ -207,9 +193,9 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
   }
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (p.weight && n[j] > 0) {
+    if (p.weight) {
       float w[8];
-      load_values<kWhole>(p.weight, p.weight_bf16, p.H == 1 ? at[j] : at[j] & (p.d - 1), n[j], w);   // (parts are powers of two)
+      load_values<kWhole>(p.weight, p.weight_bf16, p.H == 1 ? at[j] : at[j] & (p.d - 1), w);   // (parts are powers of two)
 #pragma unroll
       for (int v = 0; v < 8; ++v) u[j][v] *= rstd[j] * (w[v] + p.offset);
     } else {
@@ -224,7 +210,7 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
   if (p.out_dtype != GDN_E4M3) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (n[j] > 0) store_values<kWhole>(p.out, p.out_dtype == GDN_BF16, t * p.out_stride + at[j], n[j], u[j]);
+      store_values<kWhole>(p.out, p.out_dtype == GDN_BF16, t * p.out_stride + at[j], lo[j], u[j]);
     return;
   }
   // the groups' largest magnitudes (fmaxf passes NaN over; infinities are looked for)
@@ -265,16 +251,17 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = lanes_max(top[j], p.group / 8);
   }
-  const int shift = p.groups == 1 ? 20 : p.group == 64 ? 6 : 7;
+  const int shift = p.group == 64 ? 6 : 7;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (n[j] == 0) continue;
+    if (lo[j] == 8) continue;
     const float scale = fmaxf(top[j] / 448.0f, kMinScale), inv = 1.0f / scale;
-    if ((at[j] & ((1 << shift) - 1)) == 0) p.scale[t * p.groups + (at[j] >> shift)] = scale;
+    const int from = at[j] + lo[j];                         // (a multiple of 8)
+    if (p.groups == 1 ? from == 0 : (from & (p.group - 1)) == 0) p.scale[t * p.groups + (p.groups == 1 ? 0 : from >> shift)] = scale;
     float c[8];
 #pragma unroll
     for (int v = 0; v < 8; ++v) c[v] = u[j][v] * inv;
-    store_codes<kWhole>(static_cast<uint8_t*>(p.out), t * p.out_stride + at[j], n[j], c);
+    store_codes<kWhole>(static_cast<uint8_t*>(p.out), t * p.out_stride + at[j], lo[j], c);
   }
 }
 
@@ -394,7 +381,7 @@ hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream) {
                      reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
   const int lanes = p.d / 8;
   const bool parts = p.H == 1 || (p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
-  if (parts && W <= 32768) {
+  if (parts && W >= 8 && W <= 32768) {
     if (whole) launch_row_sizes<true>(p, W, lanes, stream); else launch_row_sizes<false>(p, W, lanes, stream);
   } else if ((W + p.H) * 4 <= 65536) {
     hipLaunchKernelGGL(lds_kernel<true>, dim3((unsigned)p.T), dim3(256), (W + p.H) * sizeof(float), stream, p);
