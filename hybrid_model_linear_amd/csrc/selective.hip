@@ -3,9 +3,10 @@
 //   h[i] = exp(delta A[c, i]) h[i] + delta x B[i],   y = sum_i C[i] h[i] + D_skip[c] x
 //
 // The scan's bound is vector arithmetic: per token, channel and state a product, an
-// exponential (the time of two to three other instructions here), a product and two fused
-// ones, ~25 cycles of a SIMD for 64 of them, where the bytes of a token and channel are 8
-// (16 states: 0.41 ms of instructions to 0.19 ms of memory at 32768 tokens x 4096 channels).
+// exponential (the time of two other instructions), a product and two fused ones, ~26 cycles
+// of a SIMD for 64 of them, where the bytes of a token and channel are 8 (at 32768 tokens x 4096
+// channels, 16 states: 0.44 ms of instructions, softplus and gate among them, to 0.19 ms of
+// memory; measured 0.56 ms).
 // A lane is a channel, the states are dealt out over the 4 or 8 waves of a workgroup: so
 // each wave reads B and C of its states as broadcasts, whole rows of x, dt, z are read and
 // written, and what there is once per token and channel (softplus, gate, conversions) is
@@ -452,8 +453,9 @@ void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus) {
   // In tokens of one workgroup: uncut, the longest sequence walks alone while the others share
   // the chip, which is full at 1.4 workgroups of four waves per CU (0.7 of eight); cut, all
   // tokens cost 1.5 times as much (the states are formed twice), plus one segment and a launch.
-  // Measured, us, 16 states, uncut / cut: one of 4096 x 4096 channels 429 / 135, two 428 / 249, four
-  // 451 / 441, eight 617 / 811; one of 256 x 1024 32 / 17; 8192 and 31 of 500 x 4096 922 / 686.
+  // Measured, us, 16 states, uncut / cut: one of 4096 x 4096 channels 400 / 124, two 400 / 232, four
+  // 409 / 411, eight 569 / 758; one of 256 x 1024 31 / 20; 8192 and 31 of 500 x 4096 824 / 520; the
+  // rule is within 10% of the best number of segments over 18 such shapes.
   // Segments: four workgroups (two of eight waves) a CU, no shorter than two tiles.
   p.segs = 1;
   p.seg_len = longest;
