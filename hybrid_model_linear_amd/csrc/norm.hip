@@ -311,8 +311,10 @@ __global__ void __launch_bounds__(256) lds_kernel(NormLaunch p) {
     if (lane == 0) rstd[h] = 1.0f / sqrtf(sum / (float)p.d + p.eps);
   }
   __syncthreads();
+  const float per_d = 1.0f / (float)p.d;
   auto result = [&](int e, float u) {
-    const int h = e / p.d, i = e - h * p.d;
+    // e / d: (e + 1/2) / d is at least 1/2d from a whole number, the product off by less (e < 2^21)
+    const int h = (int)(((float)e + 0.5f) * per_d), i = e - h * p.d;
     float y = u * rstd[h];
     if (p.weight) y *= load_any(p.weight, p.weight_bf16, i) + p.offset;
     if (p.gate && !p.gate_first) y *= step_silu(load_any(p.gate, p.in_bf16, gr + e));

@@ -22,6 +22,7 @@ from .attention import _at, _attach, _need, _place, _run, _table, _vec
 
 _BF16, _F32, _I32, _I64, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
 _CODES = {_BF16: GDN_BF16, _F32: GDN_F32}
+_MOST = 2 ** 31 - 1          # (ctypes cuts larger numbers silently)
 _OUT_CODES = {_BF16: GDN_BF16, _F32: GDN_F32, _F8: GDN_E4M3}
 
 
@@ -84,7 +85,7 @@ def _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_so
         dt.data_ptr(), _matrix(dt, "dt", shape, kind), B.data_ptr(), bs, C.data_ptr(), cs, _at(z),
         0 if z is None else _matrix(z, "z", shape, kind), A.data_ptr(), _vec(D, "D", width, _F32),
         _vec(dt_bias, "dt_bias", width, _F32), _vec(cu_seqlens, "cu_seqlens", N + 1), _vec(slot, "slot", N),
-        _vec(has_init, "has_init", N), pool.data_ptr(), pool.shape[0], o, os, max_seqlen, 1 if keep_pool else 0, None, 0), i
+        _vec(has_init, "has_init", N), pool.data_ptr(), pool.shape[0], o, os, min(max_seqlen, _MOST), 1 if keep_pool else 0, None, 0), i
 
 
 def _new_out(x, out_dtype):
@@ -190,8 +191,10 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, offset: float = 0.0, residual
     if out_code is None:
         raise ValueError(f"out must be bf16, fp32 or float8_e4m3fn, got {out.dtype}")
     f8 = out_code == GDN_E4M3
+    if group not in (0, 64, 128):
+        raise ValueError(f"group must be 0, 64 or 128, got {group}")
     if f8:
-        groups = -(-H * d // group) if group > 0 else 1
+        groups = -(-H * d // group) if group else 1
         if scale is None:
             scale = x.new_empty((T, groups), dtype=_F32)
         elif scale.dtype is not _F32 or scale.shape != (T, groups) or not scale.is_contiguous():
@@ -247,6 +250,11 @@ class StepPlan(NamedTuple):
     seq: torch.Tensor
 
 
+def _page(page: int) -> None:
+    if not 1 <= page <= 1 << 30:
+        raise ValueError(f"page must be in [1, 2^30], got {page}")
+
+
 def plan_pages(pool: PagePool, block_table, held, new, page: int, tokens: int, *, start=None,
                out: StepPlan | None = None) -> StepPlan:
     """The lengths, block-table entries and slot maps of a step, formed on the GPU.  Request n
@@ -263,6 +271,9 @@ def plan_pages(pool: PagePool, block_table, held, new, page: int, tokens: int, *
     N = held.shape[0]
     i = _place(pool._state, block_table, held, new, start)
     ts, tw = _table(block_table, N)
+    _page(page)
+    if not 0 <= tokens <= _MOST:
+        raise ValueError(f"tokens must be in [0, 2^31), got {tokens}")
     if out is None:      # (two allocations; the tensors are parts of them)
         small = held.new_empty(3 * N + 1 + 2 * tokens).split_with_sizes((N + 1, N, N, tokens, tokens))
         out = StepPlan(small[0], small[1], small[2], held.new_empty(tokens, dtype=_I64), small[3], small[4])
@@ -283,6 +294,7 @@ def release_pages(pool: PagePool, block_table, keep, held, page: int) -> None:
     back to `pool`, requests and pages in order (keep[n] = 0: all of them; keep[n] < 0 or
     held[n] <= keep[n]: none).  block_table is left as it is."""
     lib = _lib.load()
+    _page(page)
     N = held.shape[0]
     i = _place(pool._state, block_table, keep, held)
     ts, tw = _table(block_table, N)

@@ -616,7 +616,9 @@ int64_t gdn_kv_evict_workspace_size(const gdn_kv_evict_args* args);
  *   pool          : fp32 [num_slots, D, states], 16-byte aligned, read and written in place
  * Supported: states in {8, 16, 32, 64, 128} (else GDN_E_UNSUPPORTED), D % G == 0, in_dtype
  * and out_dtype bf16 or fp32.  out must not overlap x, dt, B, C, z or the pool (address
- * ranges, else GDN_E_SHAPE).
+ * ranges, else GDN_E_SHAPE).  D is at most 2^24; calls whose launch would have 2^32 threads
+ * or more (512 for each 64 channels of a group, sequence and segment; segments are left out
+ * first) are GDN_E_UNSUPPORTED.
  *
  * gdn_selective_scan: packed prompts.  cu_seqlens, slot, has_init (NULL = all 1), padding
  * tokens, skipped and empty sequences as gdn_extend; keep_pool != 0 leaves the pool as it
@@ -686,7 +688,8 @@ int gdn_selective_update(const gdn_selective_args* args, void* stream);
  *   H d values contiguous, token strides of at least H d; aligned to their element
  *   scale : fp32 [T, ceil(H d / group)], contiguous (e4m3 only, else ignored)
  * Supported: bf16 or fp32 x, weight and residual; group 0, 64 or 128 (else
- * GDN_E_UNSUPPORTED); H at most 8192, H d at most 2^20; not both a gate and a residual (GDN_E_UNSUPPORTED).
+ * GDN_E_UNSUPPORTED); H at most 8192, H d at most 2^20; T below 2^24 and not
+ * both a gate and a residual (else GDN_E_UNSUPPORTED).
  * out, scale and residual must not overlap each other or an input (address ranges, else
  * GDN_E_SHAPE).  One launch. */
 typedef struct gdn_rms_norm_args {

@@ -164,6 +164,9 @@ def test_binding_refuses_host_tensors_and_shapes():
         gdn.rms_norm(x.half())
     with pytest.raises(ValueError, match="float8_e4m3fn"):
         gdn.rms_norm(x, out_dtype=torch.float16)
+    for group in (32, 1 << 32):
+        with pytest.raises(ValueError, match="group must be"):
+            gdn.rms_norm(x, out_dtype=torch.float8_e4m3fn, group=group)
     with pytest.raises(ValueError, match="scale goes with"):
         gdn.rms_norm(x, scale=torch.zeros(4, 1))
     with pytest.raises(ValueError, match="scale must be"):
@@ -174,6 +177,21 @@ def test_binding_refuses_host_tensors_and_shapes():
         gdn.PagePool(torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="int32 vector"):
         gdn.PagePool(torch.zeros(9))
+
+
+def test_pages_refuse_numbers_that_do_not_fit():
+    pool = object.__new__(gdn.PagePool)
+    t, e = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pool._state, pool._capacity = torch.zeros(9, dtype=torch.int32), 7
+    from unittest import mock
+    from hybrid_model_linear_amd import step
+    with mock.patch.object(step, "_place", return_value=0):
+        for page, tokens in ((0, 4), ((1 << 32) + 16, 4), (16, -1), (16, 1 << 31)):
+            with pytest.raises(ValueError):
+                gdn.plan_pages(pool, t, e, e, page, tokens)
+        for page in (0, (1 << 32) + 16):
+            with pytest.raises(ValueError):
+                gdn.release_pages(pool, t, e, e, page)
 
 
 def test_shape_helpers():
