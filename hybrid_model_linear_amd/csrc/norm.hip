@@ -3,8 +3,8 @@
 // memory is the bound, so a row stays on chip between its two reductions (the parts' sums of
 // squares, and in 8 bits the groups' maxima).
 //   row_kernel : a row in the registers of 1, 4 or 16 waves, 8 values per thread and piece.
-//   lds_kernel : parts that no power of two of lanes covers, and rows of fewer than 8 values: the
-//                row in LDS.  Rows too long for either are read again for each pass (from the caches).
+//   lds_kernel : rows or parts of fewer than 8 values: the row in LDS.  Rows too long for either
+//                are read again for each pass (from the caches).
 #include "step_launch.h"
 #include "step_math.h"
 
@@ -121,11 +121,14 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int lo, const
 // first `lo` values, which are another piece's too, are 0 and not written; a piece past the row
 // is all of that: every load is whole, in the row, and under no branch (one that is waits for its
 // data before the next is sent).  part_lanes: lanes of a part for H > 1 (d / 8, a power of two up
-// to 64).
-template <bool kWhole, int K, int RW>
+// to 64); kAny: parts of any size from 8 on, of which a piece meets two at most: their sums are
+// formed from the pieces' in LDS.
+template <bool kWhole, int K, int RW, bool kAny>
 __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaunch p, int part_lanes) {
   constexpr int kRows = RW >= 4 ? 1 : 4 / RW, kRowThreads = RW * kWave;
+  constexpr int kPieces = kAny ? K * kRowThreads : 1;
   __shared__ float sums[kRows][RW], tops[kRows][RW];
+  __shared__ float front[kRows][kPieces], back[kRows][kPieces], part_rstd[kRows][kPieces];
   const int row = threadIdx.x / kRowThreads, r = threadIdx.x % kRowThreads, wave = r / kWave;
   const int64_t asked = (int64_t)blockIdx.x * kRows + row, t = min(asked, p.T - 1);
   const int W = p.H * p.d;
@@ -163,9 +166,39 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
   for (int j = 0; j < K; ++j)
 #pragma unroll
     for (int v = 0; v < 8; ++v) u[j][v] = v < lo[j] ? 0.0f : u[j][v];
-  // 1 / sqrt(mean + eps) of every piece's part
-  float rstd[K];
-  if (p.H == 1) {
+  // 1 / sqrt(mean + eps) of every piece's part (kAny: of its first `cut` values, and of the others)
+  float rstd[K], rstd2[K];
+  int cut[K], part[K];
+  if constexpr (kAny) {
+    const float per_d = 1.0f / (float)p.d;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      // at / d: (at + 1/2) / d is at least 1/2d from a whole number, the product off by less
+      part[j] = (int)(((float)at[j] + 0.5f) * per_d);
+      cut[j] = (part[j] + 1) * p.d - at[j];
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const float sq = u[j][v] * u[j][v];
+        a += v < cut[j] ? sq : 0.0f;
+        b += v < cut[j] ? 0.0f : sq;
+      }
+      front[row][j * kRowThreads + r] = a;
+      back[row][j * kRowThreads + r] = b;
+    }
+    __syncthreads();
+    for (int h = r; h < p.H; h += kRowThreads) {
+      float sum = 0.0f;
+      for (int i = h * p.d / 8; i <= ((h + 1) * p.d - 1) / 8; ++i) sum += min(8 * i, W - 8) >= h * p.d ? front[row][i] : back[row][i];
+      part_rstd[row][h] = 1.0f / sqrtf(sum * per_d + p.eps);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      rstd[j] = part_rstd[row][part[j]];
+      rstd2[j] = part_rstd[row][min(part[j] + 1, p.H - 1)];
+    }
+  } else if (p.H == 1) {
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < K; ++j)
@@ -193,7 +226,17 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
   }
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    if (p.weight) {
+    if constexpr (kAny) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        float w = 1.0f;
+        if (p.weight) {
+          const int i = v < cut[j] ? at[j] + v - part[j] * p.d : v - cut[j];
+          w = (p.weight_bf16 ? bf16_to_f32(static_cast<const u16*>(p.weight)[i]) : static_cast<const float*>(p.weight)[i]) + p.offset;
+        }
+        u[j][v] *= (v < cut[j] ? rstd[j] : rstd2[j]) * w;
+      }
+    } else if (p.weight) {
       float w[8];
       load_values<kWhole>(p.weight, p.weight_bf16, p.H == 1 ? at[j] : at[j] & (p.d - 1), w);   // (parts are powers of two)
 #pragma unroll
@@ -352,25 +395,28 @@ bool wide(const void* p, int64_t stride, int64_t size) {   // 8 values at a time
   return reinterpret_cast<uintptr_t>(p) % piece == 0 && stride * size % piece == 0;
 }
 
-template <bool kWhole, int K, int RW>
+template <bool kWhole, int K, int RW, bool kAny>
 void launch_rows(const NormLaunch& p, int part_lanes, hipStream_t stream) {
   constexpr int kRows = RW >= 4 ? 1 : 4 / RW;
-  hipLaunchKernelGGL((row_kernel<kWhole, K, RW>), dim3((unsigned)((p.T + kRows - 1) / kRows)), dim3(RW > 4 ? RW * kWave : 256), 0,
-                     stream, p, part_lanes);
+  hipLaunchKernelGGL((row_kernel<kWhole, K, RW, kAny>), dim3((unsigned)((p.T + kRows - 1) / kRows)),
+                     dim3(RW > 4 ? RW * kWave : 256), 0, stream, p, part_lanes);
 }
 
-template <bool kWhole>
+template <bool kWhole, bool kAny>
 void launch_row_sizes(const NormLaunch& p, int64_t W, int part_lanes, hipStream_t stream) {
   // A wave a row up to 1024 values where there are rows for every wave of the chip, else four
-  // waves, which are done sooner.
+  // waves, which are done sooner.  (Three pieces a thread where two are too few: with four 777 x 5003
+  // took 12.5 us for 10.9, 5000 x 20000 191 for 172.)
   const bool many = p.T >= 1024;
-  if (many && W <= 512) launch_rows<kWhole, 1, 1>(p, part_lanes, stream);
-  else if (many && W <= 1024) launch_rows<kWhole, 2, 1>(p, part_lanes, stream);
-  else if (W <= 2048) launch_rows<kWhole, 1, 4>(p, part_lanes, stream);
-  else if (W <= 4096) launch_rows<kWhole, 2, 4>(p, part_lanes, stream);
-  else if (W <= 8192) launch_rows<kWhole, 4, 4>(p, part_lanes, stream);
-  else if (W <= 16384) launch_rows<kWhole, 2, 16>(p, part_lanes, stream);
-  else launch_rows<kWhole, 4, 16>(p, part_lanes, stream);
+  if (many && W <= 512) launch_rows<kWhole, 1, 1, kAny>(p, part_lanes, stream);
+  else if (many && W <= 1024) launch_rows<kWhole, 2, 1, kAny>(p, part_lanes, stream);
+  else if (W <= 2048) launch_rows<kWhole, 1, 4, kAny>(p, part_lanes, stream);
+  else if (W <= 4096) launch_rows<kWhole, 2, 4, kAny>(p, part_lanes, stream);
+  else if (W <= 6144) launch_rows<kWhole, 3, 4, kAny>(p, part_lanes, stream);
+  else if (W <= 8192) launch_rows<kWhole, 4, 4, kAny>(p, part_lanes, stream);
+  else if (W <= 16384) launch_rows<kWhole, 2, 16, kAny>(p, part_lanes, stream);
+  else if (W <= 24576) launch_rows<kWhole, 3, 16, kAny>(p, part_lanes, stream);
+  else launch_rows<kWhole, 4, 16, kAny>(p, part_lanes, stream);
 }
 
 }  // namespace
@@ -382,9 +428,11 @@ hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream) {
                      (!p.residual || wide(p.residual, p.residual_stride, res)) && wide(p.out, p.out_stride, out) &&
                      reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
   const int lanes = p.d / 8;
-  const bool parts = p.H == 1 || (p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
-  if (parts && W >= 8 && W <= 32768) {
-    if (whole) launch_row_sizes<true>(p, W, lanes, stream); else launch_row_sizes<false>(p, W, lanes, stream);
+  const bool any = p.H > 1 && !(p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
+  if (W >= 8 && W <= 32768 && (!any || p.d >= 8)) {
+    if (any) launch_row_sizes<false, true>(p, W, lanes, stream);
+    else if (whole) launch_row_sizes<true, false>(p, W, lanes, stream);
+    else launch_row_sizes<false, false>(p, W, lanes, stream);
   } else if ((W + p.H) * 4 <= 65536) {
     hipLaunchKernelGGL(lds_kernel<true>, dim3((unsigned)p.T), dim3(256), (W + p.H) * sizeof(float), stream, p);
   } else {

@@ -244,7 +244,9 @@ def check_norm(h, got, kept, out_dtype, group, what, *, residual=None, **kw):
 
 
 @pytest.mark.parametrize("T,H,d", [(1, 1, 2048), (3, 1, 1), (5, 1, 77), (4, 1, 512), (130, 1, 4096), (7, 1, 5003), (2, 1, 20000),
-                                   (9, 32, 128), (6, 3, 100), (33, 4, 64), (5, 2, 256), (3, 64, 24), (2, 1, 40004), (1, 1, 1 << 20)])
+                                   (9, 32, 128), (6, 3, 100), (33, 4, 64), (5, 2, 256), (3, 64, 24), (2, 1, 40004), (1, 1, 1 << 20),
+                                   (1500, 5, 9), (1100, 37, 27), (4, 37, 100), (3, 11, 8), (2, 700, 17), (2, 3, 5000), (2, 31, 1000),
+                                   (5, 13, 3), (3, 400, 110), (2, 2, 12)])
 @pytest.mark.parametrize("out_dtype,group", [(BF, 0), (F8, 0), (F8, 128), (F8, 64), (F32, 0)])
 def test_norm(gdn_lib, T, H, d, out_dtype, group):
     print("[case] norm", T, H, d, out_dtype, group, flush=True)
