@@ -15,7 +15,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ int64_t pages_of(int64_t rows, int page) { return (rows + page - 1) / page; }
+// ceil(rows / page), rows < 2^31, page <= 2^30
+__device__ __forceinline__ int32_t pages_of(int32_t rows, int32_t page) {
+  return (int32_t)(((uint32_t)rows + (uint32_t)page - 1) / (uint32_t)page);
+}
 
 // Inclusive sums over the workgroup's threads of a pair; `a`, `b` become them.
 __device__ __forceinline__ void scan_pair(int64_t& a, int64_t& b, int64_t (&wave_sums)[2][kThreads / kWave]) {
@@ -81,19 +84,31 @@ struct Request {
   bool live;
 };
 
-__device__ __forceinline__ Request request_of(const PlanPagesLaunch& p, int n) {
+__device__ __forceinline__ Request request_of(const PlanPagesLaunch& p, int32_t held, int32_t add) {
   Request r{};
-  if (n >= p.N) return r;
-  r.held = p.held[n];
-  const int64_t add = p.new_len[n];
-  r.live = r.held >= 0 && add >= 0;
-  if (!r.live) return r;
-  r.tokens = add;
-  r.lo = pages_of(r.held, p.page);
-  const int64_t hi = pages_of(r.held + add, p.page);
-  r.live = hi <= p.table_width && r.held + add <= INT32_MAX;
-  if (r.live) r.need = hi - r.lo;
+  r.held = held;
+  const bool real = held >= 0 && add >= 0;
+  r.tokens = real ? add : 0;
+  const int64_t rows = (int64_t)held + add;
+  const bool fits = real && rows <= INT32_MAX;
+  r.lo = pages_of(real ? held : 0, p.page);
+  const int32_t hi = pages_of(fits ? (int32_t)rows : 0, p.page);
+  r.live = fits && hi <= p.table_width;
+  r.need = r.live ? hi - r.lo : 0;
   return r;
+}
+
+// f(a[m], b[m]) for this thread's m below n, four loads of each at once.
+template <typename Load, typename F>
+__device__ __forceinline__ void for_each_pair(int n, Load load, F f) {
+  for (int m0 = threadIdx.x; m0 < n; m0 += 4 * kThreads) {
+    int32_t a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load(min(m0 + k * kThreads, n - 1), a[k], b[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (m0 + k * kThreads < n) f(a[k], b[k]);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
@@ -105,14 +120,15 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   const int64_t count = min(max((int64_t)p.pool[0], (int64_t)0), p.capacity);
   const int32_t* stack = p.pool + 2;
   int64_t tokens0 = 0, pages0 = 0;
-  for (int n = tid; n < base; n += kThreads) {
-    const Request r = request_of(p, n);
-    tokens0 += r.tokens;
-    pages0 += r.need;
-  }
+  for_each_pair(min(base, p.N), [&](int m, int32_t& a, int32_t& b) { a = p.held[m]; b = p.new_len[m]; },
+                [&](int32_t a, int32_t b) {
+                  const Request r = request_of(p, a, b);
+                  tokens0 += r.tokens;
+                  pages0 += r.need;
+                });
   sum_pair(tokens0, pages0, wave_sums);
   const int n = base + tid;
-  const Request r = request_of(p, n);
+  const Request r = n < p.N ? request_of(p, p.held[n], p.new_len[n]) : Request{};
   int64_t te = r.tokens, pe = r.need;
   scan_pair(te, pe, wave_sums);
   const bool served = r.live && pages0 + pe <= count && tokens0 + te <= p.T;
@@ -165,10 +181,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   if (!last_to_arrive(p.pool + 1, &flag)) return;
   int64_t taken = 0, none = 0;
   if (gridDim.x * gridDim.y > 1) {
-    for (int m = tid; m < p.N; m += kThreads) {
-      const int32_t a = load_agent(p.cache_len + m), b = load_agent(p.kv_len + m);
-      if (a >= 0) taken += pages_of(b, p.page) - pages_of(a, p.page);
-    }
+    for_each_pair(p.N, [&](int m, int32_t& a, int32_t& b) { a = load_agent(p.cache_len + m); b = load_agent(p.kv_len + m); },
+                  [&](int32_t a, int32_t b) { taken += a >= 0 ? pages_of(b, p.page) - pages_of(a, p.page) : 0; });
   } else {
     taken = served ? r.need : 0;
   }
@@ -176,13 +190,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
   if (tid == 0) p.pool[0] = (int32_t)(count - taken);
 }
 
-__device__ __forceinline__ int64_t given_back(const ReleasePagesLaunch& p, int n, int64_t& lo) {
-  lo = 0;
-  if (n >= p.N) return 0;
-  const int64_t keep = p.keep[n], held = p.held[n];
-  if (keep < 0 || held <= keep) return 0;
-  lo = pages_of(keep, p.page);
-  const int64_t hi = min(pages_of(held, p.page), (int64_t)p.table_width);
+__device__ __forceinline__ int32_t given_back(const ReleasePagesLaunch& p, int32_t keep, int32_t held, int32_t& lo) {
+  const bool some = keep >= 0 && held > keep;
+  lo = pages_of(some ? keep : 0, p.page);
+  const int32_t hi = some ? min(pages_of(held, p.page), p.table_width) : 0;
   return hi > lo ? hi - lo : 0;
 }
 
@@ -193,13 +204,15 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p)
   const int tid = threadIdx.x, base = blockIdx.x * kThreads, part = blockIdx.y, parts = gridDim.y;
   const int64_t count = min(max((int64_t)p.pool[0], (int64_t)0), p.capacity);
   int32_t* stack = p.pool + 2;
-  int64_t before = 0, none = 0, lo;
-  for (int n = tid; n < base; n += kThreads) before += given_back(p, n, lo);
+  int64_t before = 0, none = 0;
+  int32_t lo = 0;
+  const auto load = [&](int m, int32_t& a, int32_t& b) { a = p.keep[m]; b = p.held[m]; };
+  for_each_pair(min(base, p.N), load, [&](int32_t a, int32_t b) { int32_t at; before += given_back(p, a, b, at); });
   sum_pair(before, none, wave_sums);
-  int64_t pe = given_back(p, base + tid, lo);
+  int64_t pe = base + tid < p.N ? given_back(p, p.keep[base + tid], p.held[base + tid], lo) : 0;
   scan_pair(pe, none, wave_sums);
   page_end[tid] = narrow(pe);
-  lo_of[tid] = (int32_t)lo;
+  lo_of[tid] = lo;
   __syncthreads();
   // (as far as the stack's capacity goes)
   const int64_t pages = min((int64_t)page_end[kThreads - 1], p.capacity - count - before);
@@ -209,16 +222,17 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p)
   }
   if (!last_to_arrive(p.pool + 1, &flag)) return;
   int64_t total = 0;
-  for (int m = tid; m < p.N; m += kThreads) total += given_back(p, m, lo);
+  for_each_pair(p.N, load, [&](int32_t a, int32_t b) { int32_t at; total += given_back(p, a, b, at); });
   none = 0;
   sum_pair(total, none, wave_sums);
   if (tid == 0) p.pool[0] = (int32_t)min(count + total, p.capacity);
 }
 
 int parts_of(int64_t items, int64_t slices) {
-  // 1024 tokens or pages a workgroup, on average over the slices
-  const int64_t want = (items / slices + 1023) / 1024;
-  return (int)(want < 1 ? 1 : want > 256 ? 256 : want);
+  // 1024 tokens or pages a workgroup, on average over the slices; no more than 256 workgroups or so,
+  // each of which adds up the requests in front of it
+  const int64_t want = (items / slices + 1023) / 1024, most = (255 + slices) / slices;
+  return (int)(want > most ? most : want < 1 ? 1 : want);
 }
 
 }  // namespace
