@@ -17,6 +17,13 @@ constexpr float kMinScale = 5.421010862427522e-20f;   // 2^-64
 __device__ __forceinline__ bool not_finite(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
 __device__ __forceinline__ float finite_abs(float v) { return not_finite(v) ? 0.0f : fabsf(v); }
 __device__ __forceinline__ float nan_unless_finite(float v) { return not_finite(v) ? __uint_as_float(0x7fc00000u) : v; }
+// v / scale, rounded once, with inv = 1 / scale: the product and what it leaves of v (exact in a
+// fused one).  The product alone put about one code in a million on the other side of a border;
+// two instructions a value, hidden behind memory but for the gated norm (139 -> 142 us at 32768 x 32 x 128).
+__device__ __forceinline__ float quotient(float v, float scale, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, scale, v), inv, q);
+}
 
 // Maximum over aligned groups of `lanes` lanes (a power of two <= 64), in each of them.
 __device__ __forceinline__ float lanes_max(float v, int lanes) {
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(RW > 4 ? RW * kWave : 256) row_kernel(NormLaun
     if (p.groups == 1 ? from == 0 : (from & (p.group - 1)) == 0) p.scale[t * p.groups + (p.groups == 1 ? 0 : from >> shift)] = scale;
     float c[8];
 #pragma unroll
-    for (int v = 0; v < 8; ++v) c[v] = u[j][v] * inv;
+    for (int v = 0; v < 8; ++v) c[v] = quotient(u[j][v], scale, inv);
     store_codes<kWhole>(static_cast<uint8_t*>(p.out), t * p.out_stride + at[j], lo[j], c);
   }
 }
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(256) lds_kernel(NormLaunch p) {
     if (lane == 0) p.scale[t * p.groups + k] = scale;
     for (int e = lo + lane; e < hi; e += kWave) {
       const float u = kStage ? 0.0f : value(e);
-      const float c = nan_unless_finite(kStage ? kept[e] : result(e, u)) * inv;
+      const float c = quotient(nan_unless_finite(kStage ? kept[e] : result(e, u)), scale, inv);
       static_cast<uint8_t*>(p.out)[orow + e] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.0f, 0, false);
       if (!kStage && p.residual) put_residual(e, u);
     }

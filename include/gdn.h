@@ -681,8 +681,8 @@ int gdn_selective_update(const gdn_selective_args* args, void* stream);
  * rounding.  weight [d] is shared by the H parts (NULL: y
  * without it and offset).  out: bf16 or fp32, or e4m3 codes with y = code * scale:
  * scale[t, k] belongs to the k-th `group` values of the token's H d (the last group may be
- * shorter; group 0: the whole row) and is max |y| / 448, at least 2^-64; a code is y / scale
- * rounded to nearest even.  Values that are not finite do not count for the scale, and are
+ * shorter; group 0: the whole row) and is max |y| / 448, at least 2^-64; a code is the fp32
+ * quotient y / scale rounded to nearest even.  Values that are not finite do not count for the scale, and are
  * stored as NaN.
  *   x, gate : in_dtype [T, H, d]; residual : bf16 or fp32 [T, H, d]; out [T, H, d]; a row's
  *   H d values contiguous, token strides of at least H d; aligned to their element
