@@ -426,7 +426,22 @@ void launch_row_sizes(const NormLaunch& p, int64_t W, int part_lanes, hipStream_
   else launch_rows<kWhole, 4, 16, kAny>(p, part_lanes, stream);
 }
 
+// Parts of d values that are no 8 times a power of two up to 64.
+bool any_parts(const NormLaunch& p) {
+  const int lanes = p.d / 8;
+  return p.H > 1 && !(p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
+}
+bool in_registers(const NormLaunch& p) {
+  const int64_t W = (int64_t)p.H * p.d;
+  return W >= 8 && W <= 32768 && (!any_parts(p) || p.d >= 8);
+}
+
 }  // namespace
+
+int64_t most_rms_norm_rows(const NormLaunch& p) {
+  const int64_t W = (int64_t)p.H * p.d, threads = in_registers(p) && W > 8192 ? 16 * kWave : 256;   // (of a workgroup)
+  return (((int64_t)1 << 32) - 1) / threads;
+}
 
 hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream) {
   const int64_t W = (int64_t)p.H * p.d, in = p.in_bf16 ? 2 : 4, res = p.residual_bf16 ? 2 : 4;
@@ -435,9 +450,8 @@ hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream) {
                      (!p.residual || wide(p.residual, p.residual_stride, res)) && wide(p.out, p.out_stride, out) &&
                      reinterpret_cast<uintptr_t>(p.weight) % 16 == 0;
   const int lanes = p.d / 8;
-  const bool any = p.H > 1 && !(p.d % 8 == 0 && lanes <= 64 && (lanes & (lanes - 1)) == 0);
-  if (W >= 8 && W <= 32768 && (!any || p.d >= 8)) {
-    if (any) launch_row_sizes<false, true>(p, W, lanes, stream);
+  if (in_registers(p)) {
+    if (any_parts(p)) launch_row_sizes<false, true>(p, W, lanes, stream);
     else if (whole) launch_row_sizes<true, false>(p, W, lanes, stream);
     else launch_row_sizes<false, false>(p, W, lanes, stream);
   } else if ((W + p.H) * 4 <= 65536) {

@@ -128,6 +128,9 @@ int plan_norm(const gdn_rms_norm_args* a, gdn::NormLaunch& p) {
       !rows_ok(a->out, a->T, a->out_stride, w, out) || (a->weight && !aligned(a->weight, size_of(a->weight_dtype))) ||
       (e4m3 && !aligned(a->scale, 4)))
     return GDN_E_SHAPE;
+  p.H = a->H;
+  p.d = a->d;
+  if (a->T > gdn::most_rms_norm_rows(p)) return GDN_E_UNSUPPORTED;
   p.group = a->group ? a->group : (int)w;
   p.groups = (int)((w + p.group - 1) / p.group);
   const Range written[3] = {rows(a->out, a->T, a->out_stride, w, out), rows(a->residual, a->T, a->residual_stride, w, res),
@@ -138,10 +141,7 @@ int plan_norm(const gdn_rms_norm_args* a, gdn::NormLaunch& p) {
     for (int j = 0; j < 3; ++j)
       if (meet(written[i], read[j]) || (j < i && meet(written[i], written[j]))) return GDN_E_SHAPE;
   }
-  if (a->T > kMaxGrid) return GDN_E_UNSUPPORTED;
   p.T = a->T;
-  p.H = a->H;
-  p.d = a->d;
   p.in_bf16 = a->in_dtype == GDN_BF16;
   p.weight_bf16 = a->weight_dtype == GDN_BF16;
   p.residual_bf16 = a->residual_dtype == GDN_BF16;

@@ -97,6 +97,9 @@ struct ReleasePagesLaunch {
   int table_width;
 };
 
+// Most rows of a norm of this width (H, d): a launch has fewer than 2^32 threads.
+int64_t most_rms_norm_rows(const NormLaunch& p);
+
 hipError_t launch_selective_scan(const SelectiveLaunch& p, hipStream_t stream);
 hipError_t launch_selective_update(const SelectiveLaunch& p, hipStream_t stream);
 hipError_t launch_rms_norm(const NormLaunch& p, hipStream_t stream);

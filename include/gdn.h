@@ -688,8 +688,9 @@ int gdn_selective_update(const gdn_selective_args* args, void* stream);
  *   H d values contiguous, token strides of at least H d; aligned to their element
  *   scale : fp32 [T, ceil(H d / group)], contiguous (e4m3 only, else ignored)
  * Supported: bf16 or fp32 x, weight and residual; group 0, 64 or 128 (else
- * GDN_E_UNSUPPORTED); H at most 8192, H d at most 2^20; T below 2^24 and not
- * both a gate and a residual (else GDN_E_UNSUPPORTED).
+ * GDN_E_UNSUPPORTED); H at most 8192, H d at most 2^20; T below 2^24 (2^22 where H d is
+ * 8193 to 32768 and d at least 8, or H 1: a launch has fewer than 2^32 threads) and not both a
+ * gate and a residual (else GDN_E_UNSUPPORTED).
  * out, scale and residual must not overlap each other or an input (address ranges, else
  * GDN_E_SHAPE).  One launch. */
 typedef struct gdn_rms_norm_args {
