@@ -616,9 +616,11 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
         # without a speculative buffer the verify pass would write the state after the
         # rejected draft tokens into the pool (and read a token tree as a chain)
         raise ValueError("target verify needs forward_batch.spec_states and spec_state_slots")
-    norm_weight = getattr(layer, "norm_weight", None)
-    if z is not None and (norm_weight is None or z.shape != (T, H_v * d_v)):
-        raise ValueError(f"z [{T}, {H_v * d_v}] goes with layer.norm_weight")
+    if z is not None:    # (in front of the calls that change state, what the norm behind them would refuse)
+        norm_weight, norm_eps = getattr(layer, "norm_weight", None), float(getattr(layer, "norm_eps", 1e-6))
+        if norm_weight is None or z.shape != (T, H_v * d_v):
+            raise ValueError(f"z [{T}, {H_v * d_v}] goes with layer.norm_weight")
+        check_gated_norm(mixed_qkv, H_v, d_v, z, norm_weight, norm_eps)
     conv_w = getattr(layer, "conv_weight", None)
     if conv_w is not None:
         if conv_w.dim() == 3:
@@ -651,7 +653,7 @@ def forward_gdn(layer, forward_batch, mixed_qkv: torch.Tensor, a: torch.Tensor, 
                    spec_parent=getattr(forward_batch, "spec_parents", None) if verify else None,
                    keep_pool=verify)
     if z is not None:
-        o = rms_norm(o, norm_weight, eps=float(getattr(layer, "norm_eps", 1e-6)), gate=z.view(T, H_v, d_v))
+        o = rms_norm(o, norm_weight, eps=norm_eps, gate=z.view(T, H_v, d_v))
     return o.view(T, H_v * d_v)
 
 
@@ -726,5 +728,5 @@ def ssd_combined_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=F
 
 from .attention import (KVCache, attn_decode, attn_decode_workspace_size, attn_extend,  # noqa: E402
                         attn_extend_workspace_size, forward_attn, kv_cache, kv_evict, kv_evict_workspace_size, kv_store)
-from .step import (PagePool, StepPlan, page_pool, plan_pages, release_pages, rms_norm,  # noqa: E402
+from .step import (PagePool, StepPlan, check_gated_norm, page_pool, plan_pages, release_pages, rms_norm,  # noqa: E402
                    selective_scan, selective_scan_workspace_size, selective_update)

@@ -23,6 +23,7 @@ from .attention import _at, _attach, _need, _place, _run, _table, _vec
 _BF16, _F32, _I32, _I64, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
 _CODES = {_BF16: GDN_BF16, _F32: GDN_F32}
 _MOST = 2 ** 31 - 1          # (ctypes cuts larger numbers silently)
+_MOST_F32 = torch.finfo(_F32).max
 _OUT_CODES = {_BF16: GDN_BF16, _F32: GDN_F32, _F8: GDN_E4M3}
 
 
@@ -212,6 +213,20 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, offset: float = 0.0, residual
         _token_rows(out, "out", x.shape), _at(scale), eps, offset, 1 if gate_first else 0, group)
     _run("gdn_rms_norm", lib.gdn_rms_norm, args, i)
     return (out, scale) if f8 else out
+
+
+def check_gated_norm(like, H: int, d: int, gate, weight, eps: float) -> None:
+    """Refuses what rms_norm would refuse of a gate [T, H d] and a weight [d] for an output [T, H, d]
+    of the type and on the device of `like`."""
+    width = H * d
+    if _token_rows(gate, "z", (like.shape[0], width), like.dtype) < width:
+        raise ValueError(f"z must have rows of {width} values apart from each other (strides {gate.stride()})")
+    _code(weight, "norm_weight")
+    if weight.shape != (d,) or not weight.is_contiguous():
+        raise ValueError(f"norm_weight must be a contiguous [{d}] vector, got {tuple(weight.shape)}")
+    if not 0.0 <= eps <= _MOST_F32:
+        raise ValueError(f"norm_eps must be finite and at least 0, got {eps}")
+    _place(like, gate, weight)
 
 
 # ------------------------------------------------------------------ pages

@@ -1,8 +1,10 @@
 """Host-side tests of the step operators at the limits of their arguments (no GPU: no call here
 passes validation)."""
 import ctypes as ct
+from unittest import mock
 
 import pytest
+import torch
 
 import hybrid_model_linear_amd as gdn
 from hybrid_model_linear_amd import _lib
@@ -23,3 +25,37 @@ def test_rms_norm_launches_have_fewer_than_2_32_threads(H, d, most):
     assert lib.gdn_rms_norm(ct.byref(_lib.RmsNormArgs(T=most + 1, **args)), None) == UNSUP
     # one row less: as far as the output that meets the input
     assert lib.gdn_rms_norm(ct.byref(_lib.RmsNormArgs(T=most, **{**args, "out": P[0]})), None) == SHAPE
+
+
+# ------------------------------------------------------------------ forward_gdn's gated norm
+def _gdn_call(z, mode, **layer):
+    from types import SimpleNamespace
+    layer = dict(dict(num_k_heads=2, num_v_heads=4, head_k_dim=128, head_v_dim=128, A_log=object(), dt_bias=object(), layer_id=3,
+                      conv_weight=torch.zeros(1024, 4), norm_weight=torch.zeros(128)), **layer)
+    fb = SimpleNamespace(forward_mode=mode, state_pool={3: object()}, conv_pool={3: object()}, state_slots=object(),
+                         cu_seqlens=object())
+    mixed, ab = torch.zeros(5, 1024, dtype=torch.bfloat16), torch.zeros(5, 4)
+    with mock.patch.object(gdn, "conv1d", return_value=mixed) as mc, mock.patch.object(gdn, "conv1d_update", return_value=mixed) as mu, \
+            mock.patch.object(gdn, "gdn_gate_inputs", return_value=SimpleNamespace(dtype=mixed.dtype)), \
+            mock.patch.object(gdn, "extend", return_value=torch.zeros(5, 4, 128)) as me, \
+            mock.patch.object(gdn, "decode", return_value=torch.zeros(5, 4, 128)) as md:
+        with pytest.raises(ValueError) as e:
+            gdn.forward_gdn(SimpleNamespace(**layer), fb, mixed, ab, ab, z)
+    for m in (mc, mu, me, md):
+        m.assert_not_called()
+    return str(e.value)
+
+
+@pytest.mark.parametrize("mode", ["extend", "decode"])
+def test_forward_gdn_refuses_its_gated_norm_before_any_state_moves(mode):
+    """The conv and the layer change their pools in place: whatever the norm behind them would
+    refuse is refused in front of them."""
+    z = torch.zeros(5, 512, dtype=torch.bfloat16)
+    for bad, kw in ((z.float(), {}), (z[:, :256], {}), (z[:4], {}), (z[0], {}), (z.view(5, 4, 128), {}),
+                    (torch.zeros(512, 5, dtype=torch.bfloat16).T, {}), (torch.zeros(5, 1024, dtype=torch.bfloat16)[:, ::2], {}),
+                    (z[:1].expand(5, 512), {}), (z, dict(norm_weight=None)), (z, dict(norm_weight=torch.zeros(64))),
+                    (z, dict(norm_weight=torch.zeros(4, 128))), (z, dict(norm_weight=torch.zeros(256)[::2])),
+                    (z, dict(norm_weight=torch.zeros(128, dtype=torch.float16))), (z, dict(norm_eps=-1e-6)),
+                    (z, dict(norm_eps=float("nan"))), (z, dict(norm_eps=float("inf"))), (z, dict(norm_eps=1e39))):
+        assert "GPU" not in _gdn_call(bad, mode, **kw)
+    assert "GPU" in _gdn_call(z, mode)          # (all else in order: a gate in host memory)
