@@ -6,7 +6,8 @@
 // slice for itself (they are few, and in the caches), scans its own, and finds the request
 // of a token or page by bisection of the scan in LDS: one launch, and no workgroup waits
 // for another.  The number of free pages, which all of them read first, is written by the
-// last one to finish.
+// last one to finish.  (A release whose table has entries without a page is walked once more by
+// that one alone.)
 #include "step_launch.h"
 
 namespace gdn {
@@ -55,19 +56,21 @@ __device__ __forceinline__ int find(const int32_t* ends, int32_t v) {
 }
 
 // True in every thread of the last workgroup of the launch to come here; `arrivals` is 0
-// before and after the launch.
-__device__ __forceinline__ bool last_to_arrive(int32_t* arrivals, int* flag) {
+// before and after the launch.  `mark` (0 or 1, uniform) becomes the number of workgroups that
+// came with 1: they are counted in the upper half, there being 511 workgroups at most.
+__device__ __forceinline__ bool last_to_arrive(int32_t* arrivals, int* flag, int& mark) {
   const int total = gridDim.x * gridDim.y;
   if (total == 1) return true;
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int before = __hip_atomic_fetch_add(arrivals, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = before == total - 1;
+    const int before = __hip_atomic_fetch_add(arrivals, 1 + (mark << 16), __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = (before & 0xffff) == total - 1 ? 1 + (before >> 16) + mark : 0;
     if (*flag) __hip_atomic_store(arrivals, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   const bool last = *flag != 0;
+  mark = *flag - 1;
   if (last) __threadfence();
   return last;
 }
@@ -178,7 +181,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanPagesLaunch p) {
     if (p.positions) p.positions[t] = position;
     if (p.seq) p.seq[t] = owner;
   }
-  if (!last_to_arrive(p.pool + 1, &flag)) return;
+  int mark = 0;
+  if (!last_to_arrive(p.pool + 1, &flag, mark)) return;
   int64_t taken = 0, none = 0;
   if (gridDim.x * gridDim.y > 1) {
     for_each_pair(p.N, [&](int m, int32_t& a, int32_t& b) { a = load_agent(p.cache_len + m); b = load_agent(p.kv_len + m); },
@@ -216,15 +220,59 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleasePagesLaunch p)
   __syncthreads();
   // (as far as the stack's capacity goes)
   const int64_t pages = min((int64_t)page_end[kThreads - 1], p.capacity - count - before);
+  auto entry = [&](int first, int32_t i) {            // the i-th of the slice whose requests begin at `first`
+    const int k = find(page_end, i);
+    return p.table[(int64_t)(first + k) * p.table_stride + lo_of[k] + i - (k ? page_end[k - 1] : 0)];
+  };
+  bool hole = false;
   for (int64_t i = (int64_t)part * kThreads + tid; i < pages; i += (int64_t)parts * kThreads) {
-    const int k = find(page_end, (int32_t)i);
-    stack[count + before + i] = p.table[(int64_t)(base + k) * p.table_stride + lo_of[k] + i - (k ? page_end[k - 1] : 0)];
+    const int32_t id = entry(base, (int32_t)i);
+    stack[count + before + i] = id;
+    hole |= id < 0;
   }
-  if (!last_to_arrive(p.pool + 1, &flag)) return;
+  int holes = __syncthreads_or(hole) != 0;
+  if (!last_to_arrive(p.pool + 1, &flag, holes)) return;
   int64_t total = 0;
-  for_each_pair(p.N, load, [&](int32_t a, int32_t b) { int32_t at; total += given_back(p, a, b, at); });
   none = 0;
-  sum_pair(total, none, wave_sums);
+  if (holes == 0) {
+    for_each_pair(p.N, load, [&](int32_t a, int32_t b) { int32_t at; total += given_back(p, a, b, at); });
+    sum_pair(total, none, wave_sums);
+  } else {
+    // Entries without a page do not come to the stack: all of them in order once more, a thread
+    // eight at a time, each at the number of pages before it.  (Rare, and not worth a count of
+    // every other release's pages ahead of its writes.)
+    constexpr int kEach = 8;
+    for (int first = 0; first < p.N; first += kThreads) {
+      const int n = first + tid;
+      pe = n < p.N ? given_back(p, p.keep[n], p.held[n], lo) : 0;
+      scan_pair(pe, none, wave_sums);                  // (its barriers end the last slice's look-ups)
+      page_end[tid] = narrow(pe);
+      lo_of[tid] = lo;
+      __syncthreads();
+      const int64_t all = page_end[kThreads - 1];
+      for (int64_t i0 = 0; i0 < all && count + total < p.capacity; i0 += kThreads * kEach) {
+        int32_t id[kEach];
+        int64_t mine = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+          const int64_t i = i0 + tid * kEach + q;
+          id[q] = i < all ? entry(first, (int32_t)i) : -1;
+          mine += id[q] >= 0;
+        }
+        int64_t at = mine, chunk = mine;
+        scan_pair(at, none, wave_sums);
+        sum_pair(chunk, none, wave_sums);
+        at += count + total - mine;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+          if (id[q] < 0) continue;
+          if (at < p.capacity) stack[at] = id[q];
+          ++at;
+        }
+        total += chunk;
+      }
+    }
+  }
   if (tid == 0) p.pool[0] = (int32_t)min(count + total, p.capacity);
 }
 

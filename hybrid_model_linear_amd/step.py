@@ -307,7 +307,8 @@ def plan_pages(pool: PagePool, block_table, held, new, page: int, tokens: int, *
 def release_pages(pool: PagePool, block_table, keep, held, page: int) -> None:
     """Request n keeps its first keep[n] rows of held[n] (int32 [N]): the pages behind them go
     back to `pool`, requests and pages in order (keep[n] = 0: all of them; keep[n] < 0 or
-    held[n] <= keep[n]: none).  block_table is left as it is."""
+    held[n] <= keep[n]: none; negative entries of the table are passed over).  block_table is
+    left as it is."""
     lib = _lib.load()
     _page(page)
     N = held.shape[0]

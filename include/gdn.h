@@ -745,8 +745,8 @@ int gdn_rms_norm(const gdn_rms_norm_args* args, void* stream);
  *
  * gdn_release_pages: request n keeps its first keep[n] rows of held[n]: the pages
  * ceil(keep / page) .. ceil(held / page) - 1 of its table go back on the stack, requests and
- * pages in order, as far as `capacity` goes; keep[n] < 0 or held[n] <= keep[n]: none.  Table
- * entries are left as they are.
+ * pages in order, as far as `capacity` goes; keep[n] < 0 or held[n] <= keep[n]: none.  Negative
+ * entries are no pages and are passed over.  Table entries are left as they are.
  *
  * Every output must be apart from every input and output (address ranges, else
  * GDN_E_SHAPE), but for block_table and pool, which are both.  Calls on one pool are

@@ -131,7 +131,7 @@ def release_pages(stack, capacity, table, keep, held, page):
     for n in range(len(held)):
         if keep[n] >= 0 and held[n] > keep[n]:
             for p in range(math.ceil(keep[n] / page), min(math.ceil(held[n] / page), table.shape[1])):
-                if len(stack) < capacity:
+                if table[n, p] >= 0 and len(stack) < capacity:
                     stack.append(int(table[n, p]))
     return stack
 

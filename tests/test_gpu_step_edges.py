@@ -5,6 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import step as os_
+from test_gpu_step import i32
+
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
@@ -29,3 +32,43 @@ def test_codes_are_rounded_quotients(gdn_lib, T, H, d, group):
     off = int((codes.view(T, W).cpu().view(torch.uint8) != quotients.to(F8).view(torch.uint8)).sum())
     print(f"  {off} of {y.numel()} codes are another value", flush=True)
     assert off == 0
+
+
+# ------------------------------------------------------------------ pages
+@pytest.mark.parametrize("N,width,room", [(1, 3, 50), (5, 40, 1000), (3, 3000, 20000), (2, 9000, 4000), (256, 30, 9000),
+                                          (300, 20, 100000), (700, 9, 2500), (4, 70, 0), (40, 600, 1)])
+@pytest.mark.parametrize("holes", [0.0, 0.02, 0.6, 1.0])
+def test_release_passes_over_entries_without_a_page(gdn_lib, N, width, room, holes):
+    """A table may hold negative ids (rows whose page was given back before): they do not come to
+    the stack, and what is behind them does, in order, as far as the capacity goes."""
+    print("[case] release with holes", N, width, room, holes, flush=True)
+    rng = np.random.default_rng(N + width)
+    page, free = 16, 7
+    table = rng.permutation(N * width).reshape(N, width) + 100
+    table[rng.random((N, width)) < holes] = -1 - rng.integers(0, 2)
+    held = rng.integers(-1, width * page + 1, N)
+    held[-1] = width * page + 90                    # (more than the table has)
+    keep = np.where(rng.random(N) < 0.3, rng.integers(-1, width * page, N), 0)
+    state = torch.full((2 + free + room,), -7, dtype=torch.int32, device="cuda")
+    state[:2 + free] = i32([free, 0] + list(range(free)))
+    pool = gdn_lib.PagePool(state)
+    for turn in range(2):                           # (the second as after any other call)
+        before = state.clone()
+        gdn_lib.release_pages(pool, i32(table), i32(keep), i32(held), page)
+        want = os_.release_pages(before[2:2 + int(before[0])].tolist(), pool.capacity, table, keep, held, page)
+        s = state.tolist()
+        assert s[:2] == [len(want), 0] and s[2:2 + s[0]] == want, turn
+        state[0] = free
+
+
+def test_no_request_gets_a_page_that_is_none(gdn_lib):
+    """The pages of a request with holes go back, and the next step's requests take them: every token has a slot."""
+    print("[case] plan behind a release with holes", flush=True)
+    pool, table = gdn_lib.page_pool(0), i32([[-1, 4, -1, 9], [-1] * 4])
+    state = torch.zeros(2 + 10, dtype=torch.int32, device="cuda")
+    pool = gdn_lib.PagePool(state)
+    gdn_lib.release_pages(pool, table, i32([0, 0]), i32([64, 0]), 16)
+    assert state.tolist()[:4] == [2, 0, 4, 9]
+    plan = gdn_lib.plan_pages(pool, table, i32([0, 0]), i32([20, 5]), 16, 25)
+    assert plan.cache_len.tolist() == [0, -1] and (plan.slots[:20] >= 0).all() and (plan.slots[20:] == -1).all()
+    assert table[0].tolist() == [9, 4, -1, 9] and state[0] == 0

@@ -152,3 +152,10 @@ def test_plan_by_hand():
     # back: the pages behind the kept rows, in order, as far as the stack's capacity goes
     assert os_.release_pages([1], 9, t, [0, -1, 4, 5, 2], [5, 9, 5, 5, 1], 4) == [1, 7, 3, 2]
     assert os_.release_pages([1], 3, t, [0, -1, 4, 5, 2], [5, 9, 5, 5, 1], 4) == [1, 7, 3]
+
+
+def test_release_passes_over_holes():
+    table = np.array([[5, -1, 6], [-1, -2, 7]])
+    assert os_.release_pages([1], 9, table, [0, 0], [12, 12], 4) == [1, 5, 6, 7]
+    assert os_.release_pages([1], 3, table, [0, 0], [12, 12], 4) == [1, 5, 6]
+    assert os_.release_pages([], 3, table, [1, 0], [8, 5], 4) == []
