@@ -134,7 +134,8 @@ def selective_scan_workspace_size(x, dt, A, B, C, cu_seqlens, slot, pool, *, D=N
     lib = _lib.load()
     args, i = _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_softplus, has_init, None,
                               x.dtype if out_dtype is None else out_dtype, max_seqlen, keep_pool)
-    args.out = max(args.x, args.dt, args.B, args.C, args.z or 0, args.pool) + (1 << 50)   # (apart from the inputs)
+    # (apart from the inputs, and aligned whatever they are)
+    args.out = (max(args.x or 0, args.dt or 0, args.B or 0, args.C or 0, args.z or 0, args.pool or 0) + (1 << 50)) & -256
     return _need("gdn_selective_scan_workspace_size", lib.gdn_selective_scan_workspace_size, args, i)
 
 

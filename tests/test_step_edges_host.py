@@ -59,3 +59,29 @@ def test_forward_gdn_refuses_its_gated_norm_before_any_state_moves(mode):
                     (z, dict(norm_eps=float("nan"))), (z, dict(norm_eps=float("inf"))), (z, dict(norm_eps=1e39))):
         assert "GPU" not in _gdn_call(bad, mode, **kw)
     assert "GPU" in _gdn_call(z, mode)          # (all else in order: a gate in host memory)
+
+
+# ------------------------------------------------------------------ selective_scan's workspace
+@pytest.mark.parametrize("lead", [0, 1, 3])
+@pytest.mark.parametrize("out_dtype", [None, torch.float32])
+def test_the_workspace_query_takes_what_the_call_takes(lead, out_dtype):
+    """Operands at any element: the query's stand-in for the output is aligned whatever they are."""
+    from hybrid_model_linear_amd import step
+    T, D, S = 3000, 37, 16
+    bf = torch.bfloat16
+    A, pool = torch.zeros(D, S), torch.zeros(2, D, S)
+    cu, slot = torch.tensor([0, T], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    flat = torch.zeros(T * 200, dtype=bf)          # x, dt, B, C and z in one buffer, z highest
+    at = lambda k, w: flat[40 * T * k + lead:].as_strided((T, w), (w, 1))  # noqa: E731
+    with mock.patch.object(step, "_place", return_value=0), mock.patch.object(step, "_need", lambda name, fn, args, i: fn(ct.byref(args))):
+        need = gdn.selective_scan_workspace_size(at(0, D), at(1, D), A, at(2, S), at(3, S), cu, slot, pool, z=at(4, D),
+                                                 out_dtype=out_dtype)
+    assert need > 0
+
+
+def test_the_workspace_query_without_tokens():
+    from hybrid_model_linear_amd import step
+    e = torch.zeros((0, 8), dtype=torch.bfloat16)
+    cu, slot = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with mock.patch.object(step, "_place", return_value=0), mock.patch.object(step, "_need", lambda name, fn, args, i: fn(ct.byref(args))):
+        assert gdn.selective_scan_workspace_size(e, e, torch.zeros(8, 8), e, e, cu, slot, torch.zeros(1, 8, 8)) == 0
