@@ -196,9 +196,10 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
         to[bc_to[k]] = kAll || bc_token[k] < left ? Elem<In>::load(&r.bc[k], 0) : 0.0f;
   };
   float sum = 0.0f;                                          // of delta (kStates)
-  // The tile's tokens in turn, LDS reads a step of kStep tokens ahead of their use.
+  // The tile's tokens in turn, LDS reads a step of kStep tokens ahead of their use.  Those that are
+  // not there are not walked: their delta of 0 would leave a state as it is, but not under an A of -inf.
   constexpr int kStep = SPL <= 4 ? 2 : 1;
-  auto walk = [&](int buf) __attribute__((always_inline)) {
+  auto walk = [&](int buf, auto whole, int left) __attribute__((always_inline)) {
     float2 d[2][kStep];
     float b[2][kStep][SPL], cc[2][kStep][SPL];
     auto read = [&](int s) __attribute__((always_inline)) {
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
+        if (!decltype(whole)::value && s * kStep + j >= left) continue;
         const float2 dd = d[s & 1][j];
         float y = 0.0f;
 #pragma unroll
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
     // last one again where there is none).
     auto turn = [&](auto parity, int k) __attribute__((always_inline)) {
       constexpr int kBuf = decltype(parity)::value;
-      walk(kBuf);
+      walk(kBuf, Par<1>{}, TT);
       stage(1 - kBuf, set[1 - kBuf], Par<1>{}, TT);
       lds_sync();
       finish(kBuf, set[kBuf], Par<1>{}, TT);
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kWaves<NS>* kWave, 2) scan_kernel(SelectiveLau
     lds_sync();                     // (the last turns' buffers have been read)
     stage(0, r, Par<0>{}, tail);
     lds_sync();
-    walk(0);
+    walk(0, Par<0>{}, tail);
     lds_sync();
     finish(0, r, Par<0>{}, tail);
   }

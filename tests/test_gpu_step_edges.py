@@ -6,10 +6,31 @@ import pytest
 import torch
 
 from oracle import step as os_
-from test_gpu_step import i32
+from test_gpu_step import call_scan, i32, scan_case
 
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+# ------------------------------------------------------------------ selective scan
+@pytest.mark.parametrize("S,dtype", [(8, BF), (16, F32), (32, BF), (64, F32), (128, BF)])
+@pytest.mark.parametrize("cut", [False, True])
+def test_a_factor_that_is_minus_infinity_forgets(gdn_lib, S, dtype, cut):
+    """exp(delta A) is 0 for A = -inf as for any large one: the same bits as with -1e30, in whole and
+    partial tiles (whose missing tokens have no delta), cut and uncut, and token by token."""
+    print("[case] A = -inf", S, dtype, cut, flush=True)
+    rng = np.random.default_rng(S)
+    lens = [1, 7, 16, 29, 700, 33, 0] if cut else [1, 7, 16, 29, 48, 33, 0]
+    c, g = scan_case(rng, lens, 70, S, 1, dtype)
+    some = torch.from_numpy(rng.random((70, S)) < 0.3).cuda()
+    got = []
+    for far in (float("-inf"), -1e30):
+        h = {**g, "A": torch.where(some, far, g["A"]), "pool": g["pool"].clone()}
+        out = call_scan(gdn_lib, h, max_seqlen=700 if cut else 48)
+        last = gdn_lib.selective_update(g["x"][:7], g["dt"][:7], h["A"], g["B"][:7], g["C"][:7], g["slot"], h["pool"], D=g["D"])
+        got.append((out, h["pool"], last))
+    for name, a, b in zip(("out", "pool", "update"), *got):
+        assert b.isfinite().all() and torch.equal(a, b), name
 
 
 # ------------------------------------------------------------------ norm
