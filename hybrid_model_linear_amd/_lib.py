@@ -11,6 +11,7 @@ GDN_OK, GDN_E_NULL, GDN_E_SHAPE, GDN_E_DTYPE, GDN_E_UNSUPPORTED, GDN_E_INDEX, GD
 GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
 GDN_MODE_GDN, GDN_MODE_SSD = 0, 1
 ABI_VERSION = 11
+GDN_SELECTIVE_UNCUT = 112
 
 EXPORTED = ["gdn_gate", "gdn_extend", "gdn_decode", "gdn_extend_gated", "gdn_decode_gated",
             "gdn_conv1d", "gdn_conv1d_update", "gdn_validate_slots", "gdn_status_str",

@@ -459,14 +459,16 @@ void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus) {
   // 409 / 411, eight 569 / 758; one of 256 x 1024 31 / 20; 8192 and 31 of 500 x 4096 824 / 520; the
   // rule is within 10% of the best number of segments over 18 such shapes.
   // Segments: four workgroups (two of eight waves) a CU, no shorter than two tiles.
+  constexpr int kShortest = 32, kLaunch = 80;      // tokens of a segment, and the launch's worth
+  static_assert(kShortest + kLaunch == GDN_SELECTIVE_UNCUT, "the header's promise");
   p.segs = 1;
   p.seg_len = longest;
   const int eight = p.states > 32;
   const int64_t work = channel_blocks(p) * p.T;
   int64_t len = work / (eight ? 2 * cus : 4 * cus) / 16 * 16;
   if (len < longest / 128) len = longest / 128;
-  len = (len < 32 ? 32 : len + 15) / 16 * 16;
-  if (15 * work / (eight ? 7 * cus : 14 * cus) + len + 80 >= longest) return;
+  len = (len < kShortest ? kShortest : len + 15) / 16 * 16;
+  if (15 * work / (eight ? 7 * cus : 14 * cus) + len + kLaunch >= longest) return;
   p.seg_len = len;
   p.segs = (int)((longest + len - 1) / len);
 }

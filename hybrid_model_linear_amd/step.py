@@ -17,7 +17,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._lib import GDN_BF16, GDN_E4M3, GDN_F32
+from ._lib import GDN_BF16, GDN_E4M3, GDN_F32, GDN_SELECTIVE_UNCUT
 from .attention import _at, _attach, _need, _place, _run, _table, _vec
 
 _BF16, _F32, _I32, _I64, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
@@ -117,9 +117,9 @@ def selective_scan(x, dt, A, B, C, cu_seqlens, slot, pool, *, D=None, z=None, dt
         raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     args, i = _selective_args(x, dt, A, B, C, cu_seqlens, slot, pool, D, z, dt_bias, dt_softplus, has_init, out, None,
                               max_seqlen, keep_pool)
-    # (no sequence of fewer than 113 tokens is cut: no query, which short calls would feel)
+    # (calls that are too short to be cut feel the query)
     ws = None
-    if workspace is not None or args.T > 112:
+    if workspace is not None or args.T > GDN_SELECTIVE_UNCUT:
         ws = _attach("gdn_selective_scan", lib.gdn_selective_scan_workspace_size, args, i, workspace)
     _run("gdn_selective_scan", lib.gdn_selective_scan, args, i)
     del ws

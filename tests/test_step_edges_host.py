@@ -85,3 +85,22 @@ def test_the_workspace_query_without_tokens():
     cu, slot = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     with mock.patch.object(step, "_place", return_value=0), mock.patch.object(step, "_need", lambda name, fn, args, i: fn(ct.byref(args))):
         assert gdn.selective_scan_workspace_size(e, e, torch.zeros(8, 8), e, e, cu, slot, torch.zeros(1, 8, 8)) == 0
+
+
+def test_calls_that_skip_the_query_are_not_cut():
+    """The binding asks for no workspace where the header says that no sequence is cut; one token
+    more, and a sequence can be."""
+    import re
+    from test_step_host import HEADER
+    uncut = int(re.search(r"#define GDN_SELECTIVE_UNCUT (\d+)", open(HEADER).read()).group(1))
+    assert _lib.GDN_SELECTIVE_UNCUT == uncut
+    query = gdn.load().gdn_selective_scan_workspace_size
+
+    def need(T, N, D, S, hint):
+        return query(ct.byref(_lib.SelectiveArgs(
+            in_dtype=1, out_dtype=1, N=N, G=1, T=T, D=D, states=S, x=P[0], x_stride=D, dt=P[1], dt_stride=D, B=P[2], B_stride=S, C=P[3],
+            C_stride=S, A=P[4], cu_seqlens=P[5], slot=P[6], pool=P[7], num_slots=4, out=P[8], out_stride=D, max_seqlen=hint)))
+    for S in (8, 16, 32, 64, 128):
+        for D in (8, 100, 4096, 1 << 20):
+            assert all(need(T, N, D, S, h) == 0 for T in (1, 33, uncut) for N in (1, 3) for h in (0, T, 1 << 30)), (S, D)
+    assert need(uncut + 1, 1, 64, 16, 0) > 0
