@@ -30,9 +30,12 @@ bool meet(const Range& a, const Range& b) {
   return a.bytes > 0 && b.bytes > 0 && a.at < b.at + (uintptr_t)b.bytes && b.at < a.at + (uintptr_t)a.bytes;
 }
 
-// A row operand: there, aligned to its element, rows of at least `width`.  Extents stay in 62 bits.
+constexpr int64_t kMostBytes = (int64_t)1 << 61;   // of an operand: extents must not wrap
+
+// A row operand: aligned to its element, rows of at least `width`.
 bool rows_ok(const void* p, int64_t n, int64_t stride, int64_t width, int64_t size) {
-  return aligned(p, size) && stride >= width && stride <= (int64_t)1 << 40 && n <= INT32_MAX;
+  return aligned(p, size) && stride >= width && stride <= (int64_t)1 << 40 && n <= INT32_MAX &&
+         stride <= kMostBytes / ((n > 0 ? n : 1) * size);
 }
 
 // Descriptor of a scan or update; need receives the workspace bytes with which a scan's sequences are cut.
@@ -52,6 +55,7 @@ int plan_selective(const gdn_selective_args* a, bool update, gdn::SelectiveLaunc
       !rows_ok(a->B, a->T, a->B_stride, bc, in) || !rows_ok(a->C, a->T, a->C_stride, bc, in) ||
       (a->z && !rows_ok(a->z, a->T, a->z_stride, a->D, in)) || !rows_ok(a->out, a->T, a->out_stride, a->D, out))
     return GDN_E_SHAPE;
+  if (a->num_slots > kMostBytes / (a->D * a->states * 4)) return GDN_E_SHAPE;
   if (!aligned(a->A, 16) || !aligned(a->pool, 16) || !aligned(a->D_skip, 4) || !aligned(a->dt_bias, 4) || !aligned(a->slot, 4) ||
       (!update && (!aligned(a->cu_seqlens, 4) || !aligned(a->has_init, 4))))
     return GDN_E_SHAPE;

@@ -104,3 +104,19 @@ def test_calls_that_skip_the_query_are_not_cut():
         for D in (8, 100, 4096, 1 << 20):
             assert all(need(T, N, D, S, h) == 0 for T in (1, 33, uncut) for N in (1, 3) for h in (0, T, 1 << 30)), (S, D)
     assert need(uncut + 1, 1, 64, 16, 0) > 0
+
+
+# ------------------------------------------------------------------ extents
+def test_extents_past_62_bits_are_refused():
+    """A row operand whose last element lies past 2^62 bytes would wrap around the overlap checks."""
+    lib = gdn.load()
+    base = dict(in_dtype=1, out_dtype=1, N=0, G=1, T=1 << 30, D=64, states=16, x=P[0], x_stride=64, dt=P[1], dt_stride=64, B=P[2],
+                B_stride=16, C=P[3], C_stride=16, A=P[4], pool=P[5], num_slots=4, out=P[6], out_stride=64)
+    call = lambda **kw: lib.gdn_selective_scan(ct.byref(_lib.SelectiveArgs(**{**base, **kw})), None)  # noqa: E731
+    assert call() == _lib.GDN_OK
+    for kw in (dict(x_stride=1 << 40), dict(out_stride=1 << 40), dict(out_stride=1 << 40, out=P[0]), dict(B_stride=1 << 33),
+               dict(num_slots=1 << 52), dict(num_slots=1 << 62)):
+        assert call(**kw) == SHAPE, kw
+    norm = dict(in_dtype=1, out_dtype=1, T=(1 << 24) - 1, H=1, d=8, x=P[0], x_stride=8, out=P[1], out_stride=8, eps=1e-6)
+    for kw in (dict(x_stride=1 << 39), dict(out_stride=1 << 39), dict(residual=P[2], residual_stride=1 << 40)):
+        assert lib.gdn_rms_norm(ct.byref(_lib.RmsNormArgs(**{**norm, **kw})), None) == SHAPE, kw
