@@ -278,7 +278,8 @@ def plan_pages(pool: PagePool, block_table, held, new, page: int, tokens: int, *
     the pages it lacks from `pool`, requests in order, into its row of block_table (int32 [N,
     width], updated in place).  From the first request on for which the pages or the room for
     `tokens` tokens do not last, and where the table is too narrow, nothing is served: cache_len
-    and kv_len are -1, as for padding rows.
+    and kv_len are -1, as for padding rows.  cu_seqlens still counts the tokens of such requests
+    (up to `tokens`): layers that go by slots skip them with slot = torch.where(plan.cache_len < 0, -1, slot).
     Returns StepPlan: cu_seqlens int32 [N+1]; cache_len = held, kv_len = held + new int32 [N];
     slots int64 [tokens], positions, seq int32 [tokens] (-1 for tokens of no served request).
     start int32 [N]: the first tokens' positions (default held).  out: a StepPlan to be

@@ -735,7 +735,8 @@ int gdn_rms_norm(const gdn_rms_norm_args* args, void* stream);
  *   - the pages and the tokens up to its end fit into the stack and into T (so that from the
  *     first request that does not fit on none is served).
  * Outputs, all written whole:
- *   cu_seqlens [N + 1] : tokens before each request, served or not, at most T
+ *   cu_seqlens [N + 1] : tokens before each request, served or not, at most T (so that a layer's
+ *     slot of a request with a negative cache_len has to be negative too: its tokens may be cut)
  *   cache_len [N]      : held[n], or -1 where the request is not served
  *   kv_len [N]         : held[n] + new_len[n], or -1
  *   slots, positions, seq [T] : of a served request's i-th token, with row r = held + i:

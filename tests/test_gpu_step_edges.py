@@ -1,6 +1,8 @@
 """GPU tests of the step operators at their edges: codes next to a border, factors that are
 not finite, page tables with holes, requests that a plan does not serve, and every kernel that
 the dispatch can choose."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -93,3 +95,40 @@ def test_no_request_gets_a_page_that_is_none(gdn_lib):
     plan = gdn_lib.plan_pages(pool, table, i32([0, 0]), i32([20, 5]), 16, 25)
     assert plan.cache_len.tolist() == [0, -1] and (plan.slots[:20] >= 0).all() and (plan.slots[20:] == -1).all()
     assert table[0].tolist() == [9, 4, -1, 9] and state[0] == 0
+
+
+@pytest.mark.parametrize("tokens,free", [(47, 3), (30, 9)])
+def test_layers_skip_requests_that_the_plan_does_not_serve(gdn_lib, tokens, free):
+    """The stack or the room for tokens ends inside of the third request's need: with its slot masked by
+    cache_len the layers leave its states and its rows (which the plan still counts, cut at the
+    room) as they are, and serve the others as alone."""
+    print("[case] unserved requests", tokens, free, flush=True)
+    rng = np.random.default_rng(7)
+    lens, page = [20, 1, 17, 9], 16
+    c, g = scan_case(rng, lens, 40, 16, 1, BF)
+    pool, table = gdn_lib.page_pool(free), torch.full((4, 4), -1, dtype=torch.int32, device="cuda")
+    table[1, 0] = 100
+    held = i32([0, 15, 0, 0])
+    plan = gdn_lib.plan_pages(pool, table, held, i32(lens), page, tokens)
+    assert plan.cache_len.tolist() == [0, 15, -1, -1] and plan.cu_seqlens.tolist() == [0, 20, 21, min(38, tokens), min(47, tokens)]
+    slot = torch.where(plan.cache_len < 0, -1, g["slot"])
+    before, out = g["pool"].clone(), torch.full((tokens, 40), 7.0, dtype=BF, device="cuda")
+    g.update({k: g[k][:tokens] for k in ("x", "dt", "B", "C", "z")})
+    call_scan(gdn_lib, {**g, "cu": plan.cu_seqlens, "slot": slot}, out=out)
+    alone = before.clone()
+    want = call_scan(gdn_lib, {**g, "cu": i32([0, 20, 21]), "slot": g["slot"][:2].contiguous(), "pool": alone})
+    assert torch.equal(out[:21], want[:21]) and (out[21:] == 7).all() and torch.equal(g["pool"], alone)
+    assert torch.equal(alone[g["slot"][2:].long()], before[g["slot"][2:].long()])
+    # the linear-attention layer, by its batch's state_slots
+    layer = SimpleNamespace(num_k_heads=1, num_v_heads=2, head_k_dim=64, head_v_dim=64, layer_id=0, A_log=torch.zeros(2, device="cuda"),
+                            dt_bias=torch.zeros(2, device="cuda"), norm_weight=torch.ones(64, device="cuda"))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(BF)  # noqa: E731
+    mixed, a, b, z, states = rand(tokens, 256), rand(tokens, 2), rand(tokens, 2), rand(tokens, 128), rand(6, 2, 64, 64).float()
+    first = states.clone()
+    fb = SimpleNamespace(forward_mode="extend", state_slots=slot, cu_seqlens=plan.cu_seqlens, state_pool={0: states})
+    got = gdn_lib.forward_gdn(layer, fb, mixed, a, b, z)
+    ref = SimpleNamespace(forward_mode="extend", state_slots=g["slot"][:2].contiguous(), cu_seqlens=i32([0, 20, 21]), state_pool={0: first.clone()})
+    assert torch.equal(got[:21], gdn_lib.forward_gdn(layer, ref, mixed, a, b, z)[:21]) and torch.equal(states, ref.state_pool[0])
+    rest = [k for k in range(6) if k not in g["slot"][:2].tolist()]
+    assert torch.equal(states[rest], first[rest])
