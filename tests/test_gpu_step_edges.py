@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from oracle import step as os_
-from test_gpu_step import call_scan, i32, scan_case
+from test_gpu_step import call_scan, check_norm, check_scan, i32, norm_case, scan_case, up
 
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
@@ -132,3 +132,54 @@ def test_layers_skip_requests_that_the_plan_does_not_serve(gdn_lib, tokens, free
     assert torch.equal(got[:21], gdn_lib.forward_gdn(layer, ref, mixed, a, b, z)[:21]) and torch.equal(states, ref.state_pool[0])
     rest = [k for k in range(6) if k not in g["slot"][:2].tolist()]
     assert torch.equal(states[rest], first[rest])
+
+
+# ------------------------------------------------------------------ every kernel of the dispatch
+@pytest.mark.parametrize("n,D,S,G,dtype", [(517, 512, 16, 1, BF), (1030, 512, 8, 4, F32), (411, 258, 32, 2, BF), (65, 1024, 64, 1, F32),
+                                           (65, 512, 128, 1, BF), (129, 2048, 16, 1, F32)])
+@pytest.mark.parametrize("aligned", [False, True])
+def test_update_of_two_rows_a_workgroup(gdn_lib, n, D, S, G, dtype, aligned):
+    """From 4096 workgroups of one row on, two share one: odd numbers of rows, padding rows as the first, the
+    second and both of a pair and as the last, B and C in wide loads and at odd elements."""
+    print("[case] update by pairs", n, D, S, G, dtype, aligned, flush=True)
+    per = 1024 // S
+    assert -(-(D // G) // per) * G * n >= 4096
+    rng = np.random.default_rng(n + D)
+    c, g = scan_case(rng, [1] * n, D, S, G, dtype, skip=(4, 11, 20, 21, n - 1))
+    if aligned:
+        g["B"], g["C"] = g["B"].contiguous(), g["C"].contiguous()
+    out = torch.full((n, D), 7.0, dtype=dtype, device="cuda")
+    gdn_lib.selective_update(g["x"], g["dt"], g["A"], g["B"], g["C"], g["slot"], g["pool"], D=g["D"], z=g["z"], dt_bias=g["dt_bias"], out=out)
+    check_scan(c, out, g["pool"], dtype, "update by pairs", untouched=7.0)
+
+
+@pytest.mark.parametrize("n,D,S", [(1, 300, 16), (5, 64, 64)])
+def test_update_with_aligned_operands(gdn_lib, n, D, S):
+    print("[case] update aligned", n, D, S, flush=True)
+    c, g = scan_case(np.random.default_rng(n), [1] * n, D, S, 1, BF)
+    out = gdn_lib.selective_update(g["x"], g["dt"], g["A"], g["B"].contiguous(), g["C"].contiguous(), g["slot"], g["pool"], D=g["D"],
+                                   z=g["z"], dt_bias=g["dt_bias"])
+    check_scan(c, out, g["pool"], BF, "update aligned")
+
+
+# rows of a wave (1024 rows and more, also where the last workgroup is not full), of four and of sixteen,
+# one to four pieces a thread; in aligned pieces, at any element, and in parts of any size
+NORMS = [(1030, 4, 128), (1027, 1, 500), (1027, 1, 1000), (1030, 8, 128), (1030, 1, 1003), (1027, 5, 100), (1029, 9, 100),
+         (3, 1, 1500), (3, 1, 2001), (3, 1, 3001), (3, 30, 100), (3, 1, 5600), (3, 1, 6001), (3, 50, 100), (2, 1, 7168), (3, 64, 128),
+         (3, 1, 7001), (3, 70, 100), (3, 1, 12000), (2, 128, 128), (3, 1, 12001), (3, 120, 100), (2, 1, 20001), (2, 200, 100),
+         (2, 1, 32768), (2, 1, 30001), (2, 300, 100), (5, 32, 80), (5, 40, 96), (3, 8, 192), (1026, 5, 96)]
+
+
+@pytest.mark.parametrize("T,H,d", NORMS)
+@pytest.mark.parametrize("out_dtype,group", [(BF, 0), (F8, 0), (F8, 128), (F8, 64), (F32, 0)])
+def test_norm_in_every_kernel(gdn_lib, T, H, d, out_dtype, group):
+    print("[case] norm", T, H, d, out_dtype, group, flush=True)
+    rng = np.random.default_rng(T + d)
+    for dtype, residual, gate, first, wdtype, offset in ((BF, BF, False, False, BF, 1.0), (BF, F32, False, False, F32, 0.0),
+                                                         (F32, None, True, False, None, 0.0), (BF, None, True, True, BF, 1.0)):
+        h = norm_case(rng, T, H, d, dtype, residual, gate, wdtype)
+        r = up(h["residual"], residual)
+        got = gdn_lib.rms_norm(up(h["x"], dtype), up(h["weight"], wdtype), eps=1e-5, offset=offset, residual=r,
+                               gate=up(h["gate"], dtype), gate_first=first, out_dtype=out_dtype, group=group)
+        check_norm(h, got, r, out_dtype, group, f"{dtype} {residual} {gate}", residual=residual, eps=1e-5, offset=offset,
+                   gate_first=first)
