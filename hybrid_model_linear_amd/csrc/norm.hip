@@ -19,7 +19,7 @@ __device__ __forceinline__ float finite_abs(float v) { return not_finite(v) ? 0.
 __device__ __forceinline__ float nan_unless_finite(float v) { return not_finite(v) ? __uint_as_float(0x7fc00000u) : v; }
 // v / scale, rounded once, with inv = 1 / scale: the product and what it leaves of v (exact in a
 // fused one).  The product alone put about one code in a million on the other side of a border;
-// two instructions a value, hidden behind memory but for the gated norm (139 -> 142 us at 32768 x 32 x 128).
+// two instructions a value, hidden behind memory but for the gated norm (134 -> 137 us at 32768 x 32 x 128).
 __device__ __forceinline__ float quotient(float v, float scale, float inv) {
   const float q = v * inv;
   return fmaf(fmaf(-q, scale, v), inv, q);

@@ -454,11 +454,14 @@ hipError_t launch_types(const SelectiveLaunch& p, bool update, hipStream_t strea
 void plan_selective_scan(SelectiveLaunch& p, int64_t longest, int cus) {
   // In tokens of one workgroup: uncut, the longest sequence walks alone while the others share
   // the chip, which is full at 1.4 workgroups of four waves per CU (0.7 of eight); cut, all
-  // tokens cost 1.5 times as much (the states are formed twice), plus one segment and a launch.
+  // tokens are counted 1.5 times, plus one segment and a launch.  (The states are formed twice, the
+  // first time without y, which is 1.83 times the recurrence's cycles; 1.5 is what fits the
+  // measurements, since a walk at 1.4 workgroups a CU does not fill its SIMDs.)
   // Measured, us, 16 states, uncut / cut: one of 4096 x 4096 channels 400 / 124, two 400 / 232, four
   // 409 / 411, eight 569 / 758; one of 256 x 1024 31 / 20; 8192 and 31 of 500 x 4096 824 / 520; the
   // rule is within 10% of the best number of segments over 18 such shapes.
-  // Segments: four workgroups (two of eight waves) a CU, no shorter than two tiles.
+  // Segments: four workgroups (two of eight waves) a CU, no shorter than two tiles.  (The LDS of
+  // the pass that forms y holds three a CU at 8, 16 and 64 states, 53 KB each, two at 32 and 128.)
   constexpr int kShortest = 32, kLaunch = 80;      // tokens of a segment, and the launch's worth
   static_assert(kShortest + kLaunch == GDN_SELECTIVE_UNCUT, "the header's promise");
   p.segs = 1;

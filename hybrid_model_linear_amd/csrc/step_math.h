@@ -19,7 +19,7 @@ __device__ __forceinline__ float step_softplus(float z) {
 }
 // z / (1 + exp(-z)).  The exponential's argument is rounded once, which is worth |z| 2^-23 of
 // the result at most (2^-19 at z = -20, where silu is 4e-8); past exp's range the result is -0.
-// Held to few instructions: the gated norm is bound by them (170 -> 141 us at 32768 x 32 x 128 when it came; 133 now).
+// Held to few instructions: the gated norm is bound by them (170 -> 141 us at 32768 x 32 x 128 when it came; 137 now).
 __device__ __forceinline__ float step_silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }

@@ -627,7 +627,8 @@ int64_t gdn_kv_evict_workspace_size(const gdn_kv_evict_args* args);
  * workgroups are cut into segments, whose states a first launch prepares in a workspace of
  * gdn_selective_scan_workspace_size bytes (0: no segments), 256-byte aligned, with any
  * contents (calls in flight at once need their own); without one (NULL) there are none.
- * A segment's start state is folded from those before it, which rounds differently.  No
+ * A segment's start state is folded from those before it, which rounds differently (and
+ * makes an infinite state NaN where the factors' product leaves fp32's range).  No
  * sequence of GDN_SELECTIVE_UNCUT tokens or fewer is cut (T up to it: no workspace).
  * gdn_selective_update: one token per row (T = N), row b continues pool[slot[b]], negative
  * slots as gdn_decode; cu_seqlens, has_init, max_seqlen, keep_pool, workspace ignored. */
